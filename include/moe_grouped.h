@@ -329,6 +329,131 @@ moe_status moe_unpermute_backward(const uint16_t* dy, const uint16_t* y_perm, co
                                   const float* routing_w, int64_t T, int32_t k, int64_t d, uint16_t* dy_perm,
                                   float* d_routing_w, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Router: from logits to expert_ids and routing_w, and back.
+ *
+ * For a row x of E logits: m = max x, p_i = exp(x_i - m) / sum exp(x - m),
+ * lse = m + log sum exp(x - m), all in fp32. The k chosen experts are those
+ * of the largest logits, in descending order, the lowest index first among
+ * equals. An expert whose logit is -inf is masked: it is never chosen, and
+ * slots left over when fewer than k experts remain get id -1 (a dropped slot
+ * to moe_permute) and weight 0. A row of -inf alone (padding) chooses nothing
+ * and has lse = -inf. The type's lowest finite value is a logit like any
+ * other. A row with a NaN or +inf has NaN weights and lse; a NaN is not chosen.
+ *
+ *   routing_w[t, j] = p_{id_j}                    (renormalize = 0)
+ *                   = p_{id_j} / sum_l p_{id_l}   (renormalize = 1)
+ *
+ *   logits  bf16 or fp32 [T, E] per dtype, aligned to its own element size
+ *   E       1 .. MOE_MAX_EXPERTS; k 1 .. min(E, MOE_ROUTER_MAX_TOPK)
+ * ------------------------------------------------------------------------- */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+#define MOE_ROUTER_MAX_TOPK 64
+
+/* The routed experts and their weights, one launch.
+ *
+ *   expert_ids  int32 [T, k]  out
+ *   routing_w   fp32  [T, k]  out
+ *   lse         fp32  [T]     out */
+moe_status moe_router_topk(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                           int32_t* expert_ids, float* routing_w, float* lse, hipStream_t stream);
+
+/* Bytes of device workspace moe_router_topk_losses needs; 0 for invalid shapes. */
+size_t moe_router_workspace_bytes(int64_t T, int32_t E);
+
+/* moe_router_topk with the training losses over the same read of the logits:
+ * n = the rows that are not all -inf, f_e = counts_e / sum counts,
+ * P_e = 1/n sum over those rows of p_e,
+ *
+ *   losses[0] = E sum_e f_e P_e   (balance loss: 1 when both are uniform)
+ *   losses[1] = 1/n sum lse^2     (z-loss)
+ *
+ *   counts     int32 [E]  out: slots that chose each expert
+ *   tokens     int32 [1]  out: n
+ *   prob_mean  fp32  [E]  out: P
+ *   losses     fp32  [2]  out (both 0 when n = 0)
+ *   workspace  device scratch of at least moe_router_workspace_bytes(T, E)
+ *
+ * Two launches; sums are taken in a fixed order, so results repeat bit for bit. */
+moe_status moe_router_topk_losses(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
+                                  int32_t renormalize, int32_t* expert_ids, float* routing_w, float* lse,
+                                  int32_t* counts, int32_t* tokens, float* prob_mean, float* losses, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of the logits, one launch: from d_routing_w [T, k] (fp32, as
+ * moe_unpermute_backward gives it; NULL: none) through the chosen weights, and
+ * from d_losses [2] (fp32, on the device; NULL: none) through the losses, with
+ * f constant (counts have no gradient).
+ *
+ *   expert_ids, routing_w  as the forward gave them; ids outside [0, E) carry
+ *                          no gradient, whatever d_routing_w holds there
+ *   counts, tokens         as moe_router_topk_losses gave them, or summed over
+ *                          several ranks for losses over a global batch
+ *   d_logits               [T, E] out, the logits' type; 0 for a row of -inf alone */
+moe_status moe_router_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                               const int32_t* expert_ids, const float* routing_w, const int32_t* counts,
+                               const int32_t* tokens, const float* d_routing_w, const float* d_losses, void* d_logits,
+                               hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4 rows and experts (OCP Microscaling Formats v1.0).
+ *
+ * 32 consecutive values along the contraction share a scale 2^e, kept as the
+ * byte e + 127; each value is a 4-bit float E2M1: sign, two exponent bits, one
+ * mantissa bit, magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6. A row of K values is
+ *
+ *   q       uint8 [16 * ceil(K / 32)]   value 2i in the low half of byte i,
+ *                                       zeros behind value K - 1
+ *   scales  uint8 [16 * ceil(K / 512)]  one byte per block, then padding
+ *                                       (written as 0, never read into a result)
+ *
+ * both row after row without gaps and 16-byte aligned. K is a multiple of 8.
+ *
+ * Quantising: e = floor(log2(largest magnitude of the block)) - 2, at least
+ * -127; values are rounded to nearest even and saturate at 6 * 2^e. A block
+ * with an infinity or a NaN gets scale byte 255, which reads back as NaN for
+ * every value of the block.
+ * ------------------------------------------------------------------------- */
+size_t moe_mxfp4_row_bytes(int64_t K);
+size_t moe_mxfp4_scale_bytes(int64_t K);
+
+/* x bf16 [rows, K] to q and scales, one launch. */
+moe_status moe_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                              hipStream_t stream);
+
+/* Expert weights of either layout to packed rows [E, d_out] of d_in values:
+ * the products below contract along a packed row. One launch. */
+moe_status moe_mxfp4_quantize_weights(const uint16_t* w, int32_t w_layout, int64_t d_in, int64_t d_out, int32_t E,
+                                      uint8_t* q, uint8_t* scales, hipStream_t stream);
+
+/* Packed rows back to bf16 [rows, K] (exact), one launch. */
+moe_status moe_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
+                                hipStream_t stream);
+
+/* moe_grouped_projection with MXFP4 rows and weights: y[rows_e] = bf16(x[rows_e] W_e^T),
+ * products exact, fp32 accumulation, one rounding.
+ *
+ *   x_q, x_scales  [cap_rows] rows of d_in values
+ *   offsets        int32 [E+1], clamped as in the bf16 calls
+ *   w_q, w_scales  [E, d_out] rows of d_in values
+ *   y              bf16 [cap_rows, d_out] out (rows past M untouched) */
+moe_status moe_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* offsets,
+                                        const uint8_t* w_q, const uint8_t* w_scales, int64_t cap_rows, int64_t d_in,
+                                        int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream);
+
+/* moe_gemm_up_swiglu(_gather) with MXFP4 rows and weights:
+ * h_buf[p] = bf16(SiLU(g) * u), [g | u] = x[perm[p] / k] W_ug[e]^T, SiLU taken
+ * of the fp32 sums (g and u are not rounded in between).
+ *
+ *   x_q, x_scales  [T] token rows of d values
+ *   perm           int32 [T*k] as written by moe_permute; NULL with k = 1 when
+ *                  the T rows are sorted already
+ *   w_q, w_scales  [E, 2h] rows of d values, gate rows first
+ *   h_buf          bf16 [T*k, h] out (rows past M untouched) */
+moe_status moe_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* perm, int64_t T,
+                                    int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
+                                    int64_t d, int64_t h, int32_t E, uint16_t* h_buf, hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char* moe_status_string(moe_status s);
 

@@ -45,6 +45,18 @@ _SIGNATURES = {
     "moe_grouped_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     "moe_permute_backward": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i64, _vp, _vp]),
     "moe_unpermute_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp]),
+    "moe_router_workspace_bytes": (_sz, [_i64, _i32]),
+    "moe_router_topk": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "moe_router_topk_losses": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _sz, _vp]),
+    "moe_router_backward": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_mxfp4_row_bytes": (_sz, [_i64]),
+    "moe_mxfp4_scale_bytes": (_sz, [_i64]),
+    "moe_mxfp4_quantize": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "moe_mxfp4_quantize_weights": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "moe_mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "moe_grouped_projection_mxfp4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "moe_gemm_up_swiglu_mxfp4": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -477,6 +489,225 @@ def moe_expert_forward(x, expert_ids, routing_w, w_ug, w_down, fused_gather: boo
     return y, p, h_buf, y_perm
 
 
+# ------------------------------------------------------------------ router
+
+_LOGITS = {torch.bfloat16: 0, torch.float32: 1}
+ROUTER_MAX_TOPK = 64
+
+
+@dataclass
+class Routed:
+    expert_ids: torch.Tensor  # int32 [T, k]; -1 for a slot left over by the mask
+    routing_w: torch.Tensor  # fp32 [T, k]
+    lse: torch.Tensor  # fp32 [T]
+    renormalize: bool
+    counts: torch.Tensor | None = None  # int32 [E]; these four from moe_router_topk_losses only
+    tokens: torch.Tensor | None = None  # int32 [1]
+    prob_mean: torch.Tensor | None = None  # fp32 [E]
+    losses: torch.Tensor | None = None  # fp32 [2]: balance loss, z-loss
+
+
+def _logits(logits: torch.Tensor, k: int):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if logits.dtype not in _LOGITS:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    T, E = logits.shape
+    _want(logits, "logits", logits.dtype, (T, E), logits.device)
+    if not 1 <= int(k) <= min(E, ROUTER_MAX_TOPK):
+        raise ValueError(f"k must be between 1 and min(E, {ROUTER_MAX_TOPK}), got {k} for E = {E}")
+    return T, E, _LOGITS[logits.dtype], logits.device
+
+
+def moe_router_topk(logits: torch.Tensor, k: int, *, renormalize: bool = True, expert_ids=None, routing_w=None,
+                    lse=None) -> Routed:
+    """The k largest logits of every row (lowest index first among equals), their softmax weights and the row's
+    log-sum-exp (one launch). Experts at -inf are never chosen: their slots get id -1 and weight 0."""
+    T, E, dtype, dev = _logits(logits, k)
+    expert_ids = _out(expert_ids, "expert_ids", torch.int32, (T, k), dev)
+    routing_w = _out(routing_w, "routing_w", torch.float32, (T, k), dev)
+    lse = _out(lse, "lse", torch.float32, (T,), dev)
+    _check(load_library().moe_router_topk(_ptr(logits), dtype, T, E, k, int(renormalize), _ptr(expert_ids),
+                                          _ptr(routing_w), _ptr(lse), _stream(logits)), "moe_router_topk")
+    return Routed(expert_ids, routing_w, lse, bool(renormalize))
+
+
+def router_workspace_bytes(T: int, E: int) -> int:
+    return int(load_library().moe_router_workspace_bytes(T, E))
+
+
+def moe_router_topk_losses(logits: torch.Tensor, k: int, *, renormalize: bool = True, expert_ids=None, routing_w=None,
+                           lse=None, counts=None, tokens=None, prob_mean=None, losses=None, workspace=None) -> Routed:
+    """moe_router_topk with the per-expert counts, the mean probabilities, and losses = [balance, z] (two launches)."""
+    T, E, dtype, dev = _logits(logits, k)
+    expert_ids = _out(expert_ids, "expert_ids", torch.int32, (T, k), dev)
+    routing_w = _out(routing_w, "routing_w", torch.float32, (T, k), dev)
+    lse = _out(lse, "lse", torch.float32, (T,), dev)
+    counts = _out(counts, "counts", torch.int32, (E,), dev)
+    tokens = _out(tokens, "tokens", torch.int32, (1,), dev)
+    prob_mean = _out(prob_mean, "prob_mean", torch.float32, (E,), dev)
+    losses = _out(losses, "losses", torch.float32, (2,), dev)
+    if workspace is None:
+        workspace = torch.empty((router_workspace_bytes(T, E),), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    _check(load_library().moe_router_topk_losses(_ptr(logits), dtype, T, E, k, int(renormalize), _ptr(expert_ids),
+                                                 _ptr(routing_w), _ptr(lse), _ptr(counts), _ptr(tokens),
+                                                 _ptr(prob_mean), _ptr(losses), _ptr(workspace), workspace.numel(),
+                                                 _stream(logits)), "moe_router_topk_losses")
+    return Routed(expert_ids, routing_w, lse, bool(renormalize), counts, tokens, prob_mean, losses)
+
+
+def moe_router_backward(logits: torch.Tensor, routed: Routed, d_routing_w: torch.Tensor | None = None,
+                        d_losses: torch.Tensor | None = None, *, d_logits=None) -> torch.Tensor:
+    """Gradient of the logits from those of the routing weights ([T, k] fp32) and of the losses ([2] fp32, on the
+    device); either may be None (one launch). For losses over several ranks' tokens, sum ``routed.counts`` and
+    ``routed.tokens`` over the ranks first."""
+    k = routed.expert_ids.shape[1]
+    T, E, dtype, dev = _logits(logits, k)
+    _want(routed.expert_ids, "expert_ids", torch.int32, (T, k), dev)
+    _want(routed.routing_w, "routing_w", torch.float32, (T, k), dev)
+    if d_routing_w is not None:
+        _want(d_routing_w, "d_routing_w", torch.float32, (T, k), dev)
+    if d_losses is not None:
+        if routed.counts is None or routed.tokens is None:
+            raise ValueError("the gradient of the losses needs the counts of moe_router_topk_losses")
+        _want(d_losses, "d_losses", torch.float32, (2,), dev)
+        _want(routed.counts, "counts", torch.int32, (E,), dev)
+        _want(routed.tokens, "tokens", torch.int32, (1,), dev)
+    d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), dev)
+    _check(load_library().moe_router_backward(_ptr(logits), dtype, T, E, k, int(routed.renormalize),
+                                              _ptr(routed.expert_ids), _ptr(routed.routing_w), _ptr(routed.counts),
+                                              _ptr(routed.tokens), _ptr(d_routing_w), _ptr(d_losses), _ptr(d_logits),
+                                              _stream(logits)), "moe_router_backward")
+    return d_logits
+
+
+# ------------------------------------------------------------------ MXFP4
+
+
+@dataclass
+class Mxfp4:
+    """Rows of ``width`` 4-bit values with a power of two per 32: q [..., 16 * ceil(width / 32)] and
+    scales [..., 16 * ceil(width / 512)], both uint8."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    width: int
+
+
+def mxfp4_row_bytes(width: int) -> int:
+    return 16 * ((width + 31) // 32)
+
+
+def mxfp4_scale_bytes(width: int) -> int:
+    return 16 * ((width + 511) // 512)
+
+
+def _want_mxfp4(m: Mxfp4, name: str, lead: tuple, device) -> None:
+    if not isinstance(m, Mxfp4):
+        raise TypeError(f"{name} must be an Mxfp4")
+    _want(m.q, f"{name}.q", torch.uint8, (*lead, mxfp4_row_bytes(m.width)), device)
+    _want(m.scales, f"{name}.scales", torch.uint8, (*lead, mxfp4_scale_bytes(m.width)), device)
+
+
+def moe_mxfp4_quantize(x: torch.Tensor, *, q=None, scales=None) -> Mxfp4:
+    """bf16 rows [..., K] to MXFP4 along the last dimension (one launch)."""
+    if x.dim() < 1:
+        raise ValueError("x must have a last dimension to quantise along")
+    _want(x, "x", torch.bfloat16, tuple(x.shape), x.device)
+    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    q = _out(q, "q", torch.uint8, (*lead, mxfp4_row_bytes(K)), x.device)
+    scales = _out(scales, "scales", torch.uint8, (*lead, mxfp4_scale_bytes(K)), x.device)
+    rows = 1
+    for n in lead:
+        rows *= n
+    _check(load_library().moe_mxfp4_quantize(_ptr(x), rows, K, _ptr(q), _ptr(scales), _stream(x)),
+           "moe_mxfp4_quantize")
+    return Mxfp4(q, scales, K)
+
+
+def moe_mxfp4_quantize_weights(w: torch.Tensor, layout: str = "in_out", *, q=None, scales=None) -> Mxfp4:
+    """Expert weights [E, d_in, d_out] ("in_out") or [E, d_out, d_in] ("out_in") to MXFP4 rows [E, d_out] of d_in
+    values, the form the MXFP4 products read (one launch)."""
+    E, d_in, d_out = _w_dims(w, layout)
+    dev = w.device
+    _want(w, "w", torch.bfloat16, tuple(w.shape), dev)
+    q = _out(q, "q", torch.uint8, (E, d_out, mxfp4_row_bytes(d_in)), dev)
+    scales = _out(scales, "scales", torch.uint8, (E, d_out, mxfp4_scale_bytes(d_in)), dev)
+    _check(load_library().moe_mxfp4_quantize_weights(_ptr(w), W_LAYOUTS[layout], d_in, d_out, E, _ptr(q), _ptr(scales),
+                                                     _stream(w)), "moe_mxfp4_quantize_weights")
+    return Mxfp4(q, scales, d_in)
+
+
+def moe_mxfp4_dequantize(m: Mxfp4, *, x=None) -> torch.Tensor:
+    """The bf16 values of MXFP4 rows (exact; one launch)."""
+    if not isinstance(m, Mxfp4) or m.q.dim() < 1:
+        raise TypeError("expected an Mxfp4")
+    lead, dev = tuple(m.q.shape[:-1]), m.q.device
+    _want_mxfp4(m, "m", lead, dev)
+    x = _out(x, "x", torch.bfloat16, (*lead, m.width), dev)
+    rows = 1
+    for n in lead:
+        rows *= n
+    _check(load_library().moe_mxfp4_dequantize(_ptr(m.q), _ptr(m.scales), rows, m.width, _ptr(x), _stream(m.q)),
+           "moe_mxfp4_dequantize")
+    return x
+
+
+def _mxfp4_experts(x: Mxfp4, offsets: torch.Tensor, w: Mxfp4):
+    if not isinstance(x, Mxfp4) or not isinstance(w, Mxfp4) or x.q.dim() != 2 or w.q.dim() != 3:
+        raise ValueError("expected Mxfp4 rows [rows, .] and Mxfp4 expert weights [E, d_out, .]")
+    if x.width != w.width:
+        raise ValueError(f"rows of {x.width} values do not fit weights of {w.width}")
+    rows, dev = x.q.shape[0], x.q.device
+    E, w_rows = w.q.shape[:2]
+    _want_mxfp4(x, "x", (rows,), dev)
+    _want_mxfp4(w, "w", (E, w_rows), dev)
+    _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    return rows, E, w_rows, dev
+
+
+def moe_grouped_projection_mxfp4(x: Mxfp4, offsets: torch.Tensor, w: Mxfp4, *, y=None) -> torch.Tensor:
+    """Y[rows_e] = bf16(X[rows_e] @ W_e^T) on MXFP4 rows [cap, d_in] and weights [E, d_out, d_in] (one launch)."""
+    cap, E, d_out, dev = _mxfp4_experts(x, offsets, w)
+    y = _out(y, "y", torch.bfloat16, (cap, d_out), dev)
+    _check(load_library().moe_grouped_projection_mxfp4(_ptr(x.q), _ptr(x.scales), _ptr(offsets), _ptr(w.q),
+                                                       _ptr(w.scales), cap, x.width, d_out, E, _ptr(y), _stream(x.q)),
+           "moe_grouped_projection_mxfp4")
+    return y
+
+
+def moe_gemm_up_swiglu_mxfp4(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, *, perm=None, k: int = 1,
+                             h_buf=None) -> torch.Tensor:
+    """h_buf[p] = bf16(SiLU(g) * u), [g | u] = X[perm[p] // k] @ W_ug[e]^T, on MXFP4 token rows [T, d] and weights
+    [E, 2h, d] (one launch). Without ``perm`` the rows are sorted already and k is 1."""
+    T, E, two_h, dev = _mxfp4_experts(x, offsets, w_ug)
+    if two_h % 2:
+        raise ValueError("w_ug must hold as many gate as up rows")
+    h, k = two_h // 2, int(k)
+    if perm is not None:
+        _want(perm, "perm", torch.int32, (T * k,), dev)
+    elif k != 1:
+        raise ValueError("k other than 1 needs perm")
+    h_buf = _out(h_buf, "h_buf", torch.bfloat16, (T * k, h), dev)
+    _check(load_library().moe_gemm_up_swiglu_mxfp4(_ptr(x.q), _ptr(x.scales), _ptr(perm), T, k, _ptr(offsets),
+                                                   _ptr(w_ug.q), _ptr(w_ug.scales), x.width, h, E, _ptr(h_buf),
+                                                   _stream(x.q)), "moe_gemm_up_swiglu_mxfp4")
+    return h_buf
+
+
+def moe_expert_forward_mxfp4(x: torch.Tensor, expert_ids: torch.Tensor, routing_w: torch.Tensor, w_ug: Mxfp4,
+                             w_down: Mxfp4):
+    """The whole step on MXFP4 experts, from bf16 token rows: the rows and the SwiGLU activations are quantised on the
+    way. ``w_ug`` holds [E, 2h] rows of d values, ``w_down`` [E, d] rows of h (moe_mxfp4_quantize_weights of the bf16
+    weights). Returns (y, Permuted)."""
+    k = expert_ids.shape[1]
+    p = moe_permute(x, expert_ids, w_ug.q.shape[0], gather=False)
+    h_buf = moe_gemm_up_swiglu_mxfp4(moe_mxfp4_quantize(x), p.offsets, w_ug, perm=p.perm, k=k)
+    y_perm = moe_grouped_projection_mxfp4(moe_mxfp4_quantize(h_buf), p.offsets, w_down)
+    return moe_unpermute(y_perm, p.inv_map, routing_w), p
+
+
 __all__ = [
     "LIB_PATH", "MAX_EXPERTS", "MoeError", "Permuted", "grouped_swiglu_expert", "header_functions", "load_library",
     "grouped_swiglu_expert_gather", "moe_expert_forward", "moe_gemm_down", "moe_gemm_up_swiglu",
@@ -484,4 +715,8 @@ __all__ = [
     "permute_workspace_bytes", "W_LAYOUTS", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_permute_backward", "wgrad_workspace_bytes",
     "moe_grouped_projection", "moe_swiglu_backward", "moe_expert_backward",
     "moe_unpermute_backward",
+    "ROUTER_MAX_TOPK", "Routed", "moe_router_topk", "moe_router_topk_losses", "moe_router_backward",
+    "router_workspace_bytes", "Mxfp4", "mxfp4_row_bytes", "mxfp4_scale_bytes", "moe_mxfp4_quantize",
+    "moe_mxfp4_quantize_weights", "moe_mxfp4_dequantize", "moe_grouped_projection_mxfp4", "moe_gemm_up_swiglu_mxfp4",
+    "moe_expert_forward_mxfp4",
 ]

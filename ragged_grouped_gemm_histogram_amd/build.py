@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmoe_grouped.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["abi.hip", "permute.hip", "gemm.hip", "unpermute.hip"]
+SOURCES = ["abi.hip", "permute.hip", "gemm.hip", "unpermute.hip", "router.hip", "mxfp4.hip", "mxfp4_gemm.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 instructions stay off: every float operation is issued unpacked.

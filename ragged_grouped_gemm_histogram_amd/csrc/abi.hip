@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "common.h"
+#include "mxfp4.h"
 
 namespace moe {
 namespace {
@@ -47,6 +48,20 @@ moe_status check_gemm_shape(int64_t cap_rows, int64_t d, int64_t h, int32_t E) {
     return MOE_ERR_BAD_SHAPE;
   if (d > kMaxGemmWidth || h > kMaxGemmWidth) return MOE_ERR_BAD_SHAPE;
   return MOE_OK;
+}
+
+inline uintptr_t logit_bytes(int32_t dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+moe_status check_router_shape(int32_t dtype, int64_t T, int32_t E, int32_t k) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_BAD_SHAPE;
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > E || k > MOE_ROUTER_MAX_TOPK || T > kMaxSlots / k)
+    return MOE_ERR_BAD_SHAPE;
+  return MOE_OK;
+}
+
+// Rows the quantising launches take: their workgroups (1024 pieces of 8 values each) are counted in 31 bits.
+inline bool bad_mxfp4_rows(int64_t rows, int64_t K) {
+  return rows < 0 || bad_width(K) || rows > (kMaxSlots * 1024) / (mx_blocks(K) * 4);
 }
 
 }  // namespace
@@ -321,6 +336,152 @@ moe_status moe_unpermute_backward(const uint16_t* dy, const uint16_t* y_perm, co
   if (T == 0) return MOE_OK;
   (void)hipGetLastError();
   return launched(launch_unpermute_backward(dy, y_perm, inv_map, routing_w, T, k, d, dy_perm, d_routing_w, stream));
+}
+
+// ------------------------------------------------------------------ router
+
+size_t moe_router_workspace_bytes(int64_t T, int32_t E) {
+  if (T < 0 || T > kMaxSlots || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+  return (size_t)router_partial_words(T, E) * sizeof(uint32_t);
+}
+
+moe_status moe_router_topk(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                           int32_t* expert_ids, float* routing_w, float* lse, hipStream_t stream) {
+  moe_status st = check_router_shape(dtype, T, E, k);
+  if (st != MOE_OK) return st;
+  const int64_t S = T * k;
+  if (missing(logits, T) || missing(expert_ids, S) || missing(routing_w, S) || missing(lse, T))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(logits, logit_bytes(dtype)) || misaligned(expert_ids, 4) || misaligned(routing_w, 4) ||
+      misaligned(lse, 4))
+    return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_router_topk(logits, dtype == MOE_F32, T, E, k, renormalize != 0, expert_ids, routing_w, lse,
+                                     stream));
+}
+
+moe_status moe_router_topk_losses(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
+                                  int32_t renormalize, int32_t* expert_ids, float* routing_w, float* lse,
+                                  int32_t* counts, int32_t* tokens, float* prob_mean, float* losses, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+  moe_status st = check_router_shape(dtype, T, E, k);
+  if (st != MOE_OK) return st;
+  const int64_t S = T * k;
+  if (missing(logits, T) || missing(expert_ids, S) || missing(routing_w, S) || missing(lse, T) || counts == nullptr ||
+      tokens == nullptr || prob_mean == nullptr || losses == nullptr || workspace == nullptr)
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(logits, logit_bytes(dtype)) || misaligned(expert_ids, 4) || misaligned(routing_w, 4) ||
+      misaligned(lse, 4) || misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(prob_mean, 4) ||
+      misaligned(losses, 4) || misaligned(workspace, 4))
+    return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < moe_router_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_router_topk_losses(logits, dtype == MOE_F32, T, E, k, renormalize != 0, expert_ids, routing_w,
+                                            lse, counts, tokens, prob_mean, losses, static_cast<uint32_t*>(workspace),
+                                            stream));
+}
+
+moe_status moe_router_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                               const int32_t* expert_ids, const float* routing_w, const int32_t* counts,
+                               const int32_t* tokens, const float* d_routing_w, const float* d_losses, void* d_logits,
+                               hipStream_t stream) {
+  moe_status st = check_router_shape(dtype, T, E, k);
+  if (st != MOE_OK) return st;
+  const int64_t S = T * k;
+  if (missing(logits, T) || missing(d_logits, T) ||
+      (d_routing_w != nullptr && (missing(expert_ids, S) || missing(routing_w, S))) ||
+      (d_losses != nullptr && (counts == nullptr || tokens == nullptr)))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(logits, logit_bytes(dtype)) || misaligned(d_logits, logit_bytes(dtype)) || misaligned(expert_ids, 4) ||
+      misaligned(routing_w, 4) || misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(d_routing_w, 4) ||
+      misaligned(d_losses, 4))
+    return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_router_backward(logits, dtype == MOE_F32, T, E, k, renormalize != 0, expert_ids, routing_w,
+                                         counts, tokens, d_routing_w, d_losses, d_logits, stream));
+}
+
+// ------------------------------------------------------------------ MXFP4
+
+size_t moe_mxfp4_row_bytes(int64_t K) { return bad_width(K) ? 0 : (size_t)mx_row_bytes(K); }
+
+size_t moe_mxfp4_scale_bytes(int64_t K) { return bad_width(K) ? 0 : (size_t)mx_scale_bytes(K); }
+
+moe_status moe_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                              hipStream_t stream) {
+  if (bad_mxfp4_rows(rows, K)) return MOE_ERR_BAD_SHAPE;
+  if (missing(x, rows) || missing(q, rows) || missing(scales, rows)) return MOE_ERR_NULL_POINTER;
+  if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scales, 16)) return MOE_ERR_MISALIGNED;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_mxfp4_quantize(x, rows, K, q, scales, stream));
+}
+
+moe_status moe_mxfp4_quantize_weights(const uint16_t* w, int32_t w_layout, int64_t d_in, int64_t d_out, int32_t E,
+                                      uint8_t* q, uint8_t* scales, hipStream_t stream) {
+  if (w_layout != MOE_W_IN_OUT && w_layout != MOE_W_OUT_IN) return MOE_ERR_BAD_SHAPE;
+  moe_status st = check_gemm_shape(0, d_in, d_out, E);
+  if (st != MOE_OK) return st;
+  if (bad_mxfp4_rows((int64_t)E * d_out, d_in)) return MOE_ERR_BAD_SHAPE;
+  if (w == nullptr || q == nullptr || scales == nullptr) return MOE_ERR_NULL_POINTER;
+  if (misaligned(w, 16) || misaligned(q, 16) || misaligned(scales, 16)) return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  if (w_layout == MOE_W_OUT_IN) return launched(launch_mxfp4_quantize(w, (int64_t)E * d_out, d_in, q, scales, stream));
+  return launched(launch_mxfp4_quantize_columns(w, d_in, d_out, E, q, scales, stream));
+}
+
+moe_status moe_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
+                                hipStream_t stream) {
+  if (bad_mxfp4_rows(rows, K)) return MOE_ERR_BAD_SHAPE;
+  if (missing(x, rows) || missing(q, rows) || missing(scales, rows)) return MOE_ERR_NULL_POINTER;
+  if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scales, 16)) return MOE_ERR_MISALIGNED;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_mxfp4_dequantize(q, scales, rows, K, x, stream));
+}
+
+moe_status moe_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* offsets,
+                                        const uint8_t* w_q, const uint8_t* w_scales, int64_t cap_rows, int64_t d_in,
+                                        int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream) {
+  moe_status st = check_gemm_shape(cap_rows, d_in, d_out, E);
+  if (st != MOE_OK) return st;
+  if (missing(x_q, cap_rows) || missing(x_scales, cap_rows) || offsets == nullptr || w_q == nullptr ||
+      w_scales == nullptr || missing(y, cap_rows))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(x_q, 16) || misaligned(x_scales, 16) || misaligned(w_q, 16) || misaligned(w_scales, 16) ||
+      misaligned(y, 16) || misaligned(offsets, 4))
+    return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  if (cap_rows == 0) return MOE_OK;
+  (void)hipGetLastError();
+  return launched(launch_grouped_projection_mxfp4(x_q, x_scales, offsets, w_q, w_scales, cap_rows, d_in, d_out, E, y,
+                                                  stream));
+}
+
+moe_status moe_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* perm, int64_t T,
+                                    int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
+                                    int64_t d, int64_t h, int32_t E, uint16_t* h_buf, hipStream_t stream) {
+  if (T < 0 || k < 1 || T > kMaxSlots / k || (perm == nullptr && k != 1 && T != 0)) return MOE_ERR_BAD_SHAPE;
+  const int64_t S = T * k;
+  moe_status st = check_gemm_shape(S, d, h, E);
+  if (st != MOE_OK) return st;
+  if (missing(x_q, T) || missing(x_scales, T) || offsets == nullptr || w_q == nullptr || w_scales == nullptr ||
+      missing(h_buf, S))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(x_q, 16) || misaligned(x_scales, 16) || misaligned(w_q, 16) || misaligned(w_scales, 16) ||
+      misaligned(h_buf, 16) || misaligned(offsets, 4) || misaligned(perm, 4))
+    return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  if (S == 0) return MOE_OK;
+  (void)hipGetLastError();
+  return launched(launch_gemm_up_swiglu_mxfp4(x_q, x_scales, T, perm, k, offsets, w_q, w_scales, S, d, h, E, h_buf,
+                                              stream));
 }
 
 static_assert(sizeof(moe_status) == sizeof(int), "moe_status travels as a C int");

@@ -95,4 +95,30 @@ hipError_t launch_unpermute_backward(const uint16_t* dy, const uint16_t* y_perm,
 hipError_t launch_unpermute(const uint16_t* y_perm, const int32_t* inv, const float* w, int64_t T, int32_t k,
                             int64_t d, uint16_t* y, hipStream_t stream);
 
+// Router. The losses' launch leaves router_partial_words(T, E) 32-bit words of partial sums.
+int64_t router_partial_words(int64_t T, int32_t E);
+hipError_t launch_router_topk(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
+                              int32_t* ids, float* w, float* lse, hipStream_t stream);
+hipError_t launch_router_topk_losses(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
+                                     int32_t* ids, float* w, float* lse, int32_t* counts, int32_t* tokens,
+                                     float* prob_mean, float* losses, uint32_t* partial, hipStream_t stream);
+hipError_t launch_router_backward(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
+                                  const int32_t* ids, const float* w, const int32_t* counts, const int32_t* tokens,
+                                  const float* d_w, const float* d_losses, void* d_logits, hipStream_t stream);
+
+// MXFP4 rows and the grouped products of them.
+hipError_t launch_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                                 hipStream_t stream);
+hipError_t launch_mxfp4_quantize_columns(const uint16_t* x, int64_t K, int64_t N, int32_t E, uint8_t* q,
+                                         uint8_t* scales, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
+                                   hipStream_t stream);
+hipError_t launch_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_s, const int32_t* offsets,
+                                           const uint8_t* w_q, const uint8_t* w_s, int64_t cap_rows, int64_t d_in,
+                                           int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream);
+hipError_t launch_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_s, int64_t x_rows, const int32_t* perm,
+                                       int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_s,
+                                       int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf,
+                                       hipStream_t stream);
+
 }  // namespace moe

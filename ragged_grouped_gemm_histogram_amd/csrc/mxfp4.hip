@@ -1,0 +1,167 @@
+// MXFP4 (OCP Microscaling Formats v1.0, MXFP4): blocks of 32 values share a power of two, kept as the
+// byte e + 127 (255 marks a block that held an infinity or a NaN); each value is a 4-bit float E2M1
+// (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6). A block's exponent is e = floor(log2 max|x|) - 2, not below
+// -127; values are rounded to nearest even and saturate at 6. A packed row of K values is
+// 16 * ceil(K / 32) bytes (value 2i in the low half of byte i) and its scale bytes are
+// 16 * ceil(K / 512), zeros behind the last block.
+//
+// Quantising and reading back are one pass over memory: 2 bytes in and 17/32 out per value (the
+// other way round back), so both are bound by HBM. A quad of lanes holds one block, 8 values (16
+// bytes) a lane; the block's maximum takes two lane exchanges and the conversion four packed
+// convert instructions a lane.
+
+#include "mxfp4.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunksPerThread = 4;
+
+// Rows of K-contiguous values. Work item: 8 consecutive values of a row padded to whole blocks; a
+// workgroup takes kThreads * kChunksPerThread consecutive items.
+__global__ __launch_bounds__(kThreads) void mxfp4_quantize_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t K,
+                                                                  uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  const int64_t cpr = mx_blocks(K) * 4;  // items per row
+  const int64_t total = rows * cpr;
+  const int64_t span = (int64_t)kThreads * kChunksPerThread;
+  const int64_t first = (int64_t)blockIdx.x * span;
+  const int64_t row0 = first / cpr;
+  const int rem0 = (int)(first - row0 * cpr);
+  const float inv = 1.0f / (float)cpr;
+  u32x4 v[kChunksPerThread];
+  int64_t row[kChunksPerThread];
+  int chunk[kChunksPerThread];
+#pragma unroll
+  for (int i = 0; i < kChunksPerThread; ++i) {
+    // rem0 + local < 2^24: the fp32 quotient is off by at most one
+    const int local = rem0 + i * kThreads + (int)threadIdx.x;
+    int r = (int)((float)local * inv);
+    int c = local - r * (int)cpr;
+    if (c < 0) { --r; c += (int)cpr; }
+    if (c >= cpr) { ++r; c -= (int)cpr; }
+    row[i] = row0 + r;
+    chunk[i] = c;
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (row[i] < rows && (int64_t)c * 8 < K) v[i] = *reinterpret_cast<const u32x4*>(x + row[i] * K + (int64_t)c * 8);
+  }
+  const int64_t qp = mx_row_bytes(K), sp = mx_scale_bytes(K);
+#pragma unroll
+  for (int i = 0; i < kChunksPerThread; ++i) {
+    if (first + i * kThreads + threadIdx.x >= total) continue;  // whole quads: total is a multiple of 4
+    uint32_t top = max_magnitude(v[i]);
+    top = max(top, quad_xor<0xB1>(top));
+    top = max(top, quad_xor<0x4E>(top));
+    const uint32_t byte = scale_byte(top);
+    reinterpret_cast<uint32_t*>(q + row[i] * qp)[chunk[i]] = to_fp4(v[i], byte);
+    if ((chunk[i] & 3) == 0) {
+      const int64_t b = chunk[i] >> 2;
+      uint8_t* s = scales + row[i] * sp;
+      s[b] = (uint8_t)byte;
+      if (b == mx_blocks(K) - 1)
+        for (int64_t z = b + 1; z < sp; ++z) s[z] = 0;
+    }
+  }
+}
+
+// Weights stored with the contraction outermost, [E, K, N]: the packed rows are the columns. A lane
+// takes two neighbouring columns (4-byte loads, 256 contiguous bytes a wave) over one block of 32 k.
+__global__ __launch_bounds__(kThreads) void mxfp4_quantize_columns_kernel(const uint16_t* __restrict__ x, int64_t K, int64_t N,
+                                                                          uint8_t* __restrict__ q,
+                                                                          uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = ((int64_t)blockIdx.x * 64 + lane) * 2;
+  const int64_t b = (int64_t)blockIdx.y * 4 + wave;
+  const int64_t e = blockIdx.z;
+  if (n >= N || b >= mx_blocks(K)) return;
+  const uint16_t* src = x + (e * K + b * 32) * N + n;
+  uint32_t v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = b * 32 + i < K ? *reinterpret_cast<const uint32_t*>(src + (int64_t)i * N) : 0u;
+  const int64_t qp = mx_row_bytes(K), sp = mx_scale_bytes(K);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    u32x4 part[4], out;
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a = v[8 * c + 2 * w], d = v[8 * c + 2 * w + 1];
+        part[c][w] = half == 0 ? (a & 0xFFFFu) | (d << 16) : (a >> 16) | (d & 0xFFFF0000u);
+      }
+      top = max(top, max_magnitude(part[c]));
+    }
+    const uint32_t byte = scale_byte(top);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[c] = to_fp4(part[c], byte);
+    const int64_t r = e * N + n + half;
+    *reinterpret_cast<u32x4*>(q + r * qp + b * 16) = out;
+    uint8_t* s = scales + r * sp;
+    s[b] = (uint8_t)byte;
+    if (b == mx_blocks(K) - 1)
+      for (int64_t z = b + 1; z < sp; ++z) s[z] = 0;
+  }
+}
+
+// Packed rows back to bf16: exact, the products of a 4-bit value and a power of two have two
+// significant bits and at least 2^-128, bf16's smallest normals and subnormals hold them.
+__global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ q,
+                                                                    const uint8_t* __restrict__ scales, int64_t rows,
+                                                                    int64_t K, uint16_t* __restrict__ x) {
+  const int64_t cpr = K / 8;
+  const int64_t span = (int64_t)kThreads * kChunksPerThread;
+  const int64_t first = (int64_t)blockIdx.x * span;
+  const int64_t row0 = first / cpr;
+  const int rem0 = (int)(first - row0 * cpr);
+  const float inv = 1.0f / (float)cpr;
+  const int64_t qp = mx_row_bytes(K), sp = mx_scale_bytes(K);
+  uint32_t code[kChunksPerThread], byte[kChunksPerThread];
+  int64_t at[kChunksPerThread];
+#pragma unroll
+  for (int i = 0; i < kChunksPerThread; ++i) {
+    const int local = rem0 + i * kThreads + (int)threadIdx.x;
+    int r = (int)((float)local * inv);
+    int c = local - r * (int)cpr;
+    if (c < 0) { --r; c += (int)cpr; }
+    if (c >= cpr) { ++r; c -= (int)cpr; }
+    const int64_t row = row0 + r;
+    at[i] = row < rows ? row * K + (int64_t)c * 8 : -1;
+    if (row < rows) {
+      code[i] = reinterpret_cast<const uint32_t*>(q + row * qp)[c];
+      byte[i] = scales[row * sp + (c >> 2)];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kChunksPerThread; ++i)
+    if (at[i] >= 0) *reinterpret_cast<u32x4*>(x + at[i]) = from_fp4(code[i], byte[i]);
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
+                                 hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const int64_t span = (int64_t)kThreads * kChunksPerThread;
+  const int64_t blocks = (rows * mx_blocks(K) * 4 + span - 1) / span;
+  hipLaunchKernelGGL(mxfp4_quantize_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, x, rows, K, q, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_quantize_columns(const uint16_t* x, int64_t K, int64_t N, int32_t E, uint8_t* q,
+                                         uint8_t* scales, hipStream_t stream) {
+  const dim3 grid((unsigned)((N + 127) / 128), (unsigned)((mx_blocks(K) + 3) / 4), (unsigned)E);
+  hipLaunchKernelGGL(mxfp4_quantize_columns_kernel, grid, dim3(kThreads), 0, stream, x, K, N, q, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
+                                   hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const int64_t span = (int64_t)kThreads * kChunksPerThread;
+  const int64_t blocks = (rows * (K / 8) + span - 1) / span;
+  hipLaunchKernelGGL(mxfp4_dequantize_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, q, scales, rows, K, x);
+  return hipGetLastError();
+}
+
+}  // namespace moe

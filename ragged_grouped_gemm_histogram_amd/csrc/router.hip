@@ -1,0 +1,539 @@
+// Router of the MoE layer: from logits x [T, E] the k routed experts of every token, their weights,
+// and, for training, the balance loss, the z-loss and the gradient of the logits.
+//
+//   m = max_i x_i,  s = sum_i exp(x_i - m),  lse = m + log s,  p_i = exp(x_i - m) / s
+//   ids = the k largest logits, the lowest index first among equals; -inf is never chosen
+//   w_j = p_{id_j}, or p_{id_j} / sum_l p_{id_l} (renormalised)
+//   losses = ( E sum_e f_e P_e , 1/n sum_t lse_t^2 ),  f_e = counts_e / sum counts,  P_e = 1/n sum_t p_te
+//
+// over the n tokens whose row is not all -inf. With c_e = dL0 E f_e / n the gradient of a row is
+//
+//   dx_i = p_i (c_i - sum_l c_l p_l + 2 dL1 lse / n) + routing part,
+//   routing part = w_j (g_j - sum_l g_l w_l) at i = id_j (renormalised), else p_i (g_i - sum_l g_l p_{id_l})
+//
+// with g the gradient of the weights (g_i zero off the chosen experts).
+//
+// G lanes hold one token (V consecutive experts each), so a wave works on 64 / G tokens and a
+// reduction over a token is log2 G lane exchanges. The row stays in registers from its one read to
+// its last use. Everything is fp32 with the correctly rounded-to-an-ulp exponential; rows are
+// summed in a fixed order, and column sums over tokens go lane -> workgroup -> a second launch over
+// the workgroups' partials, also in a fixed order (no floating-point atomics).
+
+#include <type_traits>
+
+#include "common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Value of the lane whose index differs from this one's in the bits of a group step: lanes 1, 2
+// (quad permutes), 4 (mirror of 8, after the quads agree), 8 (mirror of 16), 16 and 32 apart.
+template <int STEP>
+__device__ __forceinline__ float partner(float v) {
+  if constexpr (STEP == 1) return dpp<0xB1>(v);
+  else if constexpr (STEP == 2) return dpp<0x4E>(v);
+  else if constexpr (STEP == 4) return dpp<0x141>(v);
+  else if constexpr (STEP == 8) return dpp<0x140>(v);
+  else return __shfl_xor(v, STEP, 64);
+}
+
+// Maximum and sum over the G lanes of a token, the same value in all of them. (The mirrors pair
+// lanes of halves that already agree, and a + b = b + a, so every lane forms the same sum.)
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, partner<1>(v));
+  v = fmaxf(v, partner<2>(v));
+  v = fmaxf(v, partner<4>(v));
+  if constexpr (G > 8) v = fmaxf(v, partner<8>(v));
+  if constexpr (G > 16) v = fmaxf(v, partner<16>(v));
+  if constexpr (G > 32) v = fmaxf(v, partner<32>(v));
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  v += partner<1>(v);
+  v += partner<2>(v);
+  v += partner<4>(v);
+  if constexpr (G > 8) v += partner<8>(v);
+  if constexpr (G > 16) v += partner<16>(v);
+  if constexpr (G > 32) v += partner<32>(v);
+  return v;
+}
+
+// This lane's V logits of row t, -inf past E. `wide`: rows start on 16 bytes and E is a whole
+// number of 16-byte chunks.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* x, int64_t t, int E, int e0, bool wide, float (&v)[V]) {
+  const T* row = x + t * E;
+  constexpr int kChunk = 16 / sizeof(T);
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < V / kChunk; ++c) {
+      if (e0 + c * kChunk < E) {
+        const u32x4 r = *reinterpret_cast<const u32x4*>(row + e0 + c * kChunk);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (sizeof(T) == 2) {
+            v[c * 8 + 2 * q] = bf16_bits_to_f32(r[q] & 0xFFFFu);
+            v[c * 8 + 2 * q + 1] = bf16_bits_to_f32(r[q] >> 16);
+          } else {
+            v[c * 4 + q] = __uint_as_float(r[q]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) v[c * kChunk + i] = neg_inf();
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = neg_inf();
+      if (e0 + i < E) {
+        if constexpr (sizeof(T) == 2) v[i] = bf16_bits_to_f32(row[e0 + i]);
+        else v[i] = row[e0 + i];
+      }
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* x, int64_t t, int E, int e0, bool wide, const float (&v)[V]) {
+  T* row = x + t * E;
+  constexpr int kChunk = 16 / sizeof(T);
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < V / kChunk; ++c) {
+      if (e0 + c * kChunk < E) {
+        u32x4 r;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (sizeof(T) == 2) r[q] = pack_bf16x2(v[c * 8 + 2 * q], v[c * 8 + 2 * q + 1]);
+          else r[q] = __builtin_bit_cast(uint32_t, v[c * 4 + q]);
+        }
+        *reinterpret_cast<u32x4*>(row + e0 + c * kChunk) = r;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) {
+        if constexpr (sizeof(T) == 2) row[e0 + i] = f32_to_bf16_bits(v[i]);
+        else row[e0 + i] = v[i];
+      }
+  }
+}
+
+// exp(x_i - m) of this lane's logits and their sum over the row. A row of -inf alone has m = -inf;
+// it is shifted by 0 instead, so that its exponentials and sum are 0 and its lse -inf.
+template <int G, int V>
+__device__ __forceinline__ float row_exponentials(const float (&v)[V], float& m0, float (&e)[V]) {
+  float m = neg_inf();
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);  // a NaN never wins here; it reaches the sum below
+  m = group_max<G>(m);
+  m0 = m == neg_inf() ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    e[i] = expf(v[i] - m0);
+    s += e[i];
+  }
+  return group_sum<G>(s);
+}
+
+struct RouterArgs {
+  const void* logits;
+  int64_t T;
+  int E, k;
+  bool renormalize, wide;
+  int32_t* ids;
+  float* w;
+  float* lse;
+  uint32_t* partial;  // losses only: per workgroup E column sums, E counts, the sum of lse^2, the tokens
+};
+
+// Words of a workgroup's partial sums.
+__host__ __device__ constexpr int64_t partial_words(int E) { return 2 * (int64_t)E + 2; }
+
+template <typename T, int G, int V, bool LOSSES>
+__global__ __launch_bounds__(kThreads) void router_topk_kernel(RouterArgs a) {
+  constexpr int kGroups = kThreads / G;  // tokens a workgroup holds at once
+  constexpr int kSlots = MOE_ROUTER_MAX_TOPK;
+  __shared__ float sel_part[kGroups][kSlots];
+  __shared__ int sel_id[kGroups][kSlots];
+  __shared__ int hist[LOSSES ? G * V : 1];
+  __shared__ float colsum[LOSSES ? kGroups * G * V : 1];
+  __shared__ float zsum_s[LOSSES ? kGroups : 1];
+  __shared__ int tokens_s[LOSSES ? kGroups : 1];
+  const int tid = threadIdx.x, group = tid / G, g = tid % G, lane = tid & 63;
+  const int first_lane = lane - g;  // of the group, inside its wave
+  const int e0 = g * V;
+  float col[V];
+  float zsum = 0.f;
+  int tokens = 0;
+  if constexpr (LOSSES) {
+    for (int e = tid; e < G * V; e += kThreads) hist[e] = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) col[i] = 0.f;
+    __syncthreads();
+  }
+  for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < a.T; t += (int64_t)gridDim.x * kGroups) {
+    float v[V], ex[V];
+    load_row<T, V>(static_cast<const T*>(a.logits), t, a.E, e0, a.wide, v);
+    float m0;
+    const float s = row_exponentials<G, V>(v, m0, ex);
+    const float lse = m0 + logf(s);
+    if (g == 0) a.lse[t] = lse;
+    if constexpr (LOSSES) {
+      if (s != 0.f) {  // NaN rows count and carry their NaN
+        const float inv = 1.f / s;
+#pragma unroll
+        for (int i = 0; i < V; ++i) col[i] += ex[i] * inv;
+        if (g == 0) {
+          zsum += lse * lse;
+          ++tokens;
+        }
+      }
+    }
+    // k rounds of: the row's largest remaining logit, the lowest lane that holds it, its lowest index there
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = v[i] == v[i] ? v[i] : neg_inf();  // a NaN is never chosen
+    float chosen = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      float best = neg_inf();
+#pragma unroll
+      for (int i = 0; i < V; ++i) best = fmaxf(best, v[i]);
+      const float top = group_max<G>(best);
+      uint64_t have = __ballot(best == top) >> first_lane;
+      if constexpr (G < 64) have &= (1ull << G) - 1;
+      const int leader = __ffsll((long long)have) - 1;
+      const bool none = top == neg_inf();
+      const float part = none ? 0.f : expf(top - m0);
+      chosen += part;
+      if (g == leader) {
+        int at = -1;
+        bool found = none;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const bool hit = !found && v[i] == top;
+          at = hit ? e0 + i : at;
+          v[i] = hit ? neg_inf() : v[i];
+          found |= hit;
+        }
+        sel_id[group][j] = at;
+        sel_part[group][j] = part;
+        if constexpr (LOSSES) {
+          if (at >= 0) atomicAdd(&hist[at], 1);  // LDS integer atomics: order-free
+        }
+      }
+    }
+    // the group's lanes are of one wave: its LDS writes above are complete once waited for
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_wave_barrier();
+    float denom = a.renormalize ? chosen : s;
+    denom = s == s ? denom : s;
+    for (int j = g; j < a.k; j += G) {
+      const int id = sel_id[group][j];
+      a.ids[t * a.k + j] = id;
+      a.w[t * a.k + j] = id < 0 ? 0.f : sel_part[group][j] / denom;
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_wave_barrier();
+  }
+  if constexpr (LOSSES) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) colsum[group * (G * V) + e0 + i] = col[i];
+    if (g == 0) {
+      zsum_s[group] = zsum;
+      tokens_s[group] = tokens;
+    }
+    __syncthreads();
+    uint32_t* out = a.partial + blockIdx.x * partial_words(a.E);
+    for (int e = tid; e < a.E; e += kThreads) {
+      float sum = 0.f;
+      for (int q = 0; q < kGroups; ++q) sum += colsum[q * (G * V) + e];
+      out[e] = __builtin_bit_cast(uint32_t, sum);
+      out[a.E + e] = (uint32_t)hist[e];
+    }
+    if (tid == 0) {
+      float z = 0.f;
+      int n = 0;
+      for (int q = 0; q < kGroups; ++q) {
+        z += zsum_s[q];
+        n += tokens_s[q];
+      }
+      out[2 * a.E] = __builtin_bit_cast(uint32_t, z);
+      out[2 * a.E + 1] = (uint32_t)n;
+    }
+  }
+}
+
+// The workgroups' partial sums to counts, tokens, P and the two losses: one workgroup. 1024 threads
+// hold (column, slice) pairs; a slice adds every R-th partial in order, then a column's R slice sums
+// are added in order, so the result does not depend on scheduling.
+constexpr int kFinishThreads = 1024;
+
+__global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uint32_t* __restrict__ partial, int blocks,
+                                                                       int E, int32_t* __restrict__ counts,
+                                                                       int32_t* __restrict__ tokens,
+                                                                       float* __restrict__ prob_mean,
+                                                                       float* __restrict__ losses) {
+  __shared__ float fsum[kFinishThreads];
+  __shared__ int csum[kFinishThreads];
+  __shared__ float wave_f[kFinishThreads / 64];
+  __shared__ int wave_i[kFinishThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t words = partial_words(E);
+  // the tokens and the sum of lse^2 over the partials
+  float z = 0.f;
+  int n = 0;
+  for (int b = tid; b < blocks; b += kFinishThreads) {
+    z += __builtin_bit_cast(float, partial[b * words + 2 * E]);
+    n += (int)partial[b * words + 2 * E + 1];
+  }
+  const int R = kFinishThreads / E;  // slices (E <= 1024)
+  const int col = tid % E, slice = tid / E;
+  float f = 0.f;
+  int c = 0;
+  if (slice < R) {
+    for (int b = slice; b < blocks; b += R) {
+      f += __builtin_bit_cast(float, partial[b * words + col]);
+      c += (int)partial[b * words + E + col];
+    }
+  }
+  fsum[tid] = f;
+  csum[tid] = c;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    z += __shfl_xor(z, off, 64);
+    n += __shfl_xor(n, off, 64);
+  }
+  if (lane == 0) {
+    wave_f[wave] = z;
+    wave_i[wave] = n;
+  }
+  __syncthreads();
+  z = 0.f;
+  n = 0;
+  for (int q = 0; q < kFinishThreads / 64; ++q) {
+    z += wave_f[q];
+    n += wave_i[q];
+  }
+  const float nf = (float)(n > 0 ? n : 1);
+  float mean = 0.f;
+  int count = 0;
+  if (tid < E) {
+    for (int q = 0; q < R; ++q) {
+      mean += fsum[q * E + tid];
+      count += csum[q * E + tid];
+    }
+    mean /= nf;
+    counts[tid] = count;
+    prob_mean[tid] = mean;
+  }
+  // sum of counts and of counts_e P_e over the experts
+  float dot = (float)count * mean;
+  int total = count;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    dot += __shfl_xor(dot, off, 64);
+    total += __shfl_xor(total, off, 64);
+  }
+  __syncthreads();
+  if (lane == 0) {
+    wave_f[wave] = dot;
+    wave_i[wave] = total;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    dot = 0.f;
+    total = 0;
+    for (int q = 0; q < kFinishThreads / 64; ++q) {
+      dot += wave_f[q];
+      total += wave_i[q];
+    }
+    tokens[0] = n;
+    losses[0] = (float)E * dot / (float)(total > 0 ? total : 1);
+    losses[1] = z / nf;
+  }
+}
+
+struct RouterBackwardArgs {
+  const void* logits;
+  int64_t T;
+  int E, k;
+  bool renormalize, wide;
+  const int32_t* ids;
+  const float* w;
+  const int32_t* counts;  // null: no gradient of the losses
+  const int32_t* tokens;
+  const float* d_w;       // null: no gradient of the weights
+  const float* d_losses;
+  void* d_logits;
+};
+
+template <typename T, int G, int V>
+__global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterBackwardArgs a) {
+  constexpr int kGroups = kThreads / G;
+  const int tid = threadIdx.x, group = tid / G, g = tid % G;
+  const int e0 = g * V;
+  // c_e = dL0 E f_e / n of this lane's experts, and 2 dL1 / n
+  float c[V], dz = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) c[i] = 0.f;
+  if (a.d_losses != nullptr) {
+    // every lane of a group holds a part of the counts: their sum is the group's
+    int local = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int n = e0 + i < a.E ? a.counts[e0 + i] : 0;
+      c[i] = (float)n;
+      local += n;
+    }
+    int total = local;
+#pragma unroll
+    for (int off = 1; off < G; off <<= 1) total += __shfl_xor(total, off, 64);
+    const int n = a.tokens[0];
+    const float nf = (float)(n > 0 ? n : 1);
+    const float scale = a.d_losses[0] * (float)a.E / ((float)(total > 0 ? total : 1) * nf);
+    dz = 2.f * a.d_losses[1] / nf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] *= scale;
+  }
+  for (int64_t t = (int64_t)blockIdx.x * kGroups + group; t < a.T; t += (int64_t)gridDim.x * kGroups) {
+    float v[V], p[V], d[V];
+    load_row<T, V>(static_cast<const T*>(a.logits), t, a.E, e0, a.wide, v);
+    float m0;
+    const float s = row_exponentials<G, V>(v, m0, p);
+    if (s == 0.f) {  // nothing to choose from: no probability, no gradient
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = 0.f;
+      store_row<T, V>(static_cast<T*>(a.d_logits), t, a.E, e0, a.wide, d);
+      continue;
+    }
+    const float inv = 1.f / s;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] *= inv;
+      dot += c[i] * p[i];
+    }
+    dot = group_sum<G>(dot);
+    float shift = dz * (m0 + logf(s)) - dot;
+    float gw = 0.f;  // sum over the kept slots of g_j w_j
+    if (a.d_w != nullptr) {
+      for (int j = 0; j < a.k; ++j) {
+        const int id = a.ids[t * a.k + j];
+        if ((unsigned)id < (unsigned)a.E) gw += a.d_w[t * a.k + j] * a.w[t * a.k + j];
+      }
+      if (!a.renormalize) shift -= gw;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = p[i] * (c[i] + shift);
+    if (a.d_w != nullptr) {
+      for (int j = 0; j < a.k; ++j) {
+        const int at = a.ids[t * a.k + j] - e0;
+        if ((unsigned)at < (unsigned)V && e0 + at < a.E) {
+          const float grad = a.d_w[t * a.k + j], wj = a.w[t * a.k + j];
+          const float part = a.renormalize ? wj * (grad - gw) : wj * grad;
+#pragma unroll
+          for (int i = 0; i < V; ++i) d[i] += i == at ? part : 0.f;
+        }
+      }
+    }
+    store_row<T, V>(static_cast<T*>(a.d_logits), t, a.E, e0, a.wide, d);
+  }
+}
+
+// Workgroups of a launch over T tokens, kGroups at a time.
+int64_t router_blocks(int64_t T, int groups, int64_t cap) {
+  const int64_t blocks = (T + groups - 1) / groups;
+  return blocks < 1 ? 1 : (blocks > cap ? cap : blocks);
+}
+
+// Lanes per token: 8 experts a lane up to 512 experts, 16 beyond.
+int lanes_of(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
+
+// The losses' first launch leaves one partial a workgroup, which the second reads in one workgroup.
+constexpr int64_t kLossBlocks = 256;
+
+template <typename F>
+hipError_t by_width(int E, F&& f) {
+  if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+  if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+  if (E <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+  if (E <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+}
+
+bool wide_rows(const void* p, int E, bool f32) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && E % (f32 ? 4 : 8) == 0;
+}
+
+}  // namespace
+
+int64_t router_partial_words(int64_t T, int32_t E) {
+  return router_blocks(T, kThreads / lanes_of(E), kLossBlocks) * partial_words(E);
+}
+
+hipError_t launch_router_topk(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
+                              int32_t* ids, float* w, float* lse, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const RouterArgs a{logits, T, E, k, renormalize, wide_rows(logits, E, f32), ids, w, lse, nullptr};
+  const int64_t cap = (int64_t)device_cu_count(current_device()) * 16;
+  return by_width(E, [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    const dim3 grid((unsigned)router_blocks(T, kThreads / G, cap));
+    if (f32) hipLaunchKernelGGL((router_topk_kernel<float, G, V, false>), grid, dim3(kThreads), 0, stream, a);
+    else hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, false>), grid, dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_router_topk_losses(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
+                                     int32_t* ids, float* w, float* lse, int32_t* counts, int32_t* tokens,
+                                     float* prob_mean, float* losses, uint32_t* partial, hipStream_t stream) {
+  const RouterArgs a{logits, T, E, k, renormalize, wide_rows(logits, E, f32), ids, w, lse, partial};
+  const int64_t blocks = router_blocks(T, kThreads / lanes_of(E), kLossBlocks);
+  const hipError_t st = by_width(E, [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    if (f32)
+      hipLaunchKernelGGL((router_topk_kernel<float, G, V, true>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+    else
+      hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, true>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+  });
+  if (st != hipSuccess) return st;
+  hipLaunchKernelGGL(router_losses_kernel, dim3(1), dim3(kFinishThreads), 0, stream, partial, (int)blocks, E, counts,
+                     tokens, prob_mean, losses);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_backward(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
+                                  const int32_t* ids, const float* w, const int32_t* counts, const int32_t* tokens,
+                                  const float* d_w, const float* d_losses, void* d_logits, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const bool wide = wide_rows(logits, E, f32) && wide_rows(d_logits, E, f32);
+  const RouterBackwardArgs a{logits, T, E, k, renormalize, wide, ids, w, counts, tokens, d_w, d_losses, d_logits};
+  const int64_t cap = (int64_t)device_cu_count(current_device()) * 16;
+  return by_width(E, [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    const dim3 grid((unsigned)router_blocks(T, kThreads / G, cap));
+    if (f32) hipLaunchKernelGGL((router_backward_kernel<float, G, V>), grid, dim3(kThreads), 0, stream, a);
+    else hipLaunchKernelGGL((router_backward_kernel<uint16_t, G, V>), grid, dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe
