@@ -269,7 +269,7 @@ template <class C, bool ROUND_U = true, class Args>
 __device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::FM][C::FN], unsigned char* smem, const Args& g,
                                          const TileCoord& tc) {
   constexpr int BM = C::BM, BN = C::BN;
-  const int tid = epilogue_tid<kOpaqueEpilogue<C>>(), lane = tid & 63, wave = tid >> 6;
+  const int tid = epilogue_tid<kOpaqueEpilogue<C> || !ROUND_U>(), lane = tid & 63, wave = tid >> 6;
   const int wm = wave / C::WGN, wn = wave % C::WGN;
   unsigned char* ot = smem;  // [BM][OUTW] bf16
   constexpr int OUT_ROW_BYTES = C::OUTW * 2;
