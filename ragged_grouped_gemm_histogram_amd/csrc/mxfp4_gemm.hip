@@ -202,264 +202,461 @@ __global__ __launch_bounds__(kThinThreads) void mxfp4_thin_kernel(MxGemmArgs g) 
 }
 
 // ---------------------------------------------------------------------------------------------
-// Many rows per expert: the pipelined tiles of the bf16 products. A stage is 256 values of every
-// tile row, 128 bytes as there, four matrix steps of 64; the scale bytes of two stages (16 bytes a
-// row) are loaded into LDS with the even one's values. A lane half takes the stage's chunks 4 half
-// + step, so its four scale bytes are one LDS word and the step picks the byte.
+// Many rows per expert: 256 x 256 tiles on 8 waves, persistent workgroups, direct global -> LDS
+// loads into a ring of four stages. A stage is 128 values of every tile row (64 bytes), two matrix
+// steps of 64; the scale bytes of four stages (16 bytes a row) come with the first one's values. A
+// lane half takes the stage's chunks 2 half + step, so its two scale bytes are neighbours and the
+// step picks the byte.
+//
+// The ring runs on across tiles: while a tile's last stages are multiplied, the next tile's first
+// four are loaded, and the results leave from registers (exchanges between lanes make whole lines)
+// instead of through the ring's memory, so the loads of a new tile have no gap before them.
 // ---------------------------------------------------------------------------------------------
-constexpr int kStageK = 256;
+constexpr int kStageK = 128;
+constexpr int kRing = 4;          // stages in LDS
+constexpr int kGroup = 4;         // stages a row's 16 scale bytes cover
+constexpr int kScaleRing = 3;     // scale groups in LDS: the last two of a tile and the next tile's first
+constexpr int kTableTiles = 64;   // tiles of a workgroup whose coordinates are worked out together
+
+template <int BM_, int BN_, int WGM_, int WGN_, bool GATED_>
+struct MxTile {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
+  static constexpr bool GATED = GATED_;
+  static constexpr int NWAVES = WGM * WGN, THREADS = 64 * NWAVES;
+  static constexpr int WTM = BM / WGM, WTN = BN / WGN;
+  static constexpr int FM = WTM / 32, FN = WTN / 32;
+  static constexpr int OUTW = GATED ? BN / 2 : BN;
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int SCALE_BYTES = (BM + BN) * 16;
+  static constexpr int LDS_BYTES = kRing * STAGE_BYTES + kScaleRing * SCALE_BYTES;
+  static constexpr int A_OPS = BM / 16 / NWAVES, B_OPS = BN / 16 / NWAVES;  // wave loads of 16 rows
+  static constexpr int S_OPS = (BM + BN) / 64 / NWAVES;                     // wave loads of 64 rows' scales
+  static_assert(BM % (16 * NWAVES) == 0 && BN % (16 * NWAVES) == 0 && (BM + BN) % (64 * NWAVES) == 0 && BM % 64 == 0,
+                "loads split evenly over the waves");
+};
+
+struct MxProblems {
+  int mt_prefix[MOE_MAX_EXPERTS + 1];
+  int wave_total[8];
+  int4 table[kTableTiles];  // expert, first row, rows, first column
+};
+
+struct MxCoord {
+  int e, row0, rows_valid, n0;
+};
+
+// Lanes 8..15 of every row of 16 take `b` of the lane 8 below, the others keep a; and lanes 0..7
+// take `a` of the lane 8 above, the others keep b.
+__device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
+  const uint32_t x = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, 0x128 /* row_ror:8 */, 0xf, 0xc, false);
+  b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a, 0x128, 0xf, 0x3, false);
+  a = x;
+}
+
+// Accumulators to bf16 rows. acc[i][j][4 q + s] is row wm * WTM + 32 i + lane % 32, column (block
+// column base + 8 q + 4 (lane / 32) + s). Three exchanges between lanes (halves, 16s, 8s) gather a
+// row's 64 columns from the registers of one lane pair into eight lanes: every store writes 8 rows
+// of 128 consecutive bytes. Rows past the block and columns past N fall outside the buffer resource
+// and are dropped; every wave issues all its stores.
+template <class C>
+constexpr int kTileStores = C::FM * 4 * (C::OUTW / C::WGN / 64);
 
 template <class C>
-constexpr int kScaleBytes = 2 * (C::BM + C::BN) * 16;  // two pairs of stages
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], const MxGemmArgs& g, const MxCoord& tc) {
+  constexpr int kPieces = C::OUTW / C::WGN / 64;  // of 64 columns
+  static_assert(C::OUTW / C::WGN % 64 == 0, "a wave stores whole lines");
+  const int tid = epilogue_tid<true>(), lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / C::WGN, wn = wave % C::WGN;
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      g.out + (int64_t)tc.row0 * g.ldo, (short)0, (int)((int64_t)tc.rows_valid * g.ldo * 2), 0x00020000);
+  const uint32_t row_bytes = (uint32_t)(g.ldo * 2);
+  const uint32_t row = (uint32_t)(wm * C::WTM + (lane & 7)) * row_bytes;
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int64_t col = tc.n0 + (wn * kPieces + p) * 64 + 8 * (lane >> 5) + 16 * ((lane >> 4) & 1) + 32 * ((lane >> 3) & 1);
+    const uint32_t base = col < g.N ? row + (uint32_t)(col * 2) : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      uint32_t v[2][2][4];  // [column block][rows 0-15 / 16-31][16 bytes]
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t pk[4][2];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float f[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if constexpr (C::GATED) f[s] = swiglu(acc[i][2 * p + j][4 * q + s], acc[i][2 * kPieces + 2 * p + j][4 * q + s]);
+            else f[s] = acc[i][2 * p + j][4 * q + s];
+          }
+          pk[q][0] = pack_bf16x2(f[0], f[1]);
+          pk[q][1] = pack_bf16x2(f[2], f[3]);
+        }
+        // halves: a lane holds columns 8 (q + half) .. + 7 of q = 0 (x) and q = 2 (y)
+        uint32_t x[4], y[4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const auto a = __builtin_amdgcn_permlane32_swap(pk[0][w], pk[1][w], false, false);
+          const auto b = __builtin_amdgcn_permlane32_swap(pk[2][w], pk[3][w], false, false);
+          x[w] = a[0]; x[2 + w] = a[1];
+          y[w] = b[0]; y[2 + w] = b[1];
+        }
+        // 16s: x gets rows 0-15 with all 32 columns, y rows 16-31
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const auto a = __builtin_amdgcn_permlane16_swap(x[w], y[w], false, false);
+          v[j][0][w] = a[0];
+          v[j][1][w] = a[1];
+        }
+      }
+      // 8s: the first block's registers get rows 0-7 with all 64 columns, the second's rows 8-15
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) swap8(v[0][h][w], v[1][h][w]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[j][h][0], v[j][h][1], v[j][h][2], v[j][h][3]}, rsrc,
+                                                 base + (uint32_t)(32 * i + 16 * h + 8 * j) * row_bytes, 0, 2 /* nt */);
+      }
+    }
+  }
+}
 
 template <class C, bool KTAIL>
 __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
-  constexpr int BM = C::BM, BN = C::BN, NST = C::NST;
+  constexpr int BM = C::BM, BN = C::BN;
   constexpr int OPS = C::A_OPS + C::B_OPS;
-  constexpr int S_LOADS = (BM + BN) / 64;  // wave loads of a stage pair's scales
-  constexpr int S_OPS = (S_LOADS + C::NWAVES - 1) / C::NWAVES;
-  static_assert(NST >= 2 && NST <= 3 && OPS * (NST - 1) < 64, "ring depth, vmcnt range");
+  constexpr int TILE_N = C::OUTW;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
-  __shared__ ProblemList<C::THREADS> pl;
+  __shared__ MxProblems pl;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / C::WGN, wn = wave % C::WGN;
-  const int wm_u = __builtin_amdgcn_readfirstlane(wm);
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+  const int hh = lane >> 5;
 
-  build_problem_list<BM>(g, pl);
+  // prefix of the experts' row-tile counts, from the offsets clamped to the capacity
+  {
+    constexpr int kPer = MOE_MAX_EXPERTS / C::THREADS;
+    int mt[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      mt[i] = 0;
+      if (e < g.E) {
+        const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
+        mt[i] = hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0;
+      }
+      sum += mt[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int up = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += up;
+    }
+    if (lane == 63) pl.wave_total[wave] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int w = 0; w < wave; ++w) run += pl.wave_total[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      if (e <= g.E) pl.mt_prefix[e] = run;
+      run += mt[i];
+    }
+    if (tid == C::THREADS - 1 && g.E == MOE_MAX_EXPERTS) pl.mt_prefix[g.E] = run;
+    __syncthreads();
+  }
   const int total_mt = pl.mt_prefix[g.E];
-  constexpr int TILE_N = C::GATED ? C::OUTW : BN;
-  const int64_t n_tiles = (g.N + TILE_N - 1) / TILE_N;
+  const int n_tiles = (int)((g.N + TILE_N - 1) / TILE_N);
   const int64_t total_tiles = (int64_t)total_mt * n_tiles;
+  const int64_t t0 = logical_worker();
+  if (t0 >= total_tiles) return;
+  const int64_t my_tiles = (total_tiles - t0 + gridDim.x - 1) / gridDim.x;
+
+  // Coordinates of this workgroup's tiles [from, from + kTableTiles), one a lane of the first wave.
+  // Groups of kGroupM row tiles sweep every column tile before the next group starts, so tiles that
+  // run at the same time share rows and weights.
+  auto fill_table = [&](int64_t from) {
+    if (tid < kTableTiles && from + tid < my_tiles) {
+      const int64_t t = t0 + (from + tid) * gridDim.x;
+      const int64_t span = (int64_t)kGroupM * n_tiles, grp = t / span;
+      const int in_group = (int)(t - grp * span);
+      const int g0 = (int)grp * kGroupM;
+      const int gsize = total_mt - g0 < kGroupM ? total_mt - g0 : kGroupM;
+      const int nt = in_group / gsize, gm = g0 + in_group - nt * gsize;
+      int e = 0, hi_e = g.E;  // largest e with mt_prefix[e] <= gm
+      while (hi_e - e > 1) {
+        const int mid = (e + hi_e) >> 1;
+        if (pl.mt_prefix[mid] <= gm) e = mid; else hi_e = mid;
+      }
+      const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
+      int64_t row0 = lo + (int64_t)(gm - pl.mt_prefix[e]) * BM;
+      int64_t rows = hi - row0 < BM ? hi - row0 : BM;
+      if (row0 < lo || row0 >= hi) row0 = rows = 0;  // offsets that are no running sum can wrap the tile counts
+      pl.table[tid] = int4{e, (int)row0, (int)rows, nt * TILE_N};
+    }
+    __syncthreads();
+  };
+  auto coord = [&](int64_t i) {
+    const int4 v = pl.table[i % kTableTiles];
+    return MxCoord{__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                   __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w)};
+  };
+  fill_table(0);
+
   const int blocks = (int)mx_blocks(g.K);
-  const int nk = (blocks + 7) / 8;
+  // stages: at least four, so that loads run at most one tile ahead (what lies past the row is zeros)
+  const int nk = blocks <= 12 ? kRing : (blocks + 3) / 4;
   const uint32_t qp = (uint32_t)mx_row_bytes(g.K), sp = (uint32_t)mx_scale_bytes(g.K);
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
-  unsigned char* const scale_lds = smem + C::LDS_BYTES;
+  constexpr uint32_t kScaleBase = kRing * C::STAGE_BYTES;
+  static_assert((kScaleBase & (kScaleBase - 1)) == 0, "ring offsets wrap with a mask");
+  const bool gather = g.a_rows != nullptr;
 
-  for (int64_t t = logical_worker(); t < total_tiles; t += gridDim.x) {
-    const TileCoord tc = tile_coord<BM, TILE_N>(t, n_tiles, total_mt, g.E, pl);
-
-    // Sources of each lane's 16-byte chunks, as byte offsets from wave-uniform bases (the host
-    // guarantees that they fit). Rows past the expert's block and columns past N point at valid
-    // ones: they only feed outputs that are never stored. The swizzle picks the chunk a lane fetches.
-    const bool gather = g.a_rows != nullptr;
-    auto a_row = [&](int r) -> uint32_t {  // row of a_q / a_s, from the base below
-      const int rr = r < tc.rows_valid ? r : tc.rows_valid - 1;
-      if (!gather) return (uint32_t)rr;
-      const int32_t slot = g.a_rows[tc.row0 + rr];
-      const uint32_t last = (uint32_t)(g.a_tokens * g.a_k) - 1u;
+  // The tile being loaded: each lane's 16-byte chunks as byte offsets from wave-uniform bases (the
+  // host guarantees that they fit). Rows past the expert's block and columns past N point at valid
+  // ones: they only feed outputs that are never stored. A wave load covers 16 rows of 4 chunks;
+  // chunk c of row r is kept at position c ^ turn(r), which spreads 8 neighbouring rows over 128 bytes
+  // of banks and 16 over 256. A lane's rows are 16 apart or more: one chunk for all.
+  auto turn = [](int r) { return ((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1); };
+  const int chunk = (lane & 3) ^ turn(lane >> 2);
+  uint64_t a_ptr, b_ptr, as_ptr, bs_ptr;  // of the next stage to load, and of the next group of scales
+  int ik;                                 // that stage
+  uint32_t scale_to = 0;                  // where in the scale ring that group goes
+  uint32_t a_off[C::A_OPS], b_off[C::B_OPS], s_off[C::S_OPS];
+  __amdgpu_buffer_rsrc_t a_rsrc, b_rsrc;
+  int32_t slot_a[C::A_OPS], slot_s[C::S_OPS];  // gather: dispatch slots of the next tile's rows
+  auto row_in = [&](const MxCoord& tc, int r) { return max(min(r, tc.rows_valid - 1), 0); };
+  auto fetch_slots = [&](const MxCoord& tc) {
+    const int32_t* rows = g.a_rows + tc.row0;
+#pragma unroll
+    for (int t2 = 0; t2 < C::A_OPS; ++t2) slot_a[t2] = rows[row_in(tc, 16 * (wave + C::NWAVES * t2) + (lane >> 2))];
+#pragma unroll
+    for (int t2 = 0; t2 < C::S_OPS; ++t2) {
+      const int r = 64 * (wave_u + C::NWAVES * t2) + lane;
+      slot_s[t2] = rows[row_in(tc, r < BM ? r : 0)];
+    }
+  };
+  auto set_tile = [&](const MxCoord& tc) {
+    const uint32_t last = (uint32_t)(g.a_tokens * g.a_k) - 1u;
+    auto a_row = [&](int r, int32_t slot) -> uint32_t {
+      if (!gather) return (uint32_t)row_in(tc, r);
       return (slot < 0 ? 0u : min((uint32_t)slot, last)) / (uint32_t)g.a_k;
     };
-    auto b_row = [&](int r) -> uint32_t {  // row of the expert's weights
+    auto b_row = [&](int r) -> uint32_t {
       const int half = C::GATED && r >= BN / 2 ? 1 : 0;
-      int64_t n = tc.n0 + (r - half * (BN / 2));
-      if (n >= g.N) n = tc.n0;
-      return (uint32_t)(n + half * g.N);
+      int n = tc.n0 + (r - half * (BN / 2));
+      if (n >= (int)g.N) n = tc.n0;
+      return (uint32_t)(n + half * (int)g.N);
     };
     const int64_t a_first = gather ? 0 : tc.row0, b_first = (int64_t)tc.e * g.w_rows;
-    const uint64_t a_base = uniform_addr(g.a_q + a_first * qp), b_base = uniform_addr(g.w_q + b_first * qp);
-    const uint64_t as_base = uniform_addr(g.a_s + a_first * sp), bs_base = uniform_addr(g.w_s + b_first * sp);
-    uint32_t a_off[C::A_OPS], b_off[C::B_OPS], s_off[S_OPS];
+    a_ptr = uniform_addr(g.a_q + a_first * qp);
+    b_ptr = uniform_addr(g.w_q + b_first * qp);
+    as_ptr = uniform_addr(g.a_s + a_first * sp);
+    ik = 0;
+    bs_ptr = uniform_addr(g.w_s + b_first * sp);
 #pragma unroll
-    for (int t2 = 0; t2 < C::A_OPS; ++t2) {
-      const int r = 8 * (wave + C::NWAVES * t2) + (lane >> 3);
-      a_off[t2] = a_row(r) * qp + swz(r, lane & 7) * 16;
-    }
+    for (int t2 = 0; t2 < C::A_OPS; ++t2)
+      a_off[t2] = a_row(16 * (wave + C::NWAVES * t2) + (lane >> 2), slot_a[t2]) * qp + chunk * 16;
 #pragma unroll
-    for (int t2 = 0; t2 < C::B_OPS; ++t2) {
-      const int r = 8 * (wave + C::NWAVES * t2) + (lane >> 3);
-      b_off[t2] = b_row(r) * qp + swz(r, lane & 7) * 16;
-    }
+    for (int t2 = 0; t2 < C::B_OPS; ++t2)
+      b_off[t2] = b_row(16 * (wave + C::NWAVES * t2) + (lane >> 2)) * qp + chunk * 16;
 #pragma unroll
-    for (int t2 = 0; t2 < S_OPS; ++t2) {
+    for (int t2 = 0; t2 < C::S_OPS; ++t2) {
       const int r = 64 * (wave_u + C::NWAVES * t2) + lane;
-      s_off[t2] = (r < BM ? a_row(r) : b_row(r - BM)) * sp;
+      s_off[t2] = (r < BM ? a_row(r, slot_s[t2]) : b_row(r - BM)) * sp;
     }
-    // K not a multiple of 256: the last stage's chunks past the row get an offset past the buffer
-    // resource's range and stage zeros. A lane fetches the same chunk of all its rows (they are
-    // multiples of 8 apart with an even number of waves between).
-    static_assert(C::NWAVES % 2 == 0, "rows of a lane are 16 apart or more");
-    const bool in_tail = 8 * (nk - 1) + swz(8 * wave + (lane >> 3), lane & 7) < blocks;
-    __amdgpu_buffer_rsrc_t a_rsrc, b_rsrc;
     if constexpr (KTAIL) {
       const int64_t a_range = gather ? g.a_tokens * qp : (int64_t)tc.rows_valid * qp;
-      a_rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a_base), (short)0, (int)a_range, 0x00020000);
-      b_rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(b_base), (short)0, (int)(g.w_rows * qp), 0x00020000);
+      a_rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a_ptr), (short)0, (int)a_range, 0x00020000);
+      b_rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(b_ptr), (short)0, (int)(g.w_rows * qp), 0x00020000);
     }
-    // Loads of stage kt, the ones with index % parts == part; an even stage's first part also
-    // brings the scales of stages kt and kt + 1, before its values.
-    auto issue_part = [&](int kt, int part, int parts) {
-      const uint32_t sa = lds0 + (uint32_t)((kt % NST) * C::STAGE_BYTES);
-      const uint32_t sb = sa + C::A_BYTES;
-      const uint32_t wave_lds = __builtin_amdgcn_readfirstlane((uint32_t)wave * 1024u);
-      if (part == 0 && (kt & 1) == 0) {
-        const int pair = kt >> 1;
-        const uint32_t sl = lds0 + C::LDS_BYTES + (uint32_t)((pair & 1) * (BM + BN) * 16);
+  };
+  // Part `part` of `parts` of the loads of that stage into the ring at byte `to`; the first part of
+  // a group's first stage also brings the group's scales, the last part moves on to the next stage.
+  const uint32_t wave_lds = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)wave * 1024u);
+  auto issue_part = [&](uint32_t to, int part, int parts) {
+    const uint32_t sa = wave_lds + to, sb = sa + C::A_BYTES;
+    if (part == 0 && (ik & (kGroup - 1)) == 0) {
 #pragma unroll
-        for (int t2 = 0; t2 < S_OPS; ++t2) {
-          const int o = wave_u + C::NWAVES * t2;
-          if (o < S_LOADS)
-            dma16_off((o * 64 < BM ? as_base : bs_base) + (uint64_t)pair * 16, s_off[t2], sl + (uint32_t)o * 1024u);
-        }
+      for (int t2 = 0; t2 < C::S_OPS; ++t2) {
+        const int o = wave_u + C::NWAVES * t2;
+        dma16_off(o * 64 < BM ? as_ptr : bs_ptr, s_off[t2], lds0 + kScaleBase + scale_to + (uint32_t)o * 1024u);
       }
-      if constexpr (KTAIL) {
-        const bool last = kt == nk - 1;
-        const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)kt * 128u);
+      as_ptr += 16;
+      bs_ptr += 16;
+      scale_to = scale_to == 2 * C::SCALE_BYTES ? 0 : scale_to + C::SCALE_BYTES;
+    }
+    if constexpr (KTAIL) {
+      // chunks past the row get an offset past the buffer resource's range and stage zeros
+      const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)ik * 64u);
+      const bool in = chunk < blocks - 4 * ik;
 #pragma unroll
-        for (int t2 = 0; t2 < C::A_OPS; ++t2)
-          if (t2 % parts == part)
-            dma16_buf(a_rsrc, last && !in_tail ? 0x80000000u : a_off[t2], soff, sa + wave_lds + (uint32_t)(C::NWAVES * t2 * 1024));
+      for (int t2 = 0; t2 < C::A_OPS; ++t2)
+        if (t2 % parts == part)
+          dma16_buf(a_rsrc, in ? a_off[t2] : 0x80000000u, soff, sa + (uint32_t)(C::NWAVES * t2 * 1024));
 #pragma unroll
-        for (int t2 = 0; t2 < C::B_OPS; ++t2)
-          if (t2 % parts == part)
-            dma16_buf(b_rsrc, last && !in_tail ? 0x80000000u : b_off[t2], soff, sb + wave_lds + (uint32_t)(C::NWAVES * t2 * 1024));
-      } else {
-        const uint64_t step = (uint64_t)kt * 128;
+      for (int t2 = 0; t2 < C::B_OPS; ++t2)
+        if ((C::A_OPS + t2) % parts == part)
+          dma16_buf(b_rsrc, in ? b_off[t2] : 0x80000000u, soff, sb + (uint32_t)(C::NWAVES * t2 * 1024));
+    } else {
 #pragma unroll
-        for (int t2 = 0; t2 < C::A_OPS; ++t2)
-          if (t2 % parts == part) dma16_off(a_base + step, a_off[t2], sa + wave_lds + (uint32_t)(C::NWAVES * t2 * 1024));
+      for (int t2 = 0; t2 < C::A_OPS; ++t2)
+        if (t2 % parts == part) dma16_off(a_ptr, a_off[t2], sa + (uint32_t)(C::NWAVES * t2 * 1024));
 #pragma unroll
-        for (int t2 = 0; t2 < C::B_OPS; ++t2)
-          if (t2 % parts == part) dma16_off(b_base + step, b_off[t2], sb + wave_lds + (uint32_t)(C::NWAVES * t2 * 1024));
+      for (int t2 = 0; t2 < C::B_OPS; ++t2)
+        if ((C::A_OPS + t2) % parts == part) dma16_off(b_ptr, b_off[t2], sb + (uint32_t)(C::NWAVES * t2 * 1024));
+    }
+    if (part == parts - 1) {
+      ++ik;
+      if constexpr (!KTAIL) {
+        a_ptr += 64;
+        b_ptr += 64;
       }
-    };
-    auto issue = [&](int kt) { issue_part(kt, 0, 1); };
+    }
+  };
 
-    f32x16 acc[C::FM][C::FN];
+  f32x16 acc[C::FM][C::FN];
+  u32x4 af[2][C::FM], bfr[2][C::FN];                         // fragments of a step: the one in use and the next
+  uint32_t as[C::FM], bs[C::FN], as_next[C::FM], bs_next[C::FN];  // scale bytes of a stage, likewise (next: its words)
+  // LDS addresses: the rows of a lane's fragments are multiples of 32 apart, so a lane needs one
+  // address an operand (`turn` is the same for all), the rest are constant offsets.
+  const int lrow = lane & 31;
+  const int a_row0 = wm * C::WTM + lrow;
+  const int b_row0 = wn * (C::GATED ? BN / 2 / C::WGN : C::WTN) + lrow;
+  constexpr auto b_block = [](int j) { return C::GATED ? j / (C::FN / 2) * (BN / 2) + j % (C::FN / 2) * 32 : j * 32; };
+  const uint32_t a_at = (uint32_t)(a_row0 * 64 + ((2 * hh) ^ turn(lrow)) * 16);
+  const uint32_t b_at = (uint32_t)(C::A_BYTES + b_row0 * 64 + ((2 * hh) ^ turn(lrow)) * 16);
+  const uint32_t as_at = kScaleBase + (uint32_t)(a_row0 * 16), bs_at = kScaleBase + (uint32_t)((BM + b_row0) * 16);
+  auto load_frags = [&](int set, uint32_t at_byte, int ks) {
+    const unsigned char* at = smem + ((a_at ^ (uint32_t)(ks * 16)) + at_byte);  // the step is the chunk's lowest bit
+    const unsigned char* bt = smem + ((b_at ^ (uint32_t)(ks * 16)) + at_byte);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) af[set][i] = *reinterpret_cast<const u32x4*>(at + i * 32 * 64);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) bfr[set][j] = *reinterpret_cast<const u32x4*>(bt + b_block(j) * 64);
+  };
+  auto load_scales = [&](uint32_t at_byte) {
+    const unsigned char* at = smem + (as_at + at_byte);
+    const unsigned char* bt = smem + (bs_at + at_byte);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) as_next[i] = *reinterpret_cast<const uint32_t*>(at + i * 32 * 16);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) bs_next[j] = *reinterpret_cast<const uint32_t*>(bt + b_block(j) * 16);
+  };
+  // The same reads for a next stage's first step, one at a time.
+  auto read_next = [&](int q, uint32_t frag_byte, uint32_t scale_byte) {
+    if (q < C::FM) af[0][q] = *reinterpret_cast<const u32x4*>(smem + (a_at + frag_byte) + q * 32 * 64);
+    else if ((q -= C::FM) < C::FN) bfr[0][q] = *reinterpret_cast<const u32x4*>(smem + (b_at + frag_byte) + b_block(q) * 64);
+    else if ((q -= C::FN) < C::FM) as_next[q] = *reinterpret_cast<const uint32_t*>(smem + (as_at + scale_byte) + q * 32 * 16);
+    else if ((q -= C::FM) < C::FN) bs_next[q] = *reinterpret_cast<const uint32_t*>(smem + (bs_at + scale_byte) + b_block(q) * 16);
+  };
+  // This lane half's two bytes to the low half. Bytes past the row's last block may hold anything (255
+  // is a NaN): their values are staged as zeros, so a scale of 2^-127 keeps them zero.
+  auto take_scales = [&](int kt) {
+    uint32_t keep = 0xFFFFu;
+    if constexpr (KTAIL) {
+      const int left = blocks - 4 * kt - 2 * hh;
+      keep = left >= 2 ? keep : (left <= 0 ? 0u : 0xFFu);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) as[i] = KTAIL ? (as_next[i] >> (16 * hh)) & keep : as_next[i] >> (16 * hh);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) bs[j] = KTAIL ? (bs_next[j] >> (16 * hh)) & keep : bs_next[j] >> (16 * hh);
+  };
+  constexpr int kProducts = C::FM * C::FN, kReads = 2, kReadProducts = (2 * (C::FM + C::FN) + kReads - 1) / kReads;
+  static_assert(kReadProducts <= kProducts && OPS <= kProducts, "the reads and the loads fit between the products");
+  auto product = [&](int set, auto ks_c, int m) {
+    constexpr int ks = decltype(ks_c)::value;
+    const int j = m / C::FM, i = m % C::FM;
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(bfr[set][j]), fp4_operand(af[set][i]),
+                                                                acc[i][j], 4, 4, ks, (int)bs[j], ks, (int)as[i]);
+  };
+  constexpr std::integral_constant<int, 0> zero{};
+  constexpr std::integral_constant<int, 1> one{};
+
+  MxCoord tc = coord(0);
+  if (gather) fetch_slots(tc);
+  set_tile(tc);
+#pragma unroll
+  for (int q = 0; q < kRing; ++q) issue_part(q * C::STAGE_BYTES, 0, 1);
+  wait_vmcnt_lds<0, true>();
+  bare_barrier();
+  uint32_t ring = 0;      // where in the ring the stage being multiplied is
+  uint32_t scale_at = 0;  // and its scales' words
+  load_scales(0);
+  load_frags(0, 0, 0);
+  take_scales(0);
+  for (int64_t i_tile = 0;; ++i_tile) {
+    const bool more = i_tile + 1 < my_tiles;
+    MxCoord next = tc;  // behind the last tile its own first stages are loaded once more, for no use
+    if (more) {
+      if ((i_tile + 1) % kTableTiles == 0) {
+        __syncthreads();  // every wave has read the last entry
+        fill_table(i_tile + 1);
+      }
+      next = coord(i_tile + 1);
+      if (gather) fetch_slots(next);
+    }
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
-    u32x4 af[2][C::FM], bfr[2][C::FN];  // fragments of a step: the one in use and the next
-    int as[C::FM], bs[C::FN], as_next[C::FM], bs_next[C::FN];  // scale words of a stage, likewise
-    auto load_frags = [&](int set, int slot, int ks) {
-      const unsigned char* at = smem + slot * C::STAGE_BYTES;
-      const unsigned char* bt = at + C::A_BYTES;
-      const int chunk = 4 * (lane >> 5) + ks;
+    for (int kt = 0; kt < nk; ++kt) {
+      load_frags(1, ring, 1);
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i) {
-        const int r = wm * C::WTM + i * 32 + (lane & 31);
-        af[set][i] = *reinterpret_cast<const u32x4*>(at + r * 128 + swz(r, chunk) * 16);
-      }
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const int r = b_block_row<C>(wn, j) + (lane & 31);
-        bfr[set][j] = *reinterpret_cast<const u32x4*>(bt + r * 128 + swz(r, chunk) * 16);
-      }
-    };
-    auto load_scales = [&](int kt) {
-      const unsigned char* st = scale_lds + ((kt >> 1) & 1) * (BM + BN) * 16 + (kt & 1) * 8 + (lane >> 5) * 4;
-      // bytes past the row's last block may hold anything (255 is a NaN): their values are staged as
-      // zeros, so a scale of 2^-127 keeps them zero
-      uint32_t keep = 0xFFFFFFFFu;
-      if constexpr (KTAIL) {
-        const int left = blocks - 8 * kt - 4 * (lane >> 5);
-        keep = left >= 4 ? keep : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
-      }
-#pragma unroll
-      for (int i = 0; i < C::FM; ++i)
-        as_next[i] = (int)(*reinterpret_cast<const uint32_t*>(st + (wm * C::WTM + i * 32 + (lane & 31)) * 16) & keep);
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-        bs_next[j] = (int)(*reinterpret_cast<const uint32_t*>(st + (BM + b_block_row<C>(wn, j) + (lane & 31)) * 16) & keep);
-    };
-    auto take_scales = [&] {
-#pragma unroll
-      for (int i = 0; i < C::FM; ++i) as[i] = as_next[i];
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) bs[j] = bs_next[j];
-    };
-    auto mfmas = [&](int set, auto ks_c) {
-      constexpr int ks = decltype(ks_c)::value;
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(bfr[set][j]), fp4_operand(af[set][i]),
-                                                                      acc[i][j], 4, 4, ks, bs[j], ks, as[i]);
-    };
-    // Stage kt is complete for this wave once at most the later stages' values are in flight; after
-    // the barrier it is complete for every wave, and every wave has read the stage before it.
-    auto wait_stage = [&](int kt) {
-      const int ahead = min(nk - 1, kt + NST - 2) - kt;
-      if (NST >= 3 && ahead >= 1) wait_vmcnt_lds<(NST >= 3 ? 1 : 0) * OPS, true>();
-      else wait_vmcnt_lds<0, true>();
+      for (int m = 0; m < kProducts; ++m) product(0, zero, m);
+      interleave_reads<kProducts, C::FM + C::FN>();
+      // The second step's fragments are in registers before its products: the stage is handed over
+      // first, so that they cover the barrier and the next fragments' latency. After the wait and
+      // the barrier the next stage is complete for every wave and this one read by every wave: its
+      // place takes the stage four on, loaded between the products (a wave waiting to issue a load
+      // leaves the matrix unit to the other wave of its SIMD). Still under way may be the two stages
+      // after the next, and for a tile's first three stages the previous tile's stores, issued behind
+      // this tile's first four (before the first tile there are none, and its four are waited for
+      // above).
+      if (kt < 3) wait_vmcnt_lds<2 * OPS + kTileStores<C>, true>();
+      else wait_vmcnt_lds<2 * OPS, true>();
       bare_barrier();
-    };
-    // tile start: every slot is free (the epilogue ended on a barrier)
-    if constexpr (NST == 2) {
-      issue(0);
-      if (nk > 1) {
-        issue(1);
-        wait_vmcnt_lds<OPS, true>();
-      } else {
-        wait_vmcnt_lds<0, true>();
-      }
-      bare_barrier();
-    } else {
+      const uint32_t to = ring;
+      ring = (ring + C::STAGE_BYTES) & (kScaleBase - 1);
+      // the row's next word of scales, or the next group's first (a tile starts one)
+      const bool last = kt + 1 == nk;
+      if (last || (kt & 3) == 3) scale_at = (scale_at & ~15u) == 2 * C::SCALE_BYTES ? 0 : (scale_at & ~15u) + C::SCALE_BYTES;
+      else scale_at += 4;
+      if (kt == nk - kRing) set_tile(next);
+      // between the second step's products: first the next stage's LDS reads, then the loads
 #pragma unroll
-      for (int s2 = 0; s2 < NST - 1; ++s2)
-        if (s2 < nk) issue(s2);
-      wait_stage(0);
-    }
-    if (wm_u * C::WTM >= tc.rows_valid) {
-      // every row of this wave lies past the expert's block: its share of the loads and barriers only
-      for (int kt = 0; kt + 1 < nk; ++kt) {
-        if constexpr (NST >= 3) {
-          if (kt + NST - 1 < nk) issue(kt + NST - 1);
+      for (int m = 0; m < kProducts; ++m) {
+        product(1, one, m);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m < kReadProducts) {
+#pragma unroll
+          for (int q = m * kReads; q < (m + 1) * kReads; ++q) read_next(q, ring, scale_at);
         }
-        wait_stage(kt + 1);
-        if constexpr (NST == 2) {
-          if (kt + 2 < nk) issue(kt + 2);
-        }
+        if (m >= kProducts - OPS) issue_part(to, m - (kProducts - OPS), OPS);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
-      load_scales(0);
-      load_frags(0, 0, 0);
-      take_scales();
-      auto stage = [&](int kt, auto last_c) {
-        const int slot = kt % NST;
-        if constexpr (NST >= 3) {
-          if (kt + NST - 1 < nk) issue(kt + NST - 1);
-        }
-        load_frags(1, slot, 1);
-        mfmas(0, std::integral_constant<int, 0>{});
-        interleave_reads<C::FM * C::FN, C::FM + C::FN>();
-        load_frags(0, slot, 2);
-        mfmas(1, std::integral_constant<int, 1>{});
-        interleave_reads<C::FM * C::FN, C::FM + C::FN>();
-        load_frags(1, slot, 3);
-        mfmas(0, std::integral_constant<int, 2>{});
-        interleave_reads<C::FM * C::FN, C::FM + C::FN>();
-        if constexpr (!decltype(last_c)::value) {
-          wait_stage(kt + 1);
-          if constexpr (NST == 2) {
-            if (kt + 2 < nk) issue(kt + 2);
-          }
-          load_scales(kt + 1);
-          load_frags(0, (kt + 1) % NST, 0);
-        }
-        mfmas(1, std::integral_constant<int, 3>{});
-        if constexpr (!decltype(last_c)::value) take_scales();
-      };
-      for (int kt = 0; kt + 1 < nk; ++kt) stage(kt, std::false_type{});
-      stage(nk - 1, std::true_type{});
+      take_scales(last ? 0 : kt + 1);
     }
-    lds_barrier();  // every wave is done with the ring before the epilogue reuses it
-    epilogue<C, false>(acc, smem, g, tc);
+    store_tile<C>(acc, g, tc);
+    asm volatile("" : : : "memory");  // the stores stay here: the waits above count them
+    if (!more) break;
+    tc = next;
   }
+  wait_vmcnt_lds<0, true>();  // no load may reach LDS after the workgroup has left it
 }
 
 template <class C, bool KTAIL>
 hipError_t launch_pipe(const MxGemmArgs& g, hipStream_t stream) {
   static std::atomic<bool> done[64] = {};
   auto kern = mxfp4_pipe_kernel<C, KTAIL>;
-  constexpr int lds = C::LDS_BYTES + kScaleBytes<C>;
+  constexpr int lds = C::LDS_BYTES;
   const int dev = current_device();
   // Setting the attribute twice in a race of first calls is harmless.
   if (dev >= 0 && dev < 64 && !done[dev].load(std::memory_order_acquire)) {
@@ -468,14 +665,13 @@ hipError_t launch_pipe(const MxGemmArgs& g, hipStream_t stream) {
     if (st != hipSuccess) return st;
     done[dev].store(true, std::memory_order_release);
   }
-  constexpr int per_cu = 160 * 1024 / (lds + (int)sizeof(ProblemList<C::THREADS>));
-  static_assert(per_cu >= 1, "the ring, the scales and the problem list must fit in LDS");
-  hipLaunchKernelGGL(kern, dim3(device_cu_count(dev) * per_cu), dim3(C::THREADS), lds, stream, g);
+  static_assert(lds + sizeof(MxProblems) <= 160 * 1024, "the ring, the scales and the problem list fit in LDS");
+  hipLaunchKernelGGL(kern, dim3(device_cu_count(dev)), dim3(C::THREADS), lds, stream, g);
   return hipGetLastError();
 }
 
 template <bool GATED>
-using MxBig = std::conditional_t<GATED, Tile<256, 256, 4, 2, 2, true>, Tile<256, 256, 2, 4, 2, false>>;
+using MxBig = std::conditional_t<GATED, MxTile<256, 256, 4, 2, true>, MxTile<256, 256, 2, 4, false>>;
 
 template <bool GATED>
 hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
@@ -487,7 +683,7 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   const int64_t a_span = (g.a_rows != nullptr ? g.a_tokens : 256) * qp;
   const bool fits = a_span <= 0x7FFFFFFFll && g.w_rows * qp <= 0x7FFFFFFFll;
   if (fits && g.cap_rows >= (int64_t)64 * g.E) {
-    if (g.K % kStageK != 0) return launch_pipe<MxBig<GATED>, true>(g, stream);
+    if (g.K % kStageK != 0 || g.K < kRing * kStageK) return launch_pipe<MxBig<GATED>, true>(g, stream);
     return launch_pipe<MxBig<GATED>, false>(g, stream);
   }
   hipLaunchKernelGGL(mxfp4_thin_kernel<GATED>, dim3(cus * 4), dim3(kThinThreads), 0, stream, g);
