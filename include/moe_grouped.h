@@ -372,7 +372,8 @@ size_t moe_router_workspace_bytes(int64_t T, int32_t E);
  *   tokens     int32 [1]  out: n
  *   prob_mean  fp32  [E]  out: P
  *   losses     fp32  [2]  out (both 0 when n = 0)
- *   workspace  device scratch of at least moe_router_workspace_bytes(T, E)
+ *   workspace  device scratch of at least moe_router_workspace_bytes(T, E),
+ *              16-byte aligned
  *
  * Two launches; sums are taken in a fixed order, so results repeat bit for bit. */
 moe_status moe_router_topk_losses(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
@@ -386,7 +387,8 @@ moe_status moe_router_topk_losses(const void* logits, int32_t dtype, int64_t T, 
  * f constant (counts have no gradient).
  *
  *   expert_ids, routing_w  as the forward gave them; ids outside [0, E) carry
- *                          no gradient, whatever d_routing_w holds there
+ *                          no gradient, whatever d_routing_w holds there (the
+ *                          slots of an expert chosen twice are added up)
  *   counts, tokens         as moe_router_topk_losses gave them, or summed over
  *                          several ranks for losses over a global batch
  *   d_logits               [T, E] out, the logits' type; 0 for a row of -inf alone */

@@ -373,7 +373,7 @@ moe_status moe_router_topk_losses(const void* logits, int32_t dtype, int64_t T, 
     return MOE_ERR_NULL_POINTER;
   if (misaligned(logits, logit_bytes(dtype)) || misaligned(expert_ids, 4) || misaligned(routing_w, 4) ||
       misaligned(lse, 4) || misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(prob_mean, 4) ||
-      misaligned(losses, 4) || misaligned(workspace, 4))
+      misaligned(losses, 4) || misaligned(workspace, 16))
     return MOE_ERR_MISALIGNED;
   if (workspace_bytes < moe_router_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
   if ((st = check_device()) != MOE_OK) return st;

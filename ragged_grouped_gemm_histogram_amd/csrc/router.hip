@@ -26,7 +26,10 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kPlainThreads = 256;
+// With the losses a workgroup leaves one partial sum per column: 8 waves, and at most two such
+// workgroups a CU, so that they fill the device and the second launch has few partials to add.
+constexpr int kLossThreads = 512;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -163,11 +166,12 @@ struct RouterArgs {
   uint32_t* partial;  // losses only: per workgroup E column sums, E counts, the sum of lse^2, the tokens
 };
 
-// Words of a workgroup's partial sums.
-__host__ __device__ constexpr int64_t partial_words(int E) { return 2 * (int64_t)E + 2; }
+// Words of a workgroup's partial sums, padded to whole 16 bytes.
+__host__ __device__ constexpr int64_t partial_words(int E) { return (2 * (int64_t)E + 2 + 3) / 4 * 4; }
 
 template <typename T, int G, int V, bool LOSSES>
-__global__ __launch_bounds__(kThreads) void router_topk_kernel(RouterArgs a) {
+__global__ __launch_bounds__(LOSSES ? kLossThreads : kPlainThreads) void router_topk_kernel(RouterArgs a) {
+  constexpr int kThreads = LOSSES ? kLossThreads : kPlainThreads;
   constexpr int kGroups = kThreads / G;  // tokens a workgroup holds at once
   constexpr int kSlots = MOE_ROUTER_MAX_TOPK;
   __shared__ float sel_part[kGroups][kSlots];
@@ -275,13 +279,14 @@ __global__ __launch_bounds__(kThreads) void router_topk_kernel(RouterArgs a) {
       }
       out[2 * a.E] = __builtin_bit_cast(uint32_t, z);
       out[2 * a.E + 1] = (uint32_t)n;
+      for (int w = 2 * a.E + 2; w < (int)partial_words(a.E); ++w) out[w] = 0u;
     }
   }
 }
 
-// The workgroups' partial sums to counts, tokens, P and the two losses: one workgroup. 1024 threads
-// hold (column, slice) pairs; a slice adds every R-th partial in order, then a column's R slice sums
-// are added in order, so the result does not depend on scheduling.
+// The workgroups' partial sums to counts, tokens, P and the two losses: one workgroup. A thread adds
+// four neighbouring words (16-byte loads, eight in flight) of every R-th partial in order, then a
+// word's R slice sums are added in order, so the result does not depend on scheduling.
 constexpr int kFinishThreads = 1024;
 
 __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uint32_t* __restrict__ partial, int blocks,
@@ -289,56 +294,56 @@ __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uin
                                                                        int32_t* __restrict__ tokens,
                                                                        float* __restrict__ prob_mean,
                                                                        float* __restrict__ losses) {
-  __shared__ float fsum[kFinishThreads];
-  __shared__ int csum[kFinishThreads];
+  __shared__ u32x4 slice_sum[kFinishThreads];
   __shared__ float wave_f[kFinishThreads / 64];
   __shared__ int wave_i[kFinishThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t words = partial_words(E);
-  // the tokens and the sum of lse^2 over the partials
-  float z = 0.f;
-  int n = 0;
-  for (int b = tid; b < blocks; b += kFinishThreads) {
-    z += __builtin_bit_cast(float, partial[b * words + 2 * E]);
-    n += (int)partial[b * words + 2 * E + 1];
-  }
-  const int R = kFinishThreads / E;  // slices (E <= 1024)
-  const int col = tid % E, slice = tid / E;
-  float f = 0.f;
-  int c = 0;
+  const int quads = (int)(partial_words(E) / 4);
+  const int R = kFinishThreads / quads;  // slices (quads <= 513)
+  const int quad = tid % quads, slice = tid / quads;
+  const u32x4* src = reinterpret_cast<const u32x4*>(partial);
+  auto is_float = [&](int w) { return w < E || w == 2 * E; };  // P sums and the sum of lse^2; else counts and tokens
+  float f[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t c[4] = {0u, 0u, 0u, 0u};
   if (slice < R) {
-    for (int b = slice; b < blocks; b += R) {
-      f += __builtin_bit_cast(float, partial[b * words + col]);
-      c += (int)partial[b * words + E + col];
-    }
-  }
-  fsum[tid] = f;
-  csum[tid] = c;
+    constexpr int kBatch = 8;
+    for (int b0 = slice; b0 < blocks; b0 += R * kBatch) {
+      u32x4 v[kBatch];
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    z += __shfl_xor(z, off, 64);
-    n += __shfl_xor(n, off, 64);
-  }
-  if (lane == 0) {
-    wave_f[wave] = z;
-    wave_i[wave] = n;
+      for (int u = 0; u < kBatch; ++u)
+        v[u] = b0 + u * R < blocks ? src[(int64_t)(b0 + u * R) * quads + quad] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          f[w] += __uint_as_float(v[u][w]);  // one of the two is not used
+          c[w] += v[u][w];
+        }
+    }
+    u32x4 out;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) out[w] = is_float(4 * quad + w) ? __float_as_uint(f[w]) : c[w];
+    slice_sum[slice * quads + quad] = out;
   }
   __syncthreads();
-  z = 0.f;
-  n = 0;
-  for (int q = 0; q < kFinishThreads / 64; ++q) {
-    z += wave_f[q];
-    n += wave_i[q];
-  }
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(slice_sum);
+  auto total_f = [&](int w) {
+    float sum = 0.f;
+    for (int q = 0; q < R; ++q) sum += __uint_as_float(words[q * quads * 4 + w]);
+    return sum;
+  };
+  auto total_i = [&](int w) {
+    int sum = 0;
+    for (int q = 0; q < R; ++q) sum += (int)words[q * quads * 4 + w];
+    return sum;
+  };
+  const int n = total_i(2 * E + 1);
   const float nf = (float)(n > 0 ? n : 1);
   float mean = 0.f;
   int count = 0;
   if (tid < E) {
-    for (int q = 0; q < R; ++q) {
-      mean += fsum[q * E + tid];
-      count += csum[q * E + tid];
-    }
-    mean /= nf;
+    mean = total_f(tid) / nf;
+    count = total_i(E + tid);
     counts[tid] = count;
     prob_mean[tid] = mean;
   }
@@ -350,7 +355,6 @@ __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uin
     dot += __shfl_xor(dot, off, 64);
     total += __shfl_xor(total, off, 64);
   }
-  __syncthreads();
   if (lane == 0) {
     wave_f[wave] = dot;
     wave_i[wave] = total;
@@ -365,7 +369,7 @@ __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uin
     }
     tokens[0] = n;
     losses[0] = (float)E * dot / (float)(total > 0 ? total : 1);
-    losses[1] = z / nf;
+    losses[1] = total_f(2 * E) / nf;
   }
 }
 
@@ -384,8 +388,11 @@ struct RouterBackwardArgs {
 };
 
 template <typename T, int G, int V>
-__global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterBackwardArgs a) {
-  constexpr int kGroups = kThreads / G;
+__global__ __launch_bounds__(kPlainThreads) void router_backward_kernel(RouterBackwardArgs a) {
+  constexpr int kGroups = kPlainThreads / G;
+  // the routing part of a token's gradient, expert by expert: every chosen slot adds to its expert's
+  // place, and the lane that holds the expert reads it
+  __shared__ __align__(16) float routing[kGroups][G * V];
   const int tid = threadIdx.x, group = tid / G, g = tid % G;
   const int e0 = g * V;
   // c_e = dL0 E f_e / n of this lane's experts, and 2 dL1 / n
@@ -431,27 +438,39 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterBackwar
     }
     dot = group_sum<G>(dot);
     float shift = dz * (m0 + logf(s)) - dot;
-    float gw = 0.f;  // sum over the kept slots of g_j w_j
+    float part[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[i] = 0.f;
     if (a.d_w != nullptr) {
-      for (int j = 0; j < a.k; ++j) {
+      float* row = routing[group];
+#pragma unroll
+      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(row + e0 + i) = float4{0.f, 0.f, 0.f, 0.f};
+      float gw = 0.f;  // sum over the kept slots of g_j w_j
+      for (int j = g; j < a.k; j += G) {
         const int id = a.ids[t * a.k + j];
         if ((unsigned)id < (unsigned)a.E) gw += a.d_w[t * a.k + j] * a.w[t * a.k + j];
       }
+      gw = group_sum<G>(gw);
+      for (int j = g; j < a.k; j += G) {
+        const int id = a.ids[t * a.k + j];
+        if ((unsigned)id < (unsigned)a.E) {
+          const float grad = a.d_w[t * a.k + j], wj = a.w[t * a.k + j];
+          atomicAdd(row + id, a.renormalize ? wj * (grad - gw) : wj * grad);  // distinct ids: one addend each
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the group is of one wave
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(row + e0 + i);
+        part[i] = v.x; part[i + 1] = v.y; part[i + 2] = v.z; part[i + 3] = v.w;
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_wave_barrier();
       if (!a.renormalize) shift -= gw;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = p[i] * (c[i] + shift);
-    if (a.d_w != nullptr) {
-      for (int j = 0; j < a.k; ++j) {
-        const int at = a.ids[t * a.k + j] - e0;
-        if ((unsigned)at < (unsigned)V && e0 + at < a.E) {
-          const float grad = a.d_w[t * a.k + j], wj = a.w[t * a.k + j];
-          const float part = a.renormalize ? wj * (grad - gw) : wj * grad;
-#pragma unroll
-          for (int i = 0; i < V; ++i) d[i] += i == at ? part : 0.f;
-        }
-      }
-    }
+    for (int i = 0; i < V; ++i) d[i] = p[i] * (c[i] + shift) + part[i];
     store_row<T, V>(static_cast<T*>(a.d_logits), t, a.E, e0, a.wide, d);
   }
 }
@@ -466,7 +485,7 @@ int64_t router_blocks(int64_t T, int groups, int64_t cap) {
 int lanes_of(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
 
 // The losses' first launch leaves one partial a workgroup, which the second reads in one workgroup.
-constexpr int64_t kLossBlocks = 256;
+constexpr int64_t kLossBlocks = 512;
 
 template <typename F>
 hipError_t by_width(int E, F&& f) {
@@ -484,7 +503,7 @@ bool wide_rows(const void* p, int E, bool f32) {
 }  // namespace
 
 int64_t router_partial_words(int64_t T, int32_t E) {
-  return router_blocks(T, kThreads / lanes_of(E), kLossBlocks) * partial_words(E);
+  return router_blocks(T, kLossThreads / lanes_of(E), kLossBlocks) * partial_words(E);
 }
 
 hipError_t launch_router_topk(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
@@ -494,9 +513,9 @@ hipError_t launch_router_topk(const void* logits, bool f32, int64_t T, int32_t E
   const int64_t cap = (int64_t)device_cu_count(current_device()) * 16;
   return by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
-    const dim3 grid((unsigned)router_blocks(T, kThreads / G, cap));
-    if (f32) hipLaunchKernelGGL((router_topk_kernel<float, G, V, false>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, false>), grid, dim3(kThreads), 0, stream, a);
+    const dim3 grid((unsigned)router_blocks(T, kPlainThreads / G, cap));
+    if (f32) hipLaunchKernelGGL((router_topk_kernel<float, G, V, false>), grid, dim3(kPlainThreads), 0, stream, a);
+    else hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, false>), grid, dim3(kPlainThreads), 0, stream, a);
     return hipGetLastError();
   });
 }
@@ -505,13 +524,13 @@ hipError_t launch_router_topk_losses(const void* logits, bool f32, int64_t T, in
                                      int32_t* ids, float* w, float* lse, int32_t* counts, int32_t* tokens,
                                      float* prob_mean, float* losses, uint32_t* partial, hipStream_t stream) {
   const RouterArgs a{logits, T, E, k, renormalize, wide_rows(logits, E, f32), ids, w, lse, partial};
-  const int64_t blocks = router_blocks(T, kThreads / lanes_of(E), kLossBlocks);
+  const int64_t blocks = router_blocks(T, kLossThreads / lanes_of(E), kLossBlocks);
   const hipError_t st = by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     if (f32)
-      hipLaunchKernelGGL((router_topk_kernel<float, G, V, true>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((router_topk_kernel<float, G, V, true>), dim3((unsigned)blocks), dim3(kLossThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, true>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, true>), dim3((unsigned)blocks), dim3(kLossThreads), 0, stream, a);
     return hipGetLastError();
   });
   if (st != hipSuccess) return st;
@@ -529,9 +548,9 @@ hipError_t launch_router_backward(const void* logits, bool f32, int64_t T, int32
   const int64_t cap = (int64_t)device_cu_count(current_device()) * 16;
   return by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
-    const dim3 grid((unsigned)router_blocks(T, kThreads / G, cap));
-    if (f32) hipLaunchKernelGGL((router_backward_kernel<float, G, V>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((router_backward_kernel<uint16_t, G, V>), grid, dim3(kThreads), 0, stream, a);
+    const dim3 grid((unsigned)router_blocks(T, kPlainThreads / G, cap));
+    if (f32) hipLaunchKernelGGL((router_backward_kernel<float, G, V>), grid, dim3(kPlainThreads), 0, stream, a);
+    else hipLaunchKernelGGL((router_backward_kernel<uint16_t, G, V>), grid, dim3(kPlainThreads), 0, stream, a);
     return hipGetLastError();
   });
 }

@@ -43,7 +43,7 @@ def test_router_validation(lib, fn, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(counts=None), NULLP), (dict(tokens=None), NULLP), (dict(mean=None), NULLP), (dict(out=None), NULLP),
-    (dict(ws=None), NULLP), (dict(lse=None), NULLP), (dict(counts=FAKE + 2), ALIGN), (dict(ws=FAKE + 2), ALIGN),
+    (dict(ws=None), NULLP), (dict(lse=None), NULLP), (dict(counts=FAKE + 2), ALIGN), (dict(ws=FAKE + 4), ALIGN),
     (dict(wsb=8), WS),
 ])
 def test_router_losses_validation(lib, kw, status):
@@ -68,8 +68,8 @@ def test_router_accepts(lib):
 
 def test_router_workspace_bytes(lib):
     f = moe.router_workspace_bytes
-    assert f(0, 64) == (2 * 64 + 2) * 4  # one workgroup's partial sums
-    assert f(32, 64) == f(0, 64) and f(33, 64) == 2 * f(0, 64)
+    assert f(0, 64) == 132 * 4  # one workgroup's partial sums: 2 E + 2 words, in whole 16 bytes
+    assert f(64, 64) == f(0, 64) and f(65, 64) == 2 * f(0, 64)
     assert f(-1, 64) == 0 and f(4, 0) == 0 and f(4, 1025) == 0 and f(2**31, 4) == 0
     assert f(10**6, 64) == f(2**31 - 1, 64)  # bounded however many tokens
 
