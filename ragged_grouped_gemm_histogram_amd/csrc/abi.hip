@@ -59,9 +59,9 @@ moe_status check_router_shape(int32_t dtype, int64_t T, int32_t E, int32_t k) {
   return MOE_OK;
 }
 
-// Rows the quantising launches take: their workgroups (1024 pieces of 8 values each) are counted in 31 bits.
+// Rows the quantising launches take: their workgroups (512 pieces of 8 values or more) are counted in 31 bits.
 inline bool bad_mxfp4_rows(int64_t rows, int64_t K) {
-  return rows < 0 || bad_width(K) || rows > (kMaxSlots * 1024) / (mx_blocks(K) * 4);
+  return rows < 0 || bad_width(K) || rows > (kMaxSlots * 512) / (mx_blocks(K) * 4);
 }
 
 }  // namespace
