@@ -48,32 +48,40 @@ __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t cap) { return v 
 
 // ---------------------------------------------------------------------------------------------
 // Few rows per expert: 32 rows by 64 weight rows a workgroup, operands straight from memory to
-// registers, the contraction split over the four waves and joined through LDS.
+// registers, the contraction split over the four waves and joined through LDS. Such a call is bound
+// by reading the weights of the experts that have rows, so a wave asks for all it needs (up to
+// BATCH units of 128 values) before it multiplies, the weights first: they do not wait for the
+// dispatch order.
 // ---------------------------------------------------------------------------------------------
 constexpr int kThinThreads = 256;
 constexpr int kThinWaves = 4;
 constexpr int kUnit = 128;  // contraction per step: four blocks, two per lane half
 
-template <bool GATED>
-__global__ __launch_bounds__(kThinThreads) void mxfp4_thin_kernel(MxGemmArgs g) {
+template <bool GATED, int BATCH>
+__global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs g) {
   __shared__ int mt_prefix[MOE_MAX_EXPERTS + 1];
+  __shared__ int offs[MOE_MAX_EXPERTS + 1];  // clamped to the capacity
   __shared__ int wave_total[kThinWaves];
-  __shared__ float4 red[kThinWaves * 2 * 4 * 64];
+  __shared__ float4 red[kThinWaves * 4 * 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 31, hh = lane >> 5;
 
-  // prefix of the experts' 32-row tile counts, from the offsets clamped to the capacity
+  // prefix of the experts' 32-row tile counts
   {
     constexpr int kPer = MOE_MAX_EXPERTS / kThinThreads;
     int mt[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kThinThreads;
+      if (e <= g.E) offs[e] = (int)clamp_row(g.offsets[e], g.cap_rows);
+    }
+    if (tid == 0 && g.E == MOE_MAX_EXPERTS) offs[g.E] = (int)clamp_row(g.offsets[g.E], g.cap_rows);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
       mt[i] = 0;
-      if (e < g.E) {
-        const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
-        mt[i] = hi > lo ? (int)((hi - lo + 31) / 32) : 0;
-      }
+      if (e < g.E) mt[i] = offs[e + 1] > offs[e] ? (offs[e + 1] - offs[e] + 31) / 32 : 0;
       sum += mt[i];
     }
     int incl = sum;
@@ -96,88 +104,110 @@ __global__ __launch_bounds__(kThinThreads) void mxfp4_thin_kernel(MxGemmArgs g) 
     __syncthreads();
   }
   constexpr int kCols = GATED ? 32 : 64;
-  const int64_t n_tiles = (g.N + kCols - 1) / kCols;
+  const int n_tiles = (int)((g.N + kCols - 1) / kCols);
   const int64_t total = (int64_t)mt_prefix[g.E] * n_tiles;
   const int64_t qp = mx_row_bytes(g.K), sp = mx_scale_bytes(g.K);
   const int blocks = (int)mx_blocks(g.K);
   const int units = (int)((g.K + kUnit - 1) / kUnit);
   const int u_lo = units * wave / kThinWaves, u_hi = units * (wave + 1) / kThinWaves;
+  const int b_end = min(blocks, 4 * u_hi);
 
   for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
     const int gm = (int)(t / n_tiles);
-    const int64_t n0 = (t - (int64_t)gm * n_tiles) * kCols;
+    const int n0 = (int)(t - (int64_t)gm * n_tiles) * kCols;
     int e = 0, hi_e = g.E;  // largest e with mt_prefix[e] <= gm
     while (hi_e - e > 1) {
       const int mid = (e + hi_e) >> 1;
       if (mt_prefix[mid] <= gm) e = mid; else hi_e = mid;
     }
-    const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
+    const int64_t lo = offs[e], hi = offs[e + 1];
     const int64_t row0 = lo + (int64_t)(gm - mt_prefix[e]) * 32;
     if (row0 < lo || row0 >= hi) continue;  // offsets that are no running sum can wrap the tile counts
     const int valid = (int)(hi - row0 < 32 ? hi - row0 : 32);
     // sources: rows past the block repeat its last, columns past N the tile's first; neither is stored
     int64_t a_row = row0 + (r < valid ? r : valid - 1);
-    if (g.a_rows != nullptr) {
-      const int64_t last = g.a_tokens * g.a_k - 1;
-      int64_t slot = g.a_rows[a_row];
-      slot = slot < 0 ? 0 : (slot > last ? last : slot);
-      a_row = slot / g.a_k;
-    }
-    int64_t w_row[2];
+    int32_t slot = 0;
+    if (g.a_rows != nullptr) slot = g.a_rows[a_row];
+    // weights through buffer resources that end with the tile's 32 rows: a block past this wave's part
+    // gets an offset past the range and reads as zeros, with no branch between the loads
+    __amdgpu_buffer_rsrc_t w_q[2], w_s[2];
+    uint32_t w_row[2];
+    const int64_t w_first = (int64_t)e * g.w_rows + n0;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      int64_t n = n0 + (GATED ? r : f * 32 + r);
-      n = n < g.N ? n : n0;
-      w_row[f] = e * g.w_rows + n + (GATED ? f * g.N : 0);
+      const int64_t left = g.N - n0 - (GATED ? 0 : f * 32);  // columns of this half; none: the other's again
+      const int64_t row = w_first + (GATED ? f * g.N : (left > 0 ? f * 32 : 0));
+      w_q[f] = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform_addr(g.w_q + row * qp)), (short)0,
+                                                 (int)(32 * qp), 0x00020000);
+      w_s[f] = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform_addr(g.w_s + row * sp)), (short)0,
+                                                 (int)(32 * sp), 0x00020000);
+      w_row[f] = r < left ? (uint32_t)r : 0u;
     }
-    const uint8_t* a_q = g.a_q + a_row * qp;
-    const uint8_t* a_s = g.a_s + a_row * sp;
-    const uint8_t* w_q[2] = {g.w_q + w_row[0] * qp, g.w_q + w_row[1] * qp};
-    const uint8_t* w_s[2] = {g.w_s + w_row[0] * sp, g.w_s + w_row[1] * sp};
     f32x16 acc[2];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
-    for (int u = u_lo; u < u_hi; ++u) {
-      const int b = 4 * u + 2 * hh;  // this half's blocks: b and b + 1
-      u32x4 av[2], wv[2][2];
-      uint32_t as, ws[2];
-      const uint32_t keep = (b < blocks ? 0xFFu : 0u) | (b + 1 < blocks ? 0xFF00u : 0u);
-      as = *reinterpret_cast<const uint16_t*>(a_s + b) & keep;
+    for (int u0 = u_lo; u0 < u_hi; u0 += BATCH) {
+      u32x4 av[BATCH][2], wv[BATCH][2][2];
+      uint32_t as[BATCH], ws[BATCH][2];
+      // blocks b and b + 1 of unit u0 + x, values and scale bytes
 #pragma unroll
-      for (int f = 0; f < 2; ++f) ws[f] = *reinterpret_cast<const uint16_t*>(w_s[f] + b) & keep;
+      for (int x = 0; x < BATCH; ++x) {
+        const int b = 4 * (u0 + x) + 2 * hh;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const u32x4 zero{0u, 0u, 0u, 0u};
-        const bool in = b + i < blocks;
-        av[i] = in ? *reinterpret_cast<const u32x4*>(a_q + (b + i) * 16) : zero;
+        for (int f = 0; f < 2; ++f) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f) wv[f][i] = in ? *reinterpret_cast<const u32x4*>(w_q[f] + (b + i) * 16) : zero;
+          for (int i = 0; i < 2; ++i)
+            wv[x][f][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                w_q[f], b + i < b_end ? w_row[f] * (uint32_t)qp + (uint32_t)(b + i) * 16u : 0x80000000u, 0, 0);
+          ws[x][f] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+              w_s[f], b < b_end ? w_row[f] * (uint32_t)sp + (uint32_t)b : 0x80000000u, 0, 0);
+        }
+      }
+      if (u0 == u_lo && g.a_rows != nullptr) {
+        const int64_t last = g.a_tokens * g.a_k - 1;
+        a_row = (slot < 0 ? 0u : (uint32_t)(slot > last ? last : slot)) / (uint32_t)g.a_k;
+      }
+      // the row's blocks past the part are its last one again, times the weights' zeros
+      const uint8_t* a_q = g.a_q + a_row * qp;
+      const uint8_t* a_s = g.a_s + a_row * sp;
+#pragma unroll
+      for (int x = 0; x < BATCH; ++x) {
+        const int b = 4 * (u0 + x) + 2 * hh;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) av[x][i] = *reinterpret_cast<const u32x4*>(a_q + min(b + i, b_end - 1) * 16);
+        as[x] = *reinterpret_cast<const uint16_t*>(a_s + min(b, (b_end - 1) & ~1));
       }
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        acc[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(wv[f][0]), fp4_operand(av[0]), acc[f], 4, 4, 0,
-                                                                 (int)ws[f], 0, (int)as);
-        acc[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(wv[f][1]), fp4_operand(av[1]), acc[f], 4, 4, 1,
-                                                                 (int)ws[f], 1, (int)as);
+      for (int x = 0; x < BATCH; ++x) {
+        // bytes past the row's last block may hold anything (255 is a NaN)
+        const int b = 4 * (u0 + x) + 2 * hh;
+        const uint32_t keep = b + 1 < blocks ? 0xFFFFu : (b < blocks ? 0xFFu : 0u);
+        const int a = (int)(as[x] & keep);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int w = (int)(ws[x][f] & keep);
+          acc[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(wv[x][f][0]), fp4_operand(av[x][0]), acc[f], 4,
+                                                                   4, 0, w, 0, a);
+          acc[f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(wv[x][f][1]), fp4_operand(av[x][1]), acc[f], 4,
+                                                                   4, 1, w, 1, a);
+        }
       }
     }
-    // the waves' sums in wave order
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        red[((wave * 2 + f) * 4 + q) * 64 + lane] =
-            float4{acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]};
-    __syncthreads();
+    // the waves' sums, in wave order, one half after the other
     float4 sum[2];
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      sum[f] = red[(f * 4 + wave) * 64 + lane];  // this thread's quad of columns: q = wave
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        red[(wave * 4 + q) * 64 + lane] = float4{acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]};
+      __syncthreads();
+      sum[f] = red[wave * 64 + lane];  // this thread's quad of columns: q = wave
 #pragma unroll
       for (int w = 1; w < kThinWaves; ++w) {
-        const float4 v = red[((w * 2 + f) * 4 + wave) * 64 + lane];
+        const float4 v = red[(w * 4 + wave) * 64 + lane];
         sum[f].x += v.x; sum[f].y += v.y; sum[f].z += v.z; sum[f].w += v.w;
       }
+      __syncthreads();  // red is reused
     }
     if (r < valid) {
       uint16_t* dst = g.out + (row0 + r) * g.N;
@@ -197,7 +227,6 @@ __global__ __launch_bounds__(kThinThreads) void mxfp4_thin_kernel(MxGemmArgs g) 
           }
       }
     }
-    __syncthreads();  // red is reused by the next tile
   }
 }
 
@@ -682,11 +711,15 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   const int64_t qp = mx_row_bytes(g.K);
   const int64_t a_span = (g.a_rows != nullptr ? g.a_tokens : 256) * qp;
   const bool fits = a_span <= 0x7FFFFFFFll && g.w_rows * qp <= 0x7FFFFFFFll;
-  if (fits && g.cap_rows >= (int64_t)64 * g.E) {
+  // From a mean of 32 rows per expert (all the host knows) they are faster however the rows are spread. Thin and
+  // pipelined, evenly spread / skewed: gate/up of 64 experts 2048 x 768 at 16 rows 30 and 42 / 36 and 42 us, at 32
+  // rows 35 and 42 / 45 and 43, at 64 rows 60 and 44 / 70 and 45; of 128 experts at 32 rows 65 and 63 / 87 and 60;
+  // down projections at 32 rows 24 and 23 / 31 and 25.
+  if (fits && g.cap_rows >= (int64_t)32 * g.E) {
     if (g.K % kStageK != 0 || g.K < kRing * kStageK) return launch_pipe<MxBig<GATED>, true>(g, stream);
     return launch_pipe<MxBig<GATED>, false>(g, stream);
   }
-  hipLaunchKernelGGL(mxfp4_thin_kernel<GATED>, dim3(cus * 4), dim3(kThinThreads), 0, stream, g);
+  hipLaunchKernelGGL((mxfp4_thin_kernel<GATED, 2>), dim3(cus * 4), dim3(kThinThreads), 0, stream, g);
   return hipGetLastError();
 }
 
