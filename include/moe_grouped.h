@@ -456,6 +456,15 @@ moe_status moe_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_scales,
                                     int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
                                     int64_t d, int64_t h, int32_t E, uint16_t* h_buf, hipStream_t stream);
 
+/* The same launch with its result as MXFP4 rows of h values, ready for the
+ * down projection: h_q and h_scales [T*k] are bit for bit what
+ * moe_mxfp4_quantize makes of moe_gemm_up_swiglu_mxfp4's h_buf (rows past M
+ * untouched), without the bf16 rows in between. */
+moe_status moe_gemm_up_swiglu_mxfp4_q(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* perm, int64_t T,
+                                      int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
+                                      int64_t d, int64_t h, int32_t E, uint8_t* h_q, uint8_t* h_scales,
+                                      hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char* moe_status_string(moe_status s);
 

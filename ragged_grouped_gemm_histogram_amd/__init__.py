@@ -57,6 +57,8 @@ _SIGNATURES = {
     "moe_mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "moe_grouped_projection_mxfp4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
     "moe_gemm_up_swiglu_mxfp4": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp]),
+    "moe_gemm_up_swiglu_mxfp4_q": (ctypes.c_int,
+                                   [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -687,23 +689,41 @@ def moe_grouped_projection_mxfp4(x: Mxfp4, offsets: torch.Tensor, w: Mxfp4, *, y
     return y
 
 
-def moe_gemm_up_swiglu_mxfp4(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, *, perm=None, k: int = 1,
-                             h_buf=None) -> torch.Tensor:
-    """h_buf[p] = bf16(SiLU(g) * u), [g | u] = X[perm[p] // k] @ W_ug[e]^T, on MXFP4 token rows [T, d] and weights
-    [E, 2h, d] (one launch). Without ``perm`` the rows are sorted already and k is 1."""
+def _mxfp4_up(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, perm, k: int):
     T, E, two_h, dev = _mxfp4_experts(x, offsets, w_ug)
     if two_h % 2:
         raise ValueError("w_ug must hold as many gate as up rows")
-    h, k = two_h // 2, int(k)
+    k = int(k)
     if perm is not None:
         _want(perm, "perm", torch.int32, (T * k,), dev)
     elif k != 1:
         raise ValueError("k other than 1 needs perm")
+    return T, k, E, two_h // 2, dev
+
+
+def moe_gemm_up_swiglu_mxfp4(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, *, perm=None, k: int = 1,
+                             h_buf=None) -> torch.Tensor:
+    """h_buf[p] = bf16(SiLU(g) * u), [g | u] = X[perm[p] // k] @ W_ug[e]^T, on MXFP4 token rows [T, d] and weights
+    [E, 2h, d] (one launch). Without ``perm`` the rows are sorted already and k is 1."""
+    T, k, E, h, dev = _mxfp4_up(x, offsets, w_ug, perm, k)
     h_buf = _out(h_buf, "h_buf", torch.bfloat16, (T * k, h), dev)
     _check(load_library().moe_gemm_up_swiglu_mxfp4(_ptr(x.q), _ptr(x.scales), _ptr(perm), T, k, _ptr(offsets),
                                                    _ptr(w_ug.q), _ptr(w_ug.scales), x.width, h, E, _ptr(h_buf),
                                                    _stream(x.q)), "moe_gemm_up_swiglu_mxfp4")
     return h_buf
+
+
+def moe_gemm_up_swiglu_mxfp4_q(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, *, perm=None, k: int = 1, q=None,
+                               scales=None) -> Mxfp4:
+    """moe_gemm_up_swiglu_mxfp4 with its result quantised in the same launch, bit for bit as moe_mxfp4_quantize
+    would: MXFP4 rows [T * k] of h values for the down projection."""
+    T, k, E, h, dev = _mxfp4_up(x, offsets, w_ug, perm, k)
+    q = _out(q, "q", torch.uint8, (T * k, mxfp4_row_bytes(h)), dev)
+    scales = _out(scales, "scales", torch.uint8, (T * k, mxfp4_scale_bytes(h)), dev)
+    _check(load_library().moe_gemm_up_swiglu_mxfp4_q(_ptr(x.q), _ptr(x.scales), _ptr(perm), T, k, _ptr(offsets),
+                                                     _ptr(w_ug.q), _ptr(w_ug.scales), x.width, h, E, _ptr(q),
+                                                     _ptr(scales), _stream(x.q)), "moe_gemm_up_swiglu_mxfp4_q")
+    return Mxfp4(q, scales, h)
 
 
 def moe_expert_forward_mxfp4(x: torch.Tensor, expert_ids: torch.Tensor, routing_w: torch.Tensor, w_ug: Mxfp4,
@@ -713,8 +733,8 @@ def moe_expert_forward_mxfp4(x: torch.Tensor, expert_ids: torch.Tensor, routing_
     weights). Returns (y, Permuted)."""
     k = expert_ids.shape[1]
     p = moe_permute(x, expert_ids, w_ug.q.shape[0], gather=False)
-    h_buf = moe_gemm_up_swiglu_mxfp4(moe_mxfp4_quantize(x), p.offsets, w_ug, perm=p.perm, k=k)
-    y_perm = moe_grouped_projection_mxfp4(moe_mxfp4_quantize(h_buf), p.offsets, w_down)
+    h = moe_gemm_up_swiglu_mxfp4_q(moe_mxfp4_quantize(x), p.offsets, w_ug, perm=p.perm, k=k)
+    y_perm = moe_grouped_projection_mxfp4(h, p.offsets, w_down)
     return moe_unpermute(y_perm, p.inv_map, routing_w), p
 
 
@@ -728,5 +748,5 @@ __all__ = [
     "ROUTER_MAX_TOPK", "Routed", "moe_router_topk", "moe_router_topk_losses", "moe_router_backward",
     "router_workspace_bytes", "Mxfp4", "mxfp4_row_bytes", "mxfp4_scale_bytes", "moe_mxfp4_quantize",
     "moe_mxfp4_quantize_weights", "moe_mxfp4_dequantize", "moe_grouped_projection_mxfp4", "moe_gemm_up_swiglu_mxfp4",
-    "moe_expert_forward_mxfp4",
+    "moe_gemm_up_swiglu_mxfp4_q", "moe_expert_forward_mxfp4",
 ]

@@ -64,6 +64,22 @@ inline bool bad_mxfp4_rows(int64_t rows, int64_t K) {
   return rows < 0 || bad_width(K) || rows > (kMaxSlots * 512) / (mx_blocks(K) * 4);
 }
 
+// The MXFP4 gate/up calls' operands; out and out2 are what the call writes.
+moe_status check_up_mxfp4(const void* x_q, const void* x_scales, const void* perm, int64_t T, int32_t k,
+                          const void* offsets, const void* w_q, const void* w_scales, int64_t d, int64_t h, int32_t E,
+                          const void* out, const void* out2) {
+  if (T < 0 || k < 1 || T > kMaxSlots / k || (perm == nullptr && k != 1 && T != 0)) return MOE_ERR_BAD_SHAPE;
+  const moe_status st = check_gemm_shape(T * k, d, h, E);
+  if (st != MOE_OK) return st;
+  if (missing(x_q, T) || missing(x_scales, T) || offsets == nullptr || w_q == nullptr || w_scales == nullptr ||
+      missing(out, T) || missing(out2, T))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(x_q, 16) || misaligned(x_scales, 16) || misaligned(w_q, 16) || misaligned(w_scales, 16) ||
+      misaligned(out, 16) || misaligned(out2, 16) || misaligned(offsets, 4) || misaligned(perm, 4))
+    return MOE_ERR_MISALIGNED;
+  return check_device();
+}
+
 }  // namespace
 
 int device_cu_count(int dev) {
@@ -467,21 +483,22 @@ moe_status moe_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_sca
 moe_status moe_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* perm, int64_t T,
                                     int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
                                     int64_t d, int64_t h, int32_t E, uint16_t* h_buf, hipStream_t stream) {
-  if (T < 0 || k < 1 || T > kMaxSlots / k || (perm == nullptr && k != 1 && T != 0)) return MOE_ERR_BAD_SHAPE;
-  const int64_t S = T * k;
-  moe_status st = check_gemm_shape(S, d, h, E);
-  if (st != MOE_OK) return st;
-  if (missing(x_q, T) || missing(x_scales, T) || offsets == nullptr || w_q == nullptr || w_scales == nullptr ||
-      missing(h_buf, S))
-    return MOE_ERR_NULL_POINTER;
-  if (misaligned(x_q, 16) || misaligned(x_scales, 16) || misaligned(w_q, 16) || misaligned(w_scales, 16) ||
-      misaligned(h_buf, 16) || misaligned(offsets, 4) || misaligned(perm, 4))
-    return MOE_ERR_MISALIGNED;
-  if ((st = check_device()) != MOE_OK) return st;
-  if (S == 0) return MOE_OK;
+  const moe_status st = check_up_mxfp4(x_q, x_scales, perm, T, k, offsets, w_q, w_scales, d, h, E, h_buf, h_buf);
+  if (st != MOE_OK || T == 0) return st;
   (void)hipGetLastError();
-  return launched(launch_gemm_up_swiglu_mxfp4(x_q, x_scales, T, perm, k, offsets, w_q, w_scales, S, d, h, E, h_buf,
-                                              stream));
+  return launched(launch_gemm_up_swiglu_mxfp4(x_q, x_scales, T, perm, k, offsets, w_q, w_scales, T * k, d, h, E, h_buf,
+                                              nullptr, nullptr, stream));
+}
+
+moe_status moe_gemm_up_swiglu_mxfp4_q(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* perm, int64_t T,
+                                      int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
+                                      int64_t d, int64_t h, int32_t E, uint8_t* h_q, uint8_t* h_scales,
+                                      hipStream_t stream) {
+  const moe_status st = check_up_mxfp4(x_q, x_scales, perm, T, k, offsets, w_q, w_scales, d, h, E, h_q, h_scales);
+  if (st != MOE_OK || T == 0) return st;
+  (void)hipGetLastError();
+  return launched(launch_gemm_up_swiglu_mxfp4(x_q, x_scales, T, perm, k, offsets, w_q, w_scales, T * k, d, h, E, nullptr,
+                                              h_q, h_scales, stream));
 }
 
 static_assert(sizeof(moe_status) == sizeof(int), "moe_status travels as a C int");

@@ -118,7 +118,7 @@ hipError_t launch_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_
                                            int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream);
 hipError_t launch_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_s, int64_t x_rows, const int32_t* perm,
                                        int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_s,
-                                       int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf,
-                                       hipStream_t stream);
+                                       int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf, uint8_t* h_q,
+                                       uint8_t* h_s, hipStream_t stream);  // to h_buf, or without one to h_q and h_s
 
 }  // namespace moe

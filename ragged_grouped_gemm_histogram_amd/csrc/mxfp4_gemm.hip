@@ -38,6 +38,8 @@ struct MxGemmArgs {
   int64_t cap_rows;
   uint16_t* out;            // [cap_rows, N], row pitch ldo
   int64_t ldo;
+  uint8_t* out_q = nullptr;  // gated, instead of out: the result's MXFP4 rows
+  uint8_t* out_s = nullptr;
 };
 
 __device__ __forceinline__ i32x8 fp4_operand(const u32x4& v) {
@@ -57,7 +59,7 @@ constexpr int kThinThreads = 256;
 constexpr int kThinWaves = 4;
 constexpr int kUnit = 128;  // contraction per step: four blocks, two per lane half
 
-template <bool GATED, int BATCH>
+template <bool GATED, bool QUANT, int BATCH>
 __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs g) {
   __shared__ int mt_prefix[MOE_MAX_EXPERTS + 1];
   __shared__ int offs[MOE_MAX_EXPERTS + 1];  // clamped to the capacity
@@ -209,9 +211,31 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
       }
       __syncthreads();  // red is reused
     }
-    if (r < valid) {
+    const int col = n0 + 8 * wave + 4 * hh;
+    if constexpr (QUANT) {
+      // the tile's 32 columns are one block a row: its bf16 rows go through LDS to four lanes a row
+      uint2* h = reinterpret_cast<uint2*>(red);  // [32 rows][8 pieces of 4 columns]
+      h[r * 8 + 2 * wave + hh] = col < g.N ? uint2{pack_bf16x2(swiglu(sum[0].x, sum[1].x), swiglu(sum[0].y, sum[1].y)),
+                                                   pack_bf16x2(swiglu(sum[0].z, sum[1].z), swiglu(sum[0].w, sum[1].w))}
+                                           : uint2{0u, 0u};
+      __syncthreads();
+      const int row = tid >> 2, piece = tid & 3;
+      if (tid < 128 && row < valid) {
+        const u32x4 v = reinterpret_cast<const u32x4*>(red)[row * 4 + piece];
+        uint32_t top = max_magnitude(v);
+        top = max(top, quad_xor<0xB1>(top));
+        top = max(top, quad_xor<0x4E>(top));
+        const uint32_t byte = scale_byte(top);
+        const int64_t out_row = row0 + row, osp = mx_scale_bytes(g.N);
+        reinterpret_cast<uint32_t*>(g.out_q + out_row * mx_row_bytes(g.N) + n0 / 2)[piece] = to_fp4(v, byte);
+        uint8_t* os = g.out_s + out_row * osp;
+        if (piece == 0) os[n0 / 32] = (uint8_t)byte;
+        if (n0 + 32 >= g.N)  // the padding behind the last block
+          for (int64_t z = n0 / 32 + 1 + piece; z < osp; z += 4) os[z] = 0;
+      }
+      __syncthreads();
+    } else if (r < valid) {
       uint16_t* dst = g.out + (row0 + r) * g.N;
-      const int64_t col = n0 + 8 * wave + 4 * hh;
       if constexpr (GATED) {
         if (col < g.N) {
           const uint2 v{pack_bf16x2(swiglu(sum[0].x, sum[1].x), swiglu(sum[0].y, sum[1].y)),
@@ -287,23 +311,49 @@ __device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
 // row's 64 columns from the registers of one lane pair into eight lanes: every store writes 8 rows
 // of 128 consecutive bytes. Rows past the block and columns past N fall outside the buffer resource
 // and are dropped; every wave issues all its stores.
-template <class C>
-constexpr int kTileStores = C::FM * 4 * (C::OUTW / C::WGN / 64);
+//
+// QUANT: the rows leave as MXFP4, 4 bytes of values a lane and two scale bytes a row and store. A
+// block of 32 columns is in the four lanes 16 and 32 apart.
+template <class C, bool QUANT>
+constexpr int kTileStores = C::FM * (QUANT ? 8 : 4) * (C::OUTW / C::WGN / 64);
 
-template <class C>
+// Maximum over the four lanes whose numbers differ in bits 4 and 5.
+__device__ __forceinline__ uint32_t max_of_16s(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = max((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max((uint32_t)b[0], (uint32_t)b[1]);
+}
+
+template <class C, bool QUANT>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], const MxGemmArgs& g, const MxCoord& tc) {
   constexpr int kPieces = C::OUTW / C::WGN / 64;  // of 64 columns
   static_assert(C::OUTW / C::WGN % 64 == 0, "a wave stores whole lines");
   const int tid = epilogue_tid<true>(), lane = tid & 63, wave = tid >> 6;
   const int wm = wave / C::WGN, wn = wave % C::WGN;
-  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      g.out + (int64_t)tc.row0 * g.ldo, (short)0, (int)((int64_t)tc.rows_valid * g.ldo * 2), 0x00020000);
-  const uint32_t row_bytes = (uint32_t)(g.ldo * 2);
+  static_assert(!QUANT || (C::GATED && kPieces == 1), "quantised output is the gated projection's");
+  __amdgpu_buffer_rsrc_t rsrc, s_rsrc;
+  uint32_t row_bytes, s_bytes = 0;
+  if constexpr (QUANT) {
+    row_bytes = (uint32_t)mx_row_bytes(g.N);
+    s_bytes = (uint32_t)mx_scale_bytes(g.N);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(g.out_q + (int64_t)tc.row0 * row_bytes, (short)0,
+                                             (int)((uint32_t)tc.rows_valid * row_bytes), 0x00020000);
+    s_rsrc = __builtin_amdgcn_make_buffer_rsrc(g.out_s + (int64_t)tc.row0 * s_bytes, (short)0,
+                                               (int)((uint32_t)tc.rows_valid * s_bytes), 0x00020000);
+  } else {
+    row_bytes = (uint32_t)(g.ldo * 2);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(g.out + (int64_t)tc.row0 * g.ldo, (short)0,
+                                             (int)((int64_t)tc.rows_valid * g.ldo * 2), 0x00020000);
+  }
   const uint32_t row = (uint32_t)(wm * C::WTM + (lane & 7)) * row_bytes;
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
     const int64_t col = tc.n0 + (wn * kPieces + p) * 64 + 8 * (lane >> 5) + 16 * ((lane >> 4) & 1) + 32 * ((lane >> 3) & 1);
-    const uint32_t base = col < g.N ? row + (uint32_t)(col * 2) : 0x80000000u;
+    const bool in = col < g.N;
+    // (a block that N cuts is filled with zeros)
+    const uint32_t base = QUANT ? (col < (g.N + 31) / 32 * 32 ? row + (uint32_t)(col / 2) : 0x80000000u)
+                                : (in ? row + (uint32_t)(col * 2) : 0x80000000u);
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
       uint32_t v[2][2][4];  // [column block][rows 0-15 / 16-31][16 bytes]
@@ -344,15 +394,36 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], co
 #pragma unroll
         for (int w = 0; w < 4; ++w) swap8(v[0][h][w], v[1][h][w]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[j][h][0], v[j][h][1], v[j][h][2], v[j][h][3]}, rsrc,
-                                                 base + (uint32_t)(32 * i + 16 * h + 8 * j) * row_bytes, 0, 2 /* nt */);
+        for (int j = 0; j < 2; ++j) {
+          u32x4 w{v[j][h][0], v[j][h][1], v[j][h][2], v[j][h][3]};
+          const uint32_t at = (uint32_t)(32 * i + 16 * h + 8 * j);  // rows from the wave's first, and lane % 8
+          if constexpr (QUANT) {
+            if (!in) w = u32x4{0u, 0u, 0u, 0u};
+            const uint32_t byte = scale_byte(max_of_16s(max_magnitude(w)));
+            __builtin_amdgcn_raw_buffer_store_b32(to_fp4(w, byte), rsrc, base + at * row_bytes, 0, 0);
+            // lanes 0..7 write their row's two bytes: their own block's and that of the lane 8 above
+            const uint32_t above = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)byte, 0x128 /* row_ror:8 */, 0xf, 0xf, false);
+            const uint32_t s_at = ((uint32_t)(wm * C::WTM + lane) + at) * s_bytes + (uint32_t)((tc.n0 + wn * 64) / 32);
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(byte | above << 8), s_rsrc, lane < 8 ? s_at : 0x80000000u, 0, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, base + at * row_bytes, 0, 2 /* nt */);
+          }
+        }
       }
+    }
+  }
+  if constexpr (QUANT) {
+    // the last column tile also writes the scale rows' padding behind it
+    const uint32_t done = (uint32_t)((tc.n0 + C::OUTW) / 32);
+    if (tc.n0 + C::OUTW >= g.N && done < s_bytes) {
+      for (int r = tid; r < tc.rows_valid; r += C::THREADS)
+        for (uint32_t z = done; z < s_bytes; z += 4)
+          *reinterpret_cast<uint32_t*>(g.out_s + ((int64_t)tc.row0 + r) * s_bytes + z) = 0u;
     }
   }
 }
 
-template <class C, bool KTAIL>
+template <class C, bool KTAIL, bool QUANT>
 __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
   constexpr int BM = C::BM, BN = C::BN;
   constexpr int OPS = C::A_OPS + C::B_OPS;
@@ -649,7 +720,7 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       // after the next, and for a tile's first three stages the previous tile's stores, issued behind
       // this tile's first four (before the first tile there are none, and its four are waited for
       // above).
-      if (kt < 3) wait_vmcnt_lds<2 * OPS + kTileStores<C>, true>();
+      if (kt < 3) wait_vmcnt_lds<2 * OPS + kTileStores<C, QUANT>, true>();
       else wait_vmcnt_lds<2 * OPS, true>();
       bare_barrier();
       const uint32_t to = ring;
@@ -673,7 +744,7 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       }
       take_scales(last ? 0 : kt + 1);
     }
-    store_tile<C>(acc, g, tc);
+    store_tile<C, QUANT>(acc, g, tc);
     asm volatile("" : : : "memory");  // the stores stay here: the waits above count them
     if (!more) break;
     tc = next;
@@ -681,10 +752,10 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
   wait_vmcnt_lds<0, true>();  // no load may reach LDS after the workgroup has left it
 }
 
-template <class C, bool KTAIL>
+template <class C, bool KTAIL, bool QUANT>
 hipError_t launch_pipe(const MxGemmArgs& g, hipStream_t stream) {
   static std::atomic<bool> done[64] = {};
-  auto kern = mxfp4_pipe_kernel<C, KTAIL>;
+  auto kern = mxfp4_pipe_kernel<C, KTAIL, QUANT>;
   constexpr int lds = C::LDS_BYTES;
   const int dev = current_device();
   // Setting the attribute twice in a race of first calls is harmless.
@@ -702,7 +773,7 @@ hipError_t launch_pipe(const MxGemmArgs& g, hipStream_t stream) {
 template <bool GATED>
 using MxBig = std::conditional_t<GATED, MxTile<256, 256, 4, 2, true>, MxTile<256, 256, 2, 4, false>>;
 
-template <bool GATED>
+template <bool GATED, bool QUANT = false>
 hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   if (g.cap_rows == 0) return hipSuccess;
   const int cus = device_cu_count(current_device());
@@ -716,10 +787,10 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   // rows 35 and 42 / 45 and 43, at 64 rows 60 and 44 / 70 and 45; of 128 experts at 32 rows 65 and 63 / 87 and 60;
   // down projections at 32 rows 24 and 23 / 31 and 25.
   if (fits && g.cap_rows >= (int64_t)32 * g.E) {
-    if (g.K % kStageK != 0 || g.K < kRing * kStageK) return launch_pipe<MxBig<GATED>, true>(g, stream);
-    return launch_pipe<MxBig<GATED>, false>(g, stream);
+    if (g.K % kStageK != 0 || g.K < kRing * kStageK) return launch_pipe<MxBig<GATED>, true, QUANT>(g, stream);
+    return launch_pipe<MxBig<GATED>, false, QUANT>(g, stream);
   }
-  hipLaunchKernelGGL((mxfp4_thin_kernel<GATED, 2>), dim3(cus * 4), dim3(kThinThreads), 0, stream, g);
+  hipLaunchKernelGGL((mxfp4_thin_kernel<GATED, QUANT, 2>), dim3(cus * 4), dim3(kThinThreads), 0, stream, g);
   return hipGetLastError();
 }
 
@@ -734,10 +805,10 @@ hipError_t launch_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_
 
 hipError_t launch_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_s, int64_t x_rows, const int32_t* perm,
                                        int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_s,
-                                       int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf,
-                                       hipStream_t stream) {
-  const MxGemmArgs g{x_q, x_s, perm, k, x_rows, w_q, w_s, 2 * h, h, d, offsets, E, cap_rows, h_buf, h};
-  return launch_products<true>(g, stream);
+                                       int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf, uint8_t* h_q,
+                                       uint8_t* h_s, hipStream_t stream) {
+  const MxGemmArgs g{x_q, x_s, perm, k, x_rows, w_q, w_s, 2 * h, h, d, offsets, E, cap_rows, h_buf, h, h_q, h_s};
+  return h_buf != nullptr ? launch_products<true>(g, stream) : launch_products<true, true>(g, stream);
 }
 
 }  // namespace moe

@@ -200,6 +200,31 @@ def test_up_swiglu(T, k, E, d, h):
     check_up(T, k, E, d, h, seed=T + d)
 
 
+@pytest.mark.parametrize("T,k,E,d,h", [
+    (1, 1, 1, 8, 8), (4, 8, 128, 256, 128), (16, 4, 9, 136, 72), (100, 3, 7, 264, 40), (60, 2, 4, 520, 1000),
+    (1200, 2, 3, 768, 256), (2000, 4, 8, 512, 384), (900, 3, 3, 1032, 520), (700, 2, 5, 264, 8), (3000, 1, 2, 640, 776),
+])
+def test_up_swiglu_quantised(T, k, E, d, h):
+    """The quantising launch writes what quantising the plain launch's rows gives, and nothing past M."""
+    say(f"[gpu] mxfp4 gate/up to mxfp4 T={T} k={k} E={E} d={d} h={h}")
+    rng = np.random.default_rng(T + h)
+    ids = rng.integers(0, E, size=(T, k)).astype(np.int32)
+    ids[rng.random((T, k)) < 0.1] = -1
+    x, _ = packed(rng, (T, d))
+    w, _ = packed(rng, (E, 2 * h, d), 0.1)
+    if T > 50:
+        x.scales[T // 3, 0] = 255  # a NaN row stays one
+    p = moe.moe_permute(torch.zeros((T, 8), dtype=torch.bfloat16, device=DEV), to_dev(ids), E, gather=False)
+    M = int(p.offsets[-1])
+    plain = moe.moe_gemm_up_swiglu_mxfp4(x, p.offsets, w, perm=p.perm, k=k)
+    want = moe.moe_mxfp4_quantize(plain[:M].contiguous())
+    q = torch.full((T * k, moe.mxfp4_row_bytes(h)), 0xAB, dtype=torch.uint8, device=DEV)
+    s = torch.full((T * k, moe.mxfp4_scale_bytes(h)), 0xCD, dtype=torch.uint8, device=DEV)
+    got = moe.moe_gemm_up_swiglu_mxfp4_q(x, p.offsets, w, perm=p.perm, k=k, q=q, scales=s)
+    assert torch.equal(got.scales[:M], want.scales) and torch.equal(got.q[:M], want.q)
+    assert (q[M:] == 0xAB).all() and (s[M:] == 0xCD).all(), "rows past M were written"
+
+
 def test_up_swiglu_all_dropped_and_one_expert():
     say("[gpu] mxfp4 gate/up all dropped, one expert")
     check_up(50, 2, 5, 64, 32, ids=np.full((50, 2), -1, np.int32))
@@ -278,6 +303,8 @@ def test_whole_step_and_its_graph():
     xq = moe.moe_mxfp4_quantize(x)
     h_buf = moe.moe_gemm_up_swiglu_mxfp4(xq, p.offsets, w_ug, perm=p.perm, k=k)
     hq = moe.moe_mxfp4_quantize(h_buf)
+    fused = moe.moe_gemm_up_swiglu_mxfp4_q(xq, p.offsets, w_ug, perm=p.perm, k=k)
+    assert torch.equal(hq.q[:M], fused.q[:M]) and torch.equal(hq.scales[:M], fused.scales[:M])
     yp = moe.moe_grouped_projection_mxfp4(hq, p.offsets, w_down)
     assert torch.equal(moe.moe_unpermute(yp, p.inv_map, rw), y) and not y[7].any()
     # against 64 bits, from the quantised activations that the step itself made

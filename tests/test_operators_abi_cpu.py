@@ -121,7 +121,12 @@ def up(lib, xq=FAKE, xs=FAKE, offs=FAKE, wq=FAKE, ws=FAKE, cap=16, d_in=64, d_ou
     return lib.moe_gemm_up_swiglu_mxfp4(xq, xs, perm, cap, k, offs, wq, ws, d_in, d_out, E, out, None)
 
 
-@pytest.mark.parametrize("fn", [projection, up])
+def up_q(lib, xq=FAKE, xs=FAKE, offs=FAKE, wq=FAKE, ws=FAKE, cap=16, d_in=64, d_out=24, E=2, out=FAKE, perm=FAKE, k=2,
+         out_s=FAKE):
+    return lib.moe_gemm_up_swiglu_mxfp4_q(xq, xs, perm, cap, k, offs, wq, ws, d_in, d_out, E, out, out_s, None)
+
+
+@pytest.mark.parametrize("fn", [projection, up, up_q])
 @pytest.mark.parametrize("kw,status", [
     (dict(cap=-1), SHAPE), (dict(d_in=12), SHAPE), (dict(d_out=4), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE),
     (dict(d_in=(1 << 20) + 8), SHAPE), (dict(d_out=(1 << 20) + 8), SHAPE), (dict(cap=2**31), SHAPE),
@@ -137,7 +142,9 @@ def test_mxfp4_up_gather_validation(lib):
     assert up(lib, k=0) == SHAPE and up(lib, cap=2**30, k=2) == SHAPE and up(lib, perm=FAKE + 2) == ALIGN
     assert up(lib, perm=None, k=2) == SHAPE  # sorted rows are taken one by one
     assert up(lib, perm=None, k=1) in (OK, DEV)
+    assert up_q(lib, out_s=None) == NULLP and up_q(lib, out_s=FAKE + 8) == ALIGN and up_q(lib, perm=None, k=2) == SHAPE
     assert projection(lib, cap=0, xq=None, xs=None, out=None) in (OK, DEV)
+    assert up_q(lib, cap=0, xq=None, xs=None, out=None, out_s=None) in (OK, DEV)
 
 
 def test_binding_refusals_without_a_gpu():
