@@ -13,6 +13,12 @@
  *   moe_unpermute          atomic-free gather + weighted reduction back to
  *                          token order through the inverse map.
  *
+ * Before them stands the router (moe_router_topk: from logits to the routed
+ * experts and their weights; for training its balance and z-losses and the
+ * gradient of the logits). The expert step also runs on MXFP4 experts: rows and
+ * weights quantised to 4-bit floats with shared scales, their grouped products
+ * with fp32 accumulation.
+ *
  * The grouped expert also comes as its two single-launch halves and with the
  * permuted gather fused into the gate/up projection's loads. The backward
  * (Eq 15) adds grouped Dgrad and Wgrad for either weight layout, a plain
@@ -67,9 +73,11 @@ typedef enum moe_status {
   MOE_ERR_NULL_POINTER = 1,       /* a pointer is NULL while its tensor is non-empty           */
   MOE_ERR_BAD_SHAPE = 2,          /* T<0, k<1, E<1 or E>1024, d or h < 8 or not a multiple of 8,
                                      d or h > 2^24 (> 2^20 for the grouped GEMM calls),
-                                     T*k >= 2^31, or cap_rows < 0                               */
-  MOE_ERR_MISALIGNED = 3,         /* a bf16 tensor not 16-byte aligned, or an int32/float
-                                     tensor not 4-byte aligned                                  */
+                                     T*k >= 2^31, or cap_rows < 0; router: k > E or k > 64, or an
+                                     unknown dtype; MXFP4 rows: about 2^40 values               */
+  MOE_ERR_MISALIGNED = 3,         /* a bf16 or MXFP4 tensor not 16-byte aligned, or an
+                                     int32/float tensor not 4-byte aligned (router logits:
+                                     their element size; its workspace: 16 bytes)               */
   MOE_ERR_WORKSPACE = 4,          /* workspace_bytes below the call's *_workspace_bytes()       */
   MOE_ERR_UNSUPPORTED_DEVICE = 5, /* the current HIP device is not gfx950, or no device         */
   MOE_ERR_LAUNCH = 6,             /* a HIP error was reported while launching                    */
@@ -419,7 +427,7 @@ moe_status moe_router_backward(const void* logits, int32_t dtype, int64_t T, int
 size_t moe_mxfp4_row_bytes(int64_t K);
 size_t moe_mxfp4_scale_bytes(int64_t K);
 
-/* x bf16 [rows, K] to q and scales, one launch. */
+/* x bf16 [rows, K] to q and scales, one launch (several from 2^36 values). */
 moe_status moe_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
                               hipStream_t stream);
 
@@ -428,12 +436,13 @@ moe_status moe_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_
 moe_status moe_mxfp4_quantize_weights(const uint16_t* w, int32_t w_layout, int64_t d_in, int64_t d_out, int32_t E,
                                       uint8_t* q, uint8_t* scales, hipStream_t stream);
 
-/* Packed rows back to bf16 [rows, K] (exact), one launch. */
+/* Packed rows back to bf16 [rows, K] (exact), one launch (several from 2^36 values). */
 moe_status moe_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
                                 hipStream_t stream);
 
 /* moe_grouped_projection with MXFP4 rows and weights: y[rows_e] = bf16(x[rows_e] W_e^T),
- * products exact, fp32 accumulation, one rounding.
+ * products exact wherever they are normal fp32 numbers, fp32 accumulation, one
+ * rounding.
  *
  *   x_q, x_scales  [cap_rows] rows of d_in values
  *   offsets        int32 [E+1], clamped as in the bf16 calls

@@ -59,7 +59,7 @@ moe_status check_router_shape(int32_t dtype, int64_t T, int32_t E, int32_t k) {
   return MOE_OK;
 }
 
-// Rows the quantising launches take: their workgroups (512 pieces of 8 values or more) are counted in 31 bits.
+// Rows the quantising calls take: up to 2^40 values or so, far more than memory holds, so that sizes stay inside 64 bits.
 inline bool bad_mxfp4_rows(int64_t rows, int64_t K) {
   return rows < 0 || bad_width(K) || rows > (kMaxSlots * 512) / (mx_blocks(K) * 4);
 }

@@ -158,13 +158,30 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint8_
 
 }  // namespace
 
+namespace {
+
+// A launch has at most 2^32 - 1 work items; rows of more pieces (2^36 values and up) take several.
+template <typename F>
+hipError_t by_rows(int64_t rows, int64_t items_per_row, int chunks, F&& launch) {
+  const int64_t span = (int64_t)kThreads * chunks;
+  const int64_t most = ((int64_t(1) << 32) / kThreads - 1) * span / items_per_row;  // K <= 2^24: at least 2^10 rows
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t n = rows - r0 < most ? rows - r0 : most;
+    launch(r0, n, dim3((unsigned)((n * items_per_row + span - 1) / span)));
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess) return st;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
 hipError_t launch_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* scales,
                                  hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
-  const int64_t span = (int64_t)kThreads * kQuantizeChunks;
-  const int64_t blocks = (rows * mx_blocks(K) * 4 + span - 1) / span;
-  hipLaunchKernelGGL(mxfp4_quantize_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, x, rows, K, q, scales);
-  return hipGetLastError();
+  return by_rows(rows, mx_blocks(K) * 4, kQuantizeChunks, [&](int64_t r0, int64_t n, dim3 grid) {
+    hipLaunchKernelGGL(mxfp4_quantize_kernel, grid, dim3(kThreads), 0, stream, x + r0 * K, n, K, q + r0 * mx_row_bytes(K),
+                       scales + r0 * mx_scale_bytes(K));
+  });
 }
 
 hipError_t launch_mxfp4_quantize_columns(const uint16_t* x, int64_t K, int64_t N, int32_t E, uint8_t* q,
@@ -177,11 +194,10 @@ hipError_t launch_mxfp4_quantize_columns(const uint16_t* x, int64_t K, int64_t N
 
 hipError_t launch_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
                                    hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
-  const int64_t span = (int64_t)kThreads * kDequantizeChunks;
-  const int64_t blocks = (rows * (K / 8) + span - 1) / span;
-  hipLaunchKernelGGL(mxfp4_dequantize_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, q, scales, rows, K, x);
-  return hipGetLastError();
+  return by_rows(rows, K / 8, kDequantizeChunks, [&](int64_t r0, int64_t n, dim3 grid) {
+    hipLaunchKernelGGL(mxfp4_dequantize_kernel, grid, dim3(kThreads), 0, stream, q + r0 * mx_row_bytes(K),
+                       scales + r0 * mx_scale_bytes(K), n, K, x + r0 * K);
+  });
 }
 
 }  // namespace moe
