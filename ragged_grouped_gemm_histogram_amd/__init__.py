@@ -113,11 +113,12 @@ def _stream(t: torch.Tensor) -> int:
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()  # 0, NULL to the library, without elements
 
 
 def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> torch.Tensor:
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device
+    # (one device index compared instead of device objects: a CPU tensor's is -1, a CPU device's None)
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device.index
             and t.is_contiguous()):
         return t
     if not isinstance(t, torch.Tensor):
@@ -517,13 +518,14 @@ class Routed:
 def _logits(logits: torch.Tensor, k: int):
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
-    if logits.dtype not in _LOGITS:
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    T, E = logits.shape
-    _want(logits, "logits", logits.dtype, (T, E), logits.device)
-    if not 1 <= int(k) <= min(E, ROUTER_MAX_TOPK):
+    dtype, dev, (T, E) = logits.dtype, logits.device, logits.shape
+    code = _LOGITS.get(dtype)
+    if code is None:
+        raise TypeError(f"logits must be bfloat16 or float32, got {dtype}")
+    _want(logits, "logits", dtype, (T, E), dev)
+    if not (1 <= k <= E and k <= ROUTER_MAX_TOPK):
         raise ValueError(f"k must be between 1 and min(E, {ROUTER_MAX_TOPK}), got {k} for E = {E}")
-    return T, E, _LOGITS[logits.dtype], logits.device
+    return T, E, code, dev
 
 
 def moe_router_topk(logits: torch.Tensor, k: int, *, renormalize: bool = True, expert_ids=None, routing_w=None,
