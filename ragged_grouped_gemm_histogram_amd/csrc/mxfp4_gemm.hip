@@ -49,7 +49,7 @@ __device__ __forceinline__ i32x8 fp4_operand(const u32x4& v) {
 __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t cap) { return v < 0 ? 0 : (v > cap ? cap : v); }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows per expert: 32 rows by 64 weight rows a workgroup, operands straight from memory to
+// Few rows per expert, or few tiles: 32 rows by 64 weight rows a workgroup, operands straight from memory to
 // registers, the contraction split over the four waves and joined through LDS. Such a call is bound
 // by reading the weights of the experts that have rows: a wave asks for BATCH units of 128 values
 // before it multiplies them, the weights first, since they do not wait for the dispatch order, and
@@ -65,6 +65,8 @@ __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t cap) { return v 
 constexpr int kThinThreads = 256;
 constexpr int kThinWaves = 4;
 constexpr int kUnit = 128;  // contraction per step: four blocks, two per lane half
+template <bool GATED>
+constexpr int kThinCols = GATED ? 32 : 64;  // output columns of a tile
 
 template <bool GATED, bool QUANT, int BATCH>
 __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs g) {
@@ -112,7 +114,7 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
     if (tid == kThinThreads - 1 && g.E == MOE_MAX_EXPERTS) mt_prefix[g.E] = run;
     __syncthreads();
   }
-  constexpr int kCols = GATED ? 32 : 64;
+  constexpr int kCols = kThinCols<GATED>;
   const int n_tiles = (int)((g.N + kCols - 1) / kCols);
   const int64_t total = (int64_t)mt_prefix[g.E] * n_tiles;
   const int64_t qp = mx_row_bytes(g.K), sp = mx_scale_bytes(g.K);
@@ -789,11 +791,18 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   const int64_t qp = mx_row_bytes(g.K);
   const int64_t a_span = (g.a_rows != nullptr ? g.a_tokens : 256) * qp;
   const bool fits = a_span <= 0x7FFFFFFFll && g.w_rows * qp <= 0x7FFFFFFFll;
-  // From a mean of 32 rows per expert (all the host knows) they are faster however the rows are spread. Thin and
-  // pipelined, evenly spread / skewed: gate/up of 64 experts 2048 x 768 at 16 rows 30 and 42 / 36 and 42 us, at 32
-  // rows 35 and 42 / 45 and 43, at 64 rows 60 and 44 / 70 and 45; of 128 experts at 32 rows 65 and 63 / 87 and 60;
-  // down projections at 32 rows 24 and 23 / 31 and 25.
-  if (fits && g.cap_rows >= (int64_t)32 * g.E) {
+  // Small tiles while there are at most six of them a CU, one and a half rounds of their launch (the host knows the
+  // capacity, not the spread: half a tile more per expert): their call takes 5 us and up, one of pipelined tiles 10.
+  // Small and pipelined, plain products: 1012 rows of 6 experts 240 -> 32 5.3 and 10.2 us; 4091 rows of 8 experts
+  // 392 -> 520 (1188 small tiles) 9.6 and 13.6; 864 rows of 11 experts 1528 -> 2480 (1209) 27 and 20; 65536 rows of 64
+  // experts 768 -> 2048 532 and 108. And below a mean of 32 rows per expert, where pipelined tiles are mostly empty:
+  // gate/up of 64 experts 2048 -> 2 x 768, evenly spread / skewed, 16 rows 30 and 42 / 36 and 42 us, 32 rows 35 and 42 /
+  // 45 and 43, 64 rows 60 and 44 / 70 and 45. Over 260 calls of random sizes the choice costs 0.6% against the better
+  // of the two (the second condition alone 13%).
+  const int64_t used = g.cap_rows < g.E ? g.cap_rows : g.E;
+  const int64_t small_tiles = (g.cap_rows / 32 + used / 2) * ((g.N + kThinCols<GATED> - 1) / kThinCols<GATED>);
+  const bool small = small_tiles <= (int64_t)6 * cus || g.cap_rows < (int64_t)32 * g.E;
+  if (fits && !small) {
     if (g.K % kStageK != 0 || g.K < kRing * kStageK) return launch_pipe<MxBig<GATED>, true, QUANT>(g, stream);
     return launch_pipe<MxBig<GATED>, false, QUANT>(g, stream);
   }
