@@ -673,10 +673,13 @@ def _mxfp4_experts(x: Mxfp4, offsets: torch.Tensor, w: Mxfp4):
         raise ValueError("expected Mxfp4 rows [rows, .] and Mxfp4 expert weights [E, d_out, .]")
     if x.width != w.width:
         raise ValueError(f"rows of {x.width} values do not fit weights of {w.width}")
-    rows, dev = x.q.shape[0], x.q.device
-    E, w_rows = w.q.shape[:2]
-    _want_mxfp4(x, "x", (rows,), dev)
-    _want_mxfp4(w, "w", (E, w_rows), dev)
+    q, dev = mxfp4_row_bytes(x.width), x.q.device
+    s = mxfp4_scale_bytes(x.width)
+    rows, (E, w_rows, _) = x.q.shape[0], w.q.shape
+    _want(x.q, "x.q", torch.uint8, (rows, q), dev)
+    _want(x.scales, "x.scales", torch.uint8, (rows, s), dev)
+    _want(w.q, "w.q", torch.uint8, (E, w_rows, q), dev)
+    _want(w.scales, "w.scales", torch.uint8, (E, w_rows, s), dev)
     _want(offsets, "offsets", torch.int32, (E + 1,), dev)
     return rows, E, w_rows, dev
 
