@@ -676,7 +676,8 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) bs[j] = KTAIL ? (bs_next[j] >> (16 * hh)) & keep : bs_next[j] >> (16 * hh);
   };
-  constexpr int kProducts = C::FM * C::FN, kReads = 2, kReadProducts = (2 * (C::FM + C::FN) + kReads - 1) / kReads;
+  constexpr int kProducts = C::FM * C::FN, kReadsAll = 2 * (C::FM + C::FN);
+  constexpr int kReads = kReadsAll > 2 * kProducts ? 3 : 2, kReadProducts = (kReadsAll + kReads - 1) / kReads;
   static_assert(kReadProducts <= kProducts && OPS <= kProducts, "the reads and the loads fit between the products");
   auto product = [&](int set, auto ks_c, int m) {
     constexpr int ks = decltype(ks_c)::value;
@@ -791,17 +792,18 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   const int64_t qp = mx_row_bytes(g.K);
   const int64_t a_span = (g.a_rows != nullptr ? g.a_tokens : 256) * qp;
   const bool fits = a_span <= 0x7FFFFFFFll && g.w_rows * qp <= 0x7FFFFFFFll;
-  // Small tiles while there are at most six of them a CU, one and a half rounds of their launch (the host knows the
-  // capacity, not the spread: half a tile more per expert): their call takes 5 us and up, one of pipelined tiles 10.
-  // Small and pipelined, plain products: 1012 rows of 6 experts 240 -> 32 5.3 and 10.2 us; 4091 rows of 8 experts
-  // 392 -> 520 (1188 small tiles) 9.6 and 13.6; 864 rows of 11 experts 1528 -> 2480 (1209) 27 and 20; 65536 rows of 64
-  // experts 768 -> 2048 532 and 108. And below a mean of 32 rows per expert, where pipelined tiles are mostly empty:
-  // gate/up of 64 experts 2048 -> 2 x 768, evenly spread / skewed, 16 rows 30 and 42 / 36 and 42 us, 32 rows 35 and 42 /
-  // 45 and 43, 64 rows 60 and 44 / 70 and 45. Over 260 calls of random sizes the choice costs 0.6% against the better
-  // of the two (the second condition alone 13%).
+  // Small tiles while there are few of them: a call of small tiles takes 5 us and up, one of pipelined tiles 10, but a
+  // pipelined tile does 16 times the work in 2 to 4 times a small one's time. (The host knows the capacity, not the
+  // spread: half a tile more per expert.) The limit is 3 + 3000 / (K + 256) a CU; small and pipelined, plain products:
+  // 1012 rows of 6 experts 240 -> 32 5.3 and 10.2 us; 4091 rows of 8 experts 392 -> 520 (1188 small tiles) 9.6 and 13.6;
+  // 3706 rows of 81 experts 120 -> 976 (2480) 13.2 and 16.9; 4284 rows of 3 experts 392 -> 1432 (3082) 19 and 17; 864
+  // rows of 11 experts 1528 -> 2480 (1248) 27 and 20; 65536 rows of 64 experts 768 -> 2048 532 and 108. And below a mean
+  // of 32 rows per expert, where pipelined tiles are mostly empty: gate/up of 64 experts 2048 -> 2 x 768, evenly spread /
+  // skewed, 16 rows 30 and 42 / 36 and 42 us, 32 rows 35 and 42 / 45 and 43, 64 rows 60 and 44 / 70 and 45. Over 430
+  // calls of random sizes the choice costs 0.3% against the better of the two (the second condition alone 10%).
   const int64_t used = g.cap_rows < g.E ? g.cap_rows : g.E;
   const int64_t small_tiles = (g.cap_rows / 32 + used / 2) * ((g.N + kThinCols<GATED> - 1) / kThinCols<GATED>);
-  const bool small = small_tiles <= (int64_t)6 * cus || g.cap_rows < (int64_t)32 * g.E;
+  const bool small = small_tiles * (g.K + 256) <= cus * (3 * (g.K + 256) + 3000) || g.cap_rows < (int64_t)32 * g.E;
   if (fits && !small) {
     if (g.K % kStageK != 0 || g.K < kRing * kStageK) return launch_pipe<MxBig<GATED>, true, QUANT>(g, stream);
     return launch_pipe<MxBig<GATED>, false, QUANT>(g, stream);

@@ -191,7 +191,7 @@ def test_projection_many_rows(counts, K, N):
 
 
 @pytest.mark.parametrize("T,k,E,d,h", [
-    (1, 1, 1, 8, 8), (1, 8, 128, 256, 128), (4, 8, 128, 2048, 768), (16, 4, 9, 136, 72), (100, 3, 7, 264, 40),
+    (1, 1, 1, 8, 8), (1, 8, 128, 256, 128), (4, 8, 24, 2048, 768), (16, 4, 9, 136, 72), (100, 3, 7, 264, 40),
     (300, 2, 4, 520, 264), (1200, 2, 3, 768, 256), (2000, 4, 8, 512, 384), (640, 8, 64, 256, 96), (3000, 1, 2, 2880, 136),
     (900, 3, 3, 1032, 1000),
 ])
