@@ -16,9 +16,12 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-// Pieces of 8 values a thread has in flight, measured on 65536 x 2048: quantising 2 of them 67 us
-// (4: 73, 8: 78), reading back 4 of them 62 us (2: 68, 8: 65); 340 MB either way.
-constexpr int kQuantizeChunks = 2, kDequantizeChunks = 4;
+// Pieces of 8 values a thread has in flight. The bf16 side is streamed (non-temporal: it is read or
+// written once, and passes the caches by). Measured on 65536 x 2048, 340 MB either way: quantising 2
+// pieces 61 to 65 us (1: 61, 4: 65; with ordinary loads 63 to 66), reading back 2 pieces 48.5 us
+// (4: 50, 8: 51; with ordinary stores 62). At 4096 x 2048, between kernels that write the input and
+// read the output, streaming costs nothing (15.0 and 15.1 us for the pair, 15.3 and 15.7 without).
+constexpr int kQuantizeChunks = 2, kDequantizeChunks = 2;
 
 // Rows of K-contiguous values. Work item: 8 consecutive values of a row padded to whole blocks; a
 // workgroup takes kThreads * kQuantizeChunks consecutive items.
@@ -45,7 +48,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_quantize_kernel(const uint16_t
     row[i] = row0 + r;
     chunk[i] = c;
     v[i] = u32x4{0u, 0u, 0u, 0u};
-    if (row[i] < rows && (int64_t)c * 8 < K) v[i] = *reinterpret_cast<const u32x4*>(x + row[i] * K + (int64_t)c * 8);
+    if (row[i] < rows && (int64_t)c * 8 < K) v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + row[i] * K + (int64_t)c * 8));
   }
   const int64_t qp = mx_row_bytes(K), sp = mx_scale_bytes(K);
 #pragma unroll
@@ -69,8 +72,9 @@ __global__ __launch_bounds__(kThreads) void mxfp4_quantize_kernel(const uint16_t
 // Weights stored with the contraction outermost, [E, K, N]: the packed rows are the columns. A
 // workgroup turns 128 columns of 16 blocks (512 k): a lane takes two neighbouring columns of one
 // block at a time (4-byte loads, 256 contiguous bytes a wave), and the packed rows leave through LDS,
-// 256 bytes of values and 16 of scales each. (Written from the lanes that made them, 16 bytes and one
-// byte a row, the scattered stores cost 114 us for 16 x 2880 x 2880, the single bytes 20 of them.)
+// 256 bytes of values and 16 of scales each. 16 x 2880 x 2880 (336 MB) take 65 us, 5.2 TB/s: with
+// ordinary loads 81, with four columns a lane (8-byte loads, half the blocks) 68; with the rows
+// written from the lanes that made them, 16 bytes and one byte a row, 114, the single bytes 20 of them.
 constexpr int kTileCols = 128, kTileBlocks = 16, kRowPitch = kTileBlocks * 16 + 16;
 
 __global__ __launch_bounds__(kThreads) void mxfp4_quantize_columns_kernel(const uint16_t* __restrict__ x, int64_t K, int64_t N,
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_quantize_columns_kernel(const 
     const uint16_t* src = x + (e * K + k0) * N + n;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      v[i] = n < N && k0 + i < K ? *reinterpret_cast<const uint32_t*>(src + (int64_t)i * N) : 0u;
+      v[i] = n < N && k0 + i < K ? __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(src + (int64_t)i * N)) : 0u;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       u32x4 part[4], out;
@@ -153,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint8_
   }
 #pragma unroll
   for (int i = 0; i < kDequantizeChunks; ++i)
-    if (at[i] >= 0) *reinterpret_cast<u32x4*>(x + at[i]) = from_fp4(code[i], byte[i]);
+    if (at[i] >= 0) __builtin_nontemporal_store(from_fp4(code[i], byte[i]), reinterpret_cast<u32x4*>(x + at[i]));
 }
 
 }  // namespace
