@@ -26,9 +26,13 @@ namespace moe {
 namespace {
 
 constexpr int kPlainThreads = 256;
-// With the losses a workgroup leaves one partial sum per column: 8 waves, and at most two such
-// workgroups a CU, so that they fill the device and the second launch has few partials to add.
-constexpr int kLossThreads = 512;
+// With the losses a workgroup leaves one partial sum per column, and the second launch adds them in
+// one workgroup: at most one large workgroup a CU, of 8 waves while those hold all tokens at once, of
+// 16 beyond. Both launches of 65537 tokens of 100 experts 28 us (two workgroups of 8 waves a CU: 30,
+// one: 34), of 8192 tokens of 256 experts 19 us (24 and 20), of 4096 tokens of 128 experts (8 waves,
+// 128 workgroups) 11.4 us (16 waves: 12.7).
+constexpr int64_t kLossBlocks = 256;
+constexpr int kLossThreads = 512, kLossThreadsMany = 1024;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -197,9 +201,8 @@ struct RouterArgs {
 // Words of a workgroup's partial sums, padded to whole 16 bytes.
 __host__ __device__ constexpr int64_t partial_words(int E) { return (2 * (int64_t)E + 2 + 3) / 4 * 4; }
 
-template <typename T, int G, int V, bool LOSSES>
-__global__ __launch_bounds__(LOSSES ? kLossThreads : kPlainThreads) void router_topk_kernel(RouterArgs a) {
-  constexpr int kThreads = LOSSES ? kLossThreads : kPlainThreads;
+template <typename T, int G, int V, bool LOSSES, int kThreads>
+__global__ __launch_bounds__(kThreads) void router_topk_kernel(RouterArgs a) {
   constexpr int kGroups = kThreads / G;  // tokens a workgroup holds at once
   constexpr int kSlots = MOE_ROUTER_MAX_TOPK;
   constexpr int kSelWords = 2 * kGroups * kSlots, kSumWords = LOSSES ? kGroups * G * V : 1;
@@ -305,6 +308,7 @@ __global__ __launch_bounds__(LOSSES ? kLossThreads : kPlainThreads) void router_
     uint32_t* out = a.partial + blockIdx.x * partial_words(a.E);
     for (int e = tid; e < a.E; e += kThreads) {
       float sum = 0.f;
+#pragma unroll 16
       for (int q = 0; q < kGroups; ++q) sum += colsum[q * (G * V) + e];
       out[e] = __builtin_bit_cast(uint32_t, sum);
       out[a.E + e] = (uint32_t)hist[e];
@@ -312,6 +316,7 @@ __global__ __launch_bounds__(LOSSES ? kLossThreads : kPlainThreads) void router_
     if (tid == 0) {
       float z = 0.f;
       int n = 0;
+#pragma unroll 16
       for (int q = 0; q < kGroups; ++q) {
         z += zsum_s[q];
         n += tokens_s[q];
@@ -338,14 +343,14 @@ __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uin
   __shared__ int wave_i[kFinishThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int quads = (int)(partial_words(E) / 4);
-  const int R = kFinishThreads / quads;  // slices (quads <= 513)
+  constexpr int kBatch = 16;
+  const int R = min(kFinishThreads / quads, (blocks + kBatch - 1) / kBatch);  // slices (quads <= 513)
   const int quad = tid % quads, slice = tid / quads;
   const u32x4* src = reinterpret_cast<const u32x4*>(partial);
   auto is_float = [&](int w) { return w < E || w == 2 * E; };  // P sums and the sum of lse^2; else counts and tokens
   float f[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t c[4] = {0u, 0u, 0u, 0u};
   if (slice < R) {
-    constexpr int kBatch = 16;
     for (int b0 = slice; b0 < blocks; b0 += R * kBatch) {
       u32x4 v[kBatch];
 #pragma unroll
@@ -365,26 +370,27 @@ __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uin
     slice_sum[slice * quads + quad] = out;
   }
   __syncthreads();
+  // the slices' sums in order: of this thread's expert, and of lse^2 and the tokens (neighbouring words)
   const uint32_t* words = reinterpret_cast<const uint32_t*>(slice_sum);
-  auto total_f = [&](int w) {
-    float sum = 0.f;
-    for (int q = 0; q < R; ++q) sum += __uint_as_float(words[q * quads * 4 + w]);
-    return sum;
-  };
-  auto total_i = [&](int w) {
-    int sum = 0;
-    for (int q = 0; q < R; ++q) sum += (int)words[q * quads * 4 + w];
-    return sum;
-  };
-  const int n = total_i(2 * E + 1);
+  const int expert = tid < E ? tid : 0;
+  float p_sum = 0.f, z_sum = 0.f;
+  int count = 0, n = 0;
+#pragma unroll 8
+  for (int q = 0; q < R; ++q) {
+    const uint32_t* at = words + q * quads * 4;
+    const uint2 zn = *reinterpret_cast<const uint2*>(at + 2 * E);
+    p_sum += __uint_as_float(at[expert]);
+    count += (int)at[E + expert];
+    z_sum += __uint_as_float(zn.x);
+    n += (int)zn.y;
+  }
   const float nf = (float)(n > 0 ? n : 1);
-  float mean = 0.f;
-  int count = 0;
+  const float mean = tid < E ? p_sum / nf : 0.f;
   if (tid < E) {
-    mean = total_f(tid) / nf;
-    count = total_i(E + tid);
     counts[tid] = count;
     prob_mean[tid] = mean;
+  } else {
+    count = 0;
   }
   // sum of counts and of counts_e P_e over the experts
   float dot = (float)count * mean;
@@ -408,7 +414,7 @@ __global__ __launch_bounds__(kFinishThreads) void router_losses_kernel(const uin
     }
     tokens[0] = n;
     losses[0] = (float)E * dot / (float)(total > 0 ? total : 1);
-    losses[1] = total_f(2 * E) / nf;
+    losses[1] = z_sum / nf;
   }
 }
 
@@ -546,8 +552,9 @@ int64_t router_blocks(int64_t T, int groups, int64_t cap) {
 // experts: selection 21.0 instead of 22.4 us, gradient 19.2 instead of 17.3.)
 int lanes_of(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
 
-// The losses' first launch leaves one partial a workgroup, which the second reads in one workgroup.
-constexpr int64_t kLossBlocks = 512;
+int loss_threads(int64_t T, int E) { return T * lanes_of(E) <= kLossBlocks * kLossThreads ? kLossThreads : kLossThreadsMany; }
+
+int64_t loss_blocks(int64_t T, int E) { return router_blocks(T, loss_threads(T, E) / lanes_of(E), kLossBlocks); }
 
 template <typename F>
 hipError_t by_width(int E, F&& f) {
@@ -565,7 +572,7 @@ bool wide_rows(const void* p, int E, bool f32) {
 }  // namespace
 
 int64_t router_partial_words(int64_t T, int32_t E) {
-  return router_blocks(T, kLossThreads / lanes_of(E), kLossBlocks) * partial_words(E);
+  return loss_blocks(T, E) * partial_words(E);
 }
 
 hipError_t launch_router_topk(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renormalize,
@@ -576,8 +583,8 @@ hipError_t launch_router_topk(const void* logits, bool f32, int64_t T, int32_t E
   return by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     const dim3 grid((unsigned)router_blocks(T, kPlainThreads / G, cap));
-    if (f32) hipLaunchKernelGGL((router_topk_kernel<float, G, V, false>), grid, dim3(kPlainThreads), 0, stream, a);
-    else hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, false>), grid, dim3(kPlainThreads), 0, stream, a);
+    if (f32) hipLaunchKernelGGL((router_topk_kernel<float, G, V, false, kPlainThreads>), grid, dim3(kPlainThreads), 0, stream, a);
+    else hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, false, kPlainThreads>), grid, dim3(kPlainThreads), 0, stream, a);
     return hipGetLastError();
   });
 }
@@ -586,14 +593,18 @@ hipError_t launch_router_topk_losses(const void* logits, bool f32, int64_t T, in
                                      int32_t* ids, float* w, float* lse, int32_t* counts, int32_t* tokens,
                                      float* prob_mean, float* losses, uint32_t* partial, hipStream_t stream) {
   const RouterArgs a{logits, T, E, k, renormalize, wide_rows(logits, E, f32), ids, w, lse, partial};
-  const int64_t blocks = router_blocks(T, kLossThreads / lanes_of(E), kLossBlocks);
+  const int64_t blocks = loss_blocks(T, E);
+  const bool many = loss_threads(T, E) == kLossThreadsMany;
   const hipError_t st = by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
-    if (f32)
-      hipLaunchKernelGGL((router_topk_kernel<float, G, V, true>), dim3((unsigned)blocks), dim3(kLossThreads), 0, stream, a);
-    else
-      hipLaunchKernelGGL((router_topk_kernel<uint16_t, G, V, true>), dim3((unsigned)blocks), dim3(kLossThreads), 0, stream, a);
-    return hipGetLastError();
+    auto launch = [&](auto kernel, int threads) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, a);
+      return hipGetLastError();
+    };
+    if (f32) return many ? launch(router_topk_kernel<float, G, V, true, kLossThreadsMany>, kLossThreadsMany)
+                         : launch(router_topk_kernel<float, G, V, true, kLossThreads>, kLossThreads);
+    return many ? launch(router_topk_kernel<uint16_t, G, V, true, kLossThreadsMany>, kLossThreadsMany)
+                : launch(router_topk_kernel<uint16_t, G, V, true, kLossThreads>, kLossThreads);
   });
   if (st != hipSuccess) return st;
   hipLaunchKernelGGL(router_losses_kernel, dim3(1), dim3(kFinishThreads), 0, stream, partial, (int)blocks, E, counts,
