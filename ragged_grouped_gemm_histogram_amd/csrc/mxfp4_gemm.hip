@@ -448,7 +448,9 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
   const int hh = lane >> 5;
 
-  // prefix of the experts' row-tile counts, from the offsets clamped to the capacity
+  // prefix of the experts' row-tile counts, from the offsets clamped to the capacity (kept in the ring's memory until
+  // the first loads)
+  int2* first_offsets = reinterpret_cast<int2*>(smem);
   {
     constexpr int kPer = MOE_MAX_EXPERTS / C::THREADS;
     int mt[kPer], sum = 0;
@@ -458,6 +460,7 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       mt[i] = 0;
       if (e < g.E) {
         const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
+        first_offsets[e] = int2{(int)lo, (int)hi};
         mt[i] = hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0;
       }
       sum += mt[i];
@@ -471,7 +474,8 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
     if (lane == 63) pl.wave_total[wave] = incl;
     __syncthreads();
     int run = incl - sum;
-    for (int w = 0; w < wave; ++w) run += pl.wave_total[w];
+#pragma unroll
+    for (int w = 0; w < C::NWAVES; ++w) run += w < wave ? pl.wave_total[w] : 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
@@ -483,18 +487,20 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
   }
   const int total_mt = pl.mt_prefix[g.E];
   const int n_tiles = (int)((g.N + TILE_N - 1) / TILE_N);
-  const int64_t total_tiles = (int64_t)total_mt * n_tiles;
-  const int64_t t0 = logical_worker();
+  // (tiles are counted in 31 bits: more have no memory to be stored in)
+  const int64_t tiles64 = (int64_t)total_mt * n_tiles;
+  const uint32_t total_tiles = (uint32_t)(tiles64 < 0 ? 0 : (tiles64 > 0x7FFFFFFF ? 0x7FFFFFFF : tiles64));
+  const uint32_t t0 = (uint32_t)logical_worker();
   if (t0 >= total_tiles) return;
-  const int64_t my_tiles = (total_tiles - t0 + gridDim.x - 1) / gridDim.x;
+  const uint32_t my_tiles = (total_tiles - t0 + gridDim.x - 1) / gridDim.x;
 
   // Coordinates of this workgroup's tiles [from, from + kTableTiles), one a lane of the first wave.
   // Groups of kGroupRows row tiles sweep every column tile before the next group starts, so tiles that
   // run at the same time share rows and weights.
-  auto fill_table = [&](int64_t from) {
+  auto fill_table = [&](uint32_t from, auto block_of) {
     if (tid < kTableTiles && from + tid < my_tiles) {
-      const int64_t t = t0 + (from + tid) * gridDim.x;
-      const int64_t span = (int64_t)kGroupRows * n_tiles, grp = t / span;
+      const uint32_t t = t0 + (from + tid) * gridDim.x;
+      const uint32_t span = (uint32_t)kGroupRows * (uint32_t)n_tiles, grp = t / span;
       const int in_group = (int)(t - grp * span);
       const int g0 = (int)grp * kGroupRows;
       const int gsize = total_mt - g0 < kGroupRows ? total_mt - g0 : kGroupRows;
@@ -504,7 +510,8 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
         const int mid = (e + hi_e) >> 1;
         if (pl.mt_prefix[mid] <= gm) e = mid; else hi_e = mid;
       }
-      const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
+      const int2 block = block_of(e);
+      const int64_t lo = block.x, hi = block.y;
       int64_t row0 = lo + (int64_t)(gm - pl.mt_prefix[e]) * BM;
       int64_t rows = hi - row0 < BM ? hi - row0 : BM;
       if (row0 < lo || row0 >= hi) row0 = rows = 0;  // offsets that are no running sum can wrap the tile counts
@@ -512,12 +519,12 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
     }
     __syncthreads();
   };
-  auto coord = [&](int64_t i) {
+  auto coord = [&](uint32_t i) {
     const int4 v = pl.table[i % kTableTiles];
     return MxCoord{__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
                    __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w)};
   };
-  fill_table(0);
+  fill_table(0, [&](int e) { return first_offsets[e]; });
 
   const int blocks = (int)mx_blocks(g.K);
   // stages: at least four, so that loads run at most one tile ahead (what lies past the row is zeros)
@@ -696,20 +703,22 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
   set_tile(tc);
 #pragma unroll
   for (int q = 0; q < kRing; ++q) issue_part(q * C::STAGE_BYTES, 0, 1);
-  wait_vmcnt_lds<0, true>();
+  wait_vmcnt_lds<3 * OPS, true>();  // the first stage and its scales
   bare_barrier();
   uint32_t ring = 0;      // where in the ring the stage being multiplied is
   uint32_t scale_at = 0;  // and its scales' words
   load_scales(0);
   load_frags(0, 0, 0);
   take_scales(0);
-  for (int64_t i_tile = 0;; ++i_tile) {
+  for (uint32_t i_tile = 0;; ++i_tile) {
     const bool more = i_tile + 1 < my_tiles;
     MxCoord next = tc;  // behind the last tile its own first stages are loaded once more, for no use
     if (more) {
       if ((i_tile + 1) % kTableTiles == 0) {
         __syncthreads();  // every wave has read the last entry
-        fill_table(i_tile + 1);
+        fill_table(i_tile + 1, [&](int e) {
+          return int2{(int)clamp_row(g.offsets[e], g.cap_rows), (int)clamp_row(g.offsets[e + 1], g.cap_rows)};
+        });
       }
       next = coord(i_tile + 1);
       if (gather) fetch_slots(next);
@@ -731,9 +740,8 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       // place takes the stage four on, loaded between the products (a wave waiting to issue a load
       // leaves the matrix unit to the other wave of its SIMD). Still under way may be the two stages
       // after the next, and for a tile's first three stages the previous tile's stores, issued behind
-      // this tile's first four (before the first tile there are none, and its four are waited for
-      // above).
-      if (kt < 3) wait_vmcnt_lds<2 * OPS + kTileStores<C, QUANT>, true>();
+      // this tile's first four (before the first tile there are none).
+      if (kt < 3 && i_tile != 0) wait_vmcnt_lds<2 * OPS + kTileStores<C, QUANT>, true>();
       else wait_vmcnt_lds<2 * OPS, true>();
       bare_barrier();
       const uint32_t to = ring;
