@@ -381,7 +381,8 @@ size_t moe_router_workspace_bytes(int64_t T, int32_t E);
  *   prob_mean  fp32  [E]  out: P
  *   losses     fp32  [2]  out (both 0 when n = 0)
  *   workspace  device scratch of at least moe_router_workspace_bytes(T, E),
- *              16-byte aligned
+ *              16-byte aligned; calls and graphs that may run at the same time
+ *              need one each
  *
  * Two launches; sums are taken in a fixed order, so results repeat bit for bit. */
 moe_status moe_router_topk_losses(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,

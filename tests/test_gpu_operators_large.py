@@ -189,3 +189,36 @@ def test_two_streams_at_once():
     for i in range(2):
         for out in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_router_gradient_of_experts_chosen_twice(renormalize):
+    """Ids from elsewhere may name an expert more than once, or none: its slots' parts are added up.
+
+    Every term is a product of fp32 numbers below 4 in size with at most k + 3 roundings behind it, and each row adds at
+    most 2 k + 2 of them: (4 k + 8) u of the terms' sizes, beside the weights' own softmax of 2^-18."""
+    say("[gpu] router gradient of repeated ids")
+    T, E, k = 200, 24, 6
+    g = generator(8)
+    x = torch.randn((T, E), generator=g, device=DEV)
+    r = moe.moe_router_topk(x, k, renormalize=renormalize)
+    r.expert_ids = torch.randint(-1, 3, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    r.expert_ids[0] = 5
+    r.expert_ids[1] = -1
+    r.routing_w = torch.rand((T, k), generator=g, device=DEV)
+    dw = torch.randn((T, k), generator=g, device=DEV)
+    first, again = moe.moe_router_backward(x, r, dw), moe.moe_router_backward(x, r, dw)
+    assert torch.equal(first, again)
+    on = (r.expert_ids >= 0).double()
+    w, d, p = r.routing_w.double() * on, dw.double(), torch.softmax(x.double(), 1)
+    total = (w * d).sum(1, keepdim=True)
+    slot = w * ((d - total) if renormalize else d)
+    want = torch.zeros((T, E), dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(want)
+    for j in range(k):
+        want.scatter_add_(1, r.expert_ids[:, j:j + 1].clamp(min=0).long(), slot[:, j:j + 1])
+        size.scatter_add_(1, r.expert_ids[:, j:j + 1].clamp(min=0).long(), w[:, j:j + 1] * (d[:, j:j + 1].abs() + (w * d.abs()).sum(1, keepdim=True)))
+    if not renormalize:
+        want -= p * total
+        size += p * (w * d.abs()).sum(1, keepdim=True)
+    assert ((first.double() - want).abs() <= size * ((4 * k + 8) * 2.0 ** -24 + 2.0 ** -18)).all()
