@@ -102,14 +102,20 @@ def _check(status: int, call: str) -> None:
         raise MoeError(status, call)
 
 
+# Names that every call looks up, bound once.
+_Tensor = torch.Tensor
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(t: torch.Tensor) -> int:
     # The library launches on the current HIP device; a stream of another device would fail the launch.
     # (The raw queries behind torch.cuda.current_device() and current_stream(): two microseconds less a call.)
     index = t.get_device()
-    if index != torch._C._cuda_getDevice():
+    if index != _current_device():
         raise ValueError(f"tensors are on {t.device} but the current device is cuda:{torch.cuda.current_device()}; "
                          "call inside torch.cuda.device(...)")
-    return torch._C._cuda_getCurrentRawStream(index)
+    return _raw_stream(index)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -118,7 +124,7 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> torch.Tensor:
     # (one device index compared instead of device objects: a CPU tensor's is -1, a CPU device's None)
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device.index
+    if (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device.index
             and t.is_contiguous()):
         return t
     if not isinstance(t, torch.Tensor):
@@ -137,6 +143,9 @@ def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) 
 def _out(t, name, dtype, shape, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device.index
+            and t.is_contiguous()):
+        return t
     return _want(t, name, dtype, shape, device)
 
 
@@ -536,8 +545,8 @@ def moe_router_topk(logits: torch.Tensor, k: int, *, renormalize: bool = True, e
     expert_ids = _out(expert_ids, "expert_ids", torch.int32, (T, k), dev)
     routing_w = _out(routing_w, "routing_w", torch.float32, (T, k), dev)
     lse = _out(lse, "lse", torch.float32, (T,), dev)
-    _check(load_library().moe_router_topk(_ptr(logits), dtype, T, E, k, int(renormalize), _ptr(expert_ids),
-                                          _ptr(routing_w), _ptr(lse), _stream(logits)), "moe_router_topk")
+    _check(load_library().moe_router_topk(logits.data_ptr(), dtype, T, E, k, int(renormalize), expert_ids.data_ptr(),
+                                          routing_w.data_ptr(), lse.data_ptr(), _stream(logits)), "moe_router_topk")
     return Routed(expert_ids, routing_w, lse, bool(renormalize))
 
 
@@ -565,9 +574,10 @@ def moe_router_topk_losses(logits: torch.Tensor, k: int, *, renormalize: bool = 
         workspace = torch.empty((router_workspace_bytes(T, E),), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
-    _check(load_library().moe_router_topk_losses(_ptr(logits), dtype, T, E, k, int(renormalize), _ptr(expert_ids),
-                                                 _ptr(routing_w), _ptr(lse), _ptr(counts), _ptr(tokens),
-                                                 _ptr(prob_mean), _ptr(losses), _ptr(workspace), workspace.numel(),
+    _check(load_library().moe_router_topk_losses(logits.data_ptr(), dtype, T, E, k, int(renormalize),
+                                                 expert_ids.data_ptr(), routing_w.data_ptr(), lse.data_ptr(),
+                                                 counts.data_ptr(), tokens.data_ptr(), prob_mean.data_ptr(),
+                                                 losses.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                                  _stream(logits)), "moe_router_topk_losses")
     return Routed(expert_ids, routing_w, lse, bool(renormalize), counts, tokens, prob_mean, losses)
 
@@ -590,9 +600,9 @@ def moe_router_backward(logits: torch.Tensor, routed: Routed, d_routing_w: torch
         _want(routed.counts, "counts", torch.int32, (E,), dev)
         _want(routed.tokens, "tokens", torch.int32, (1,), dev)
     d_logits = _out(d_logits, "d_logits", logits.dtype, (T, E), dev)
-    _check(load_library().moe_router_backward(_ptr(logits), dtype, T, E, k, int(routed.renormalize),
-                                              _ptr(routed.expert_ids), _ptr(routed.routing_w), _ptr(routed.counts),
-                                              _ptr(routed.tokens), _ptr(d_routing_w), _ptr(d_losses), _ptr(d_logits),
+    _check(load_library().moe_router_backward(logits.data_ptr(), dtype, T, E, k, int(routed.renormalize),
+                                              routed.expert_ids.data_ptr(), routed.routing_w.data_ptr(), _ptr(routed.counts),
+                                              _ptr(routed.tokens), _ptr(d_routing_w), _ptr(d_losses), d_logits.data_ptr(),
                                               _stream(logits)), "moe_router_backward")
     return d_logits
 
@@ -635,7 +645,7 @@ def moe_mxfp4_quantize(x: torch.Tensor, *, q=None, scales=None) -> Mxfp4:
     rows = 1
     for n in lead:
         rows *= n
-    _check(load_library().moe_mxfp4_quantize(_ptr(x), rows, K, _ptr(q), _ptr(scales), _stream(x)),
+    _check(load_library().moe_mxfp4_quantize(x.data_ptr(), rows, K, q.data_ptr(), scales.data_ptr(), _stream(x)),
            "moe_mxfp4_quantize")
     return Mxfp4(q, scales, K)
 
@@ -648,8 +658,8 @@ def moe_mxfp4_quantize_weights(w: torch.Tensor, layout: str = "in_out", *, q=Non
     _want(w, "w", torch.bfloat16, tuple(w.shape), dev)
     q = _out(q, "q", torch.uint8, (E, d_out, mxfp4_row_bytes(d_in)), dev)
     scales = _out(scales, "scales", torch.uint8, (E, d_out, mxfp4_scale_bytes(d_in)), dev)
-    _check(load_library().moe_mxfp4_quantize_weights(_ptr(w), W_LAYOUTS[layout], d_in, d_out, E, _ptr(q), _ptr(scales),
-                                                     _stream(w)), "moe_mxfp4_quantize_weights")
+    _check(load_library().moe_mxfp4_quantize_weights(w.data_ptr(), W_LAYOUTS[layout], d_in, d_out, E, q.data_ptr(),
+                                                     scales.data_ptr(), _stream(w)), "moe_mxfp4_quantize_weights")
     return Mxfp4(q, scales, d_in)
 
 
@@ -663,8 +673,8 @@ def moe_mxfp4_dequantize(m: Mxfp4, *, x=None) -> torch.Tensor:
     rows = 1
     for n in lead:
         rows *= n
-    _check(load_library().moe_mxfp4_dequantize(_ptr(m.q), _ptr(m.scales), rows, m.width, _ptr(x), _stream(m.q)),
-           "moe_mxfp4_dequantize")
+    _check(load_library().moe_mxfp4_dequantize(m.q.data_ptr(), m.scales.data_ptr(), rows, m.width, x.data_ptr(),
+                                               _stream(m.q)), "moe_mxfp4_dequantize")
     return x
 
 
@@ -688,9 +698,9 @@ def moe_grouped_projection_mxfp4(x: Mxfp4, offsets: torch.Tensor, w: Mxfp4, *, y
     """Y[rows_e] = bf16(X[rows_e] @ W_e^T) on MXFP4 rows [cap, d_in] and weights [E, d_out, d_in] (one launch)."""
     cap, E, d_out, dev = _mxfp4_experts(x, offsets, w)
     y = _out(y, "y", torch.bfloat16, (cap, d_out), dev)
-    _check(load_library().moe_grouped_projection_mxfp4(_ptr(x.q), _ptr(x.scales), _ptr(offsets), _ptr(w.q),
-                                                       _ptr(w.scales), cap, x.width, d_out, E, _ptr(y), _stream(x.q)),
-           "moe_grouped_projection_mxfp4")
+    _check(load_library().moe_grouped_projection_mxfp4(x.q.data_ptr(), x.scales.data_ptr(), offsets.data_ptr(),
+                                                       w.q.data_ptr(), w.scales.data_ptr(), cap, x.width, d_out, E,
+                                                       y.data_ptr(), _stream(x.q)), "moe_grouped_projection_mxfp4")
     return y
 
 
@@ -712,9 +722,10 @@ def moe_gemm_up_swiglu_mxfp4(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, *, pe
     [E, 2h, d] (one launch). Without ``perm`` the rows are sorted already and k is 1."""
     T, k, E, h, dev = _mxfp4_up(x, offsets, w_ug, perm, k)
     h_buf = _out(h_buf, "h_buf", torch.bfloat16, (T * k, h), dev)
-    _check(load_library().moe_gemm_up_swiglu_mxfp4(_ptr(x.q), _ptr(x.scales), _ptr(perm), T, k, _ptr(offsets),
-                                                   _ptr(w_ug.q), _ptr(w_ug.scales), x.width, h, E, _ptr(h_buf),
-                                                   _stream(x.q)), "moe_gemm_up_swiglu_mxfp4")
+    _check(load_library().moe_gemm_up_swiglu_mxfp4(x.q.data_ptr(), x.scales.data_ptr(), _ptr(perm), T, k,
+                                                   offsets.data_ptr(), w_ug.q.data_ptr(), w_ug.scales.data_ptr(),
+                                                   x.width, h, E, h_buf.data_ptr(), _stream(x.q)),
+           "moe_gemm_up_swiglu_mxfp4")
     return h_buf
 
 
@@ -725,9 +736,10 @@ def moe_gemm_up_swiglu_mxfp4_q(x: Mxfp4, offsets: torch.Tensor, w_ug: Mxfp4, *, 
     T, k, E, h, dev = _mxfp4_up(x, offsets, w_ug, perm, k)
     q = _out(q, "q", torch.uint8, (T * k, mxfp4_row_bytes(h)), dev)
     scales = _out(scales, "scales", torch.uint8, (T * k, mxfp4_scale_bytes(h)), dev)
-    _check(load_library().moe_gemm_up_swiglu_mxfp4_q(_ptr(x.q), _ptr(x.scales), _ptr(perm), T, k, _ptr(offsets),
-                                                     _ptr(w_ug.q), _ptr(w_ug.scales), x.width, h, E, _ptr(q),
-                                                     _ptr(scales), _stream(x.q)), "moe_gemm_up_swiglu_mxfp4_q")
+    _check(load_library().moe_gemm_up_swiglu_mxfp4_q(x.q.data_ptr(), x.scales.data_ptr(), _ptr(perm), T, k,
+                                                     offsets.data_ptr(), w_ug.q.data_ptr(), w_ug.scales.data_ptr(),
+                                                     x.width, h, E, q.data_ptr(), scales.data_ptr(), _stream(x.q)),
+           "moe_gemm_up_swiglu_mxfp4_q")
     return Mxfp4(q, scales, h)
 
 
