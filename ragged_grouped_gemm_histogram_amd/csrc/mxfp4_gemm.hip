@@ -322,32 +322,31 @@ struct MxCoord {
   int e, row0, rows_valid, n0;
 };
 
-// Lanes 8..15 of every row of 16 take `b` of the lane 8 below, the others keep a; and lanes 0..7
-// take `a` of the lane 8 above, the others keep b.
-__device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
-  const uint32_t x = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, 0x128 /* row_ror:8 */, 0xf, 0xc, false);
-  b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a, 0x128, 0xf, 0x3, false);
-  a = x;
+// Exchanges a lane bit (0 or 1: CTRL is the quad permute that flips it, `set` where it is set) with the
+// choice between two registers, for four pairs: lanes that have it set take b of their partner into a, the
+// others a of theirs into b.
+template <int CTRL>
+__device__ __forceinline__ void swap_bit(uint32_t (&a)[4], uint32_t (&b)[4], bool set) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t from_b = quad_xor<CTRL>(b[w]), from_a = quad_xor<CTRL>(a[w]);  // read in every lane, whichever it keeps
+    a[w] = set ? from_b : a[w];
+    b[w] = set ? b[w] : from_a;
+  }
 }
 
 // Accumulators to bf16 rows. acc[i][j][4 q + s] is row wm * WTM + 32 i + lane % 32, column (block
-// column base + 8 q + 4 (lane / 32) + s). Three exchanges between lanes (halves, 16s, 8s) gather a
-// row's 64 columns from the registers of one lane pair into eight lanes: every store writes 8 rows
-// of 128 consecutive bytes. Rows past the block and columns past N fall outside the buffer resource
-// and are dropped; every wave issues all its stores.
+// column base + 8 q + 4 (lane / 32) + s). Three exchanges between lanes gather a row's 64 columns from
+// the registers of one lane pair into eight lanes: the halves exchange the column block, lane bits 0 and
+// 1 the group of 8 columns (q). Every store then writes 8 rows of 128 consecutive bytes, neighbouring
+// lanes neighbouring bytes: a CU takes such stores at 110 bytes a cycle, those of the same lines with
+// rows in the low lane bits at 32 (65536 x 2048 results of 768 values: 88 and 96 us a call). Rows past the block and columns past N fall outside the buffer
+// resource and are dropped; every wave issues all its stores.
 //
 // QUANT: the rows leave as MXFP4, 4 bytes of values a lane and two scale bytes a row and store. A
-// block of 32 columns is in the four lanes 16 and 32 apart.
+// block of 32 columns is in the four lanes of a quad.
 template <class C, bool QUANT>
 constexpr int kTileStores = C::FM * (QUANT ? 8 : 4) * (C::OUTW / C::WGN / 64);
-
-// Maximum over the four lanes whose numbers differ in bits 4 and 5.
-__device__ __forceinline__ uint32_t max_of_16s(uint32_t v) {
-  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  v = max((uint32_t)a[0], (uint32_t)a[1]);
-  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  return max((uint32_t)b[0], (uint32_t)b[1]);
-}
 
 template <class C, bool QUANT>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], const MxGemmArgs& g, const MxCoord& tc) {
@@ -370,68 +369,61 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], co
     rsrc = __builtin_amdgcn_make_buffer_rsrc(g.out + (int64_t)tc.row0 * g.ldo, (short)0,
                                              (int)((int64_t)tc.rows_valid * g.ldo * 2), 0x00020000);
   }
-  const uint32_t row = (uint32_t)(wm * C::WTM + (lane & 7)) * row_bytes;
+  const uint32_t row = (uint32_t)(wm * C::WTM + (lane & 28)) * row_bytes;
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
-    const int64_t col = tc.n0 + (wn * kPieces + p) * 64 + 8 * (lane >> 5) + 16 * ((lane >> 4) & 1) + 32 * ((lane >> 3) & 1);
+    const int64_t col = tc.n0 + (wn * kPieces + p) * 64 + 32 * (lane >> 5) + 8 * (lane & 3);
     const bool in = col < g.N;
     // (a block that N cuts is filled with zeros)
     const uint32_t base = QUANT ? (col < (g.N + 31) / 32 * 32 ? row + (uint32_t)(col / 2) : 0x80000000u)
                                 : (in ? row + (uint32_t)(col * 2) : 0x80000000u);
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      uint32_t v[2][2][4];  // [column block][rows 0-15 / 16-31][16 bytes]
+      uint32_t v[4][4];  // [group of 8 columns; after the exchanges: row lane & 28 + this][16 bytes]
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t pk[4][2];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[2][2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int j = 0; j < 2; ++j) {
           float f[4];
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             if constexpr (C::GATED) f[s] = swiglu(acc[i][2 * p + j][4 * q + s], acc[i][2 * kPieces + 2 * p + j][4 * q + s]);
             else f[s] = acc[i][2 * p + j][4 * q + s];
           }
-          pk[q][0] = pack_bf16x2(f[0], f[1]);
-          pk[q][1] = pack_bf16x2(f[2], f[3]);
+          pk[j][0] = pack_bf16x2(f[0], f[1]);
+          pk[j][1] = pack_bf16x2(f[2], f[3]);
         }
-        // halves: a lane holds columns 8 (q + half) .. + 7 of q = 0 (x) and q = 2 (y)
-        uint32_t x[4], y[4];
+        // halves: the lower one gets the first column block's 8 columns, the upper one the second's
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const auto a = __builtin_amdgcn_permlane32_swap(pk[0][w], pk[1][w], false, false);
-          const auto b = __builtin_amdgcn_permlane32_swap(pk[2][w], pk[3][w], false, false);
-          x[w] = a[0]; x[2 + w] = a[1];
-          y[w] = b[0]; y[2 + w] = b[1];
-        }
-        // 16s: x gets rows 0-15 with all 32 columns, y rows 16-31
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const auto a = __builtin_amdgcn_permlane16_swap(x[w], y[w], false, false);
-          v[j][0][w] = a[0];
-          v[j][1][w] = a[1];
+          const auto x = __builtin_amdgcn_permlane32_swap(pk[0][w], pk[1][w], false, false);
+          v[q][w] = x[0];
+          v[q][2 + w] = x[1];
         }
       }
-      // 8s: the first block's registers get rows 0-7 with all 64 columns, the second's rows 8-15
+      swap_bit<0xB1>(v[0], v[1], lane & 1);
+      swap_bit<0xB1>(v[2], v[3], lane & 1);
+      swap_bit<0x4E>(v[0], v[2], lane & 2);
+      swap_bit<0x4E>(v[1], v[3], lane & 2);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) swap8(v[0][h][w], v[1][h][w]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          u32x4 w{v[j][h][0], v[j][h][1], v[j][h][2], v[j][h][3]};
-          const uint32_t at = (uint32_t)(32 * i + 16 * h + 8 * j);  // rows from the wave's first, and lane % 8
-          if constexpr (QUANT) {
-            if (!in) w = u32x4{0u, 0u, 0u, 0u};
-            const uint32_t byte = scale_byte(max_of_16s(max_magnitude(w)));
-            __builtin_amdgcn_raw_buffer_store_b32(to_fp4(w, byte), rsrc, base + at * row_bytes, 0, 0);
-            // lanes 0..7 write their row's two bytes: their own block's and that of the lane 8 above
-            const uint32_t above = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)byte, 0x128 /* row_ror:8 */, 0xf, 0xf, false);
-            const uint32_t s_at = ((uint32_t)(wm * C::WTM + lane) + at) * s_bytes + (uint32_t)((tc.n0 + wn * 64) / 32);
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(byte | above << 8), s_rsrc, lane < 8 ? s_at : 0x80000000u, 0, 0);
-          } else {
-            __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, base + at * row_bytes, 0, 2 /* nt */);
-          }
+      for (int t = 0; t < 4; ++t) {
+        u32x4 w{v[t][0], v[t][1], v[t][2], v[t][3]};
+        const uint32_t at = (uint32_t)(32 * i + t);  // rows from the wave's first, and lane & 28
+        if constexpr (QUANT) {
+          if (!in) w = u32x4{0u, 0u, 0u, 0u};
+          uint32_t top = max_magnitude(w);
+          top = max(top, quad_xor<0xB1>(top));
+          top = max(top, quad_xor<0x4E>(top));
+          const uint32_t byte = scale_byte(top);
+          __builtin_amdgcn_raw_buffer_store_b32(to_fp4(w, byte), rsrc, base + at * row_bytes, 0, 0);
+          // the first lane of a quad of the lower half writes its row's two bytes
+          const auto both = __builtin_amdgcn_permlane32_swap(byte, byte, false, false);
+          const uint32_t s_at = ((uint32_t)(wm * C::WTM + lane) + at) * s_bytes + (uint32_t)((tc.n0 + wn * 64) / 32);
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(both[0] | both[1] << 8), s_rsrc,
+                                                (lane & 35) == 0 ? s_at : 0x80000000u, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, base + at * row_bytes, 0, 2 /* nt */);
         }
       }
     }
