@@ -343,10 +343,11 @@ __device__ __forceinline__ void swap_bit(uint32_t (&a)[4], uint32_t (&b)[4], boo
 // rows in the low lane bits at 32 (65536 x 2048 results of 768 values: 88 and 96 us a call). Rows past the block and columns past N fall outside the buffer
 // resource and are dropped; every wave issues all its stores.
 //
-// QUANT: the rows leave as MXFP4, 4 bytes of values a lane and two scale bytes a row and store. A
-// block of 32 columns is in the four lanes of a quad.
+// QUANT: the rows leave as MXFP4. After the first exchange a lane holds a whole block of its row, so the
+// block's maximum needs no other lane, and the lane stores its 16 bytes; the lower half's lanes store their
+// row's two scale bytes.
 template <class C, bool QUANT>
-constexpr int kTileStores = C::FM * (QUANT ? 8 : 4) * (C::OUTW / C::WGN / 64);
+constexpr int kTileStores = C::FM * (QUANT ? 2 : 4) * (C::OUTW / C::WGN / 64);
 
 template <class C, bool QUANT>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], const MxGemmArgs& g, const MxCoord& tc) {
@@ -369,14 +370,11 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], co
     rsrc = __builtin_amdgcn_make_buffer_rsrc(g.out + (int64_t)tc.row0 * g.ldo, (short)0,
                                              (int)((int64_t)tc.rows_valid * g.ldo * 2), 0x00020000);
   }
-  const uint32_t row = (uint32_t)(wm * C::WTM + (lane & 28)) * row_bytes;
+  const uint32_t row = (uint32_t)(wm * C::WTM + (lane & (QUANT ? 31 : 28)));
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
-    const int64_t col = tc.n0 + (wn * kPieces + p) * 64 + 32 * (lane >> 5) + 8 * (lane & 3);
-    const bool in = col < g.N;
-    // (a block that N cuts is filled with zeros)
-    const uint32_t base = QUANT ? (col < (g.N + 31) / 32 * 32 ? row + (uint32_t)(col / 2) : 0x80000000u)
-                                : (in ? row + (uint32_t)(col * 2) : 0x80000000u);
+    const int64_t col = tc.n0 + (wn * kPieces + p) * 64 + 32 * (lane >> 5) + (QUANT ? 0 : 8 * (lane & 3));
+    const uint32_t base = col < g.N ? row * row_bytes + (uint32_t)(QUANT ? col / 2 : col * 2) : 0x80000000u;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
       uint32_t v[4][4];  // [group of 8 columns; after the exchanges: row lane & 28 + this][16 bytes]
@@ -402,29 +400,32 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[C::FM][C::FN], co
           v[q][2 + w] = x[1];
         }
       }
-      swap_bit<0xB1>(v[0], v[1], lane & 1);
-      swap_bit<0xB1>(v[2], v[3], lane & 1);
-      swap_bit<0x4E>(v[0], v[2], lane & 2);
-      swap_bit<0x4E>(v[1], v[3], lane & 2);
+      if constexpr (QUANT) {
+        u32x4 part[4], out;
+        uint32_t top = 0;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        u32x4 w{v[t][0], v[t][1], v[t][2], v[t][3]};
-        const uint32_t at = (uint32_t)(32 * i + t);  // rows from the wave's first, and lane & 28
-        if constexpr (QUANT) {
-          if (!in) w = u32x4{0u, 0u, 0u, 0u};
-          uint32_t top = max_magnitude(w);
-          top = max(top, quad_xor<0xB1>(top));
-          top = max(top, quad_xor<0x4E>(top));
-          const uint32_t byte = scale_byte(top);
-          __builtin_amdgcn_raw_buffer_store_b32(to_fp4(w, byte), rsrc, base + at * row_bytes, 0, 0);
-          // the first lane of a quad of the lower half writes its row's two bytes
-          const auto both = __builtin_amdgcn_permlane32_swap(byte, byte, false, false);
-          const uint32_t s_at = ((uint32_t)(wm * C::WTM + lane) + at) * s_bytes + (uint32_t)((tc.n0 + wn * 64) / 32);
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(both[0] | both[1] << 8), s_rsrc,
-                                                (lane & 35) == 0 ? s_at : 0x80000000u, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b128(w, rsrc, base + at * row_bytes, 0, 2 /* nt */);
+        for (int q = 0; q < 4; ++q) {
+          part[q] = u32x4{v[q][0], v[q][1], v[q][2], v[q][3]};
+          if (col + 8 * q >= g.N) part[q] = u32x4{0u, 0u, 0u, 0u};  // a block that N cuts is filled with zeros
+          top = max(top, max_magnitude(part[q]));
         }
+        const uint32_t byte = scale_byte(top);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) out[q] = to_fp4(part[q], byte);
+        __builtin_amdgcn_raw_buffer_store_b128(out, rsrc, base + (uint32_t)(32 * i) * row_bytes, 0, 0);
+        const auto both = __builtin_amdgcn_permlane32_swap(byte, byte, false, false);
+        const uint32_t s_at = (row + (uint32_t)(32 * i)) * s_bytes + (uint32_t)((tc.n0 + wn * 64) / 32);
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(both[0] | both[1] << 8), s_rsrc, lane < 32 ? s_at : 0x80000000u,
+                                              0, 0);
+      } else {
+        swap_bit<0xB1>(v[0], v[1], lane & 1);
+        swap_bit<0xB1>(v[2], v[3], lane & 1);
+        swap_bit<0x4E>(v[0], v[2], lane & 2);
+        swap_bit<0x4E>(v[1], v[3], lane & 2);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[t][0], v[t][1], v[t][2], v[t][3]}, rsrc,
+                                                 base + (uint32_t)(32 * i + t) * row_bytes, 0, 2 /* nt */);
       }
     }
   }
