@@ -274,17 +274,17 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
 // four are loaded, and the results leave from registers (exchanges between lanes make whole lines)
 // instead of through the ring's memory, so the loads of a new tile have no gap before them.
 //
-// Measured: gate/up of 8192 tokens, top-8 of 64 experts 2048 -> 2 x 768, skewed (392 GFLOP) 137 us; down
-// projection of 65536 rows 768 -> 2048 of the same experts (206 GFLOP, 268 MB written) 99 us; 16 experts
-// 4096 -> 4096, 65536 rows, 3.5 PFLOP/s. The matrix unit is busy 37 and 25% of 281 and 221 thousand cycles
-// (the first two). What the rest is, in thousand cycles: 241 and 136 without SwiGLU and stores, 245 and 196
-// without loads, 237 and 209 without LDS reads, 169 and 108 with products and barriers alone, 11 of them
-// before the first product. So the down projection is bound by its stores, which HBM takes 120 thousand
-// cycles to write and which overlap little with the next tile's products (a CU's waves store together),
-// gate/up by LDS, loads and matrix unit sharing a stage. Tried and slower: 128 x 128 tiles, two workgroups
-// a CU (gate/up 220, down 153 us; over 170 random calls 0.3% would be gained by taking them where they
-// win); four waves of 128 x 128 (registers spill); staggered starts; ordinary stores; products skipped by
-// waves without rows.
+// Measured: gate/up of 8192 tokens, top-8 of 64 experts 2048 -> 2 x 768, skewed (392 GFLOP) 133 us; down
+// projection of 65536 rows 768 -> 2048 of the same experts (206 GFLOP, 268 MB written) 89 us; 16 experts
+// 4096 -> 4096, 65536 rows, 3.5 PFLOP/s. The matrix unit is busy 37 and 28% of 279 and 198 thousand cycles
+// (the first two). What the rest is, in thousand cycles: 241 and 135 without SwiGLU and stores, 243 and 160
+// without loads, 232 and 188 without LDS reads, 160 and 99 with products and barriers alone, 11 of them
+// before the first product. So the down projection is bound by its stores, which HBM alone takes 120
+// thousand cycles to write and which overlap half with the next tile's products, gate/up by LDS, loads and
+// matrix unit sharing a stage. Tried and slower: 128 x 128 tiles, two workgroups a CU (gate/up 220, down
+// 153 us when these were 150 and 114; over 170 random calls 0.3% would be gained by taking them where they
+// win); four waves of 128 x 128 (registers spill); staggered starts; ordinary stores (106 us); wave
+// priorities; products skipped by waves without rows.
 // ---------------------------------------------------------------------------------------------
 constexpr int kStageK = 128;
 constexpr int kRing = 4;          // stages in LDS
