@@ -222,3 +222,47 @@ def test_router_gradient_of_experts_chosen_twice(renormalize):
         want -= p * total
         size += p * (w * d.abs()).sum(1, keepdim=True)
     assert ((first.double() - want).abs() <= size * ((4 * k + 8) * 2.0 ** -24 + 2.0 ** -18)).all()
+
+
+def test_two_captured_layers_replayed_in_turn():
+    """Router, MXFP4 step and router gradient of two layers, a graph each: every replay, in any order and with new
+    inputs and eager work between, equals the eager calls."""
+    say("[gpu] two captured router and mxfp4 layers")
+    T, k, E, d, h = 640, 4, 16, 264, 136
+    g = generator(9)
+    layers = []
+    for _ in range(2):
+        w = [torch.randn((E, *s), generator=g, device=DEV).mul_(0.1).bfloat16() for s in ((2 * h, d), (h, d))]
+        layers.append((torch.randn((T, d), generator=g, device=DEV).bfloat16(), torch.randn((T, E), generator=g, device=DEV),
+                       torch.randn((T, k), generator=g, device=DEV),
+                       moe.moe_mxfp4_quantize_weights(w[0], "out_in"), moe.moe_mxfp4_quantize_weights(w[1], "in_out")))
+    dl = torch.tensor([0.01, 0.001], device=DEV)
+
+    def step(x, logits, dw, w_ug, w_down):
+        r = moe.moe_router_topk_losses(logits, k)
+        y, _ = moe.moe_expert_forward_mxfp4(x, r.expert_ids, r.routing_w, w_ug, w_down)
+        return y, r.losses, r.counts, moe.moe_router_backward(logits, r, dw, dl)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(s):
+        for layer in layers:
+            step(*layer)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                outs.append(step(*layer))
+            graphs.append(graph)
+    torch.cuda.current_stream().wait_stream(s)
+    for rep, order in enumerate(([0, 1], [1, 0], [1, 1, 0], [0, 0, 1])):
+        for x, logits, *_ in layers:
+            x.copy_(torch.randn((T, d), generator=g, device=DEV))
+            logits.copy_(torch.randn((T, E), generator=g, device=DEV))
+        logits[rep::7] = -float("inf")
+        want = [[t.clone() for t in step(*layer)] for layer in layers]
+        torch.cuda.synchronize()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i])), (rep, i)
