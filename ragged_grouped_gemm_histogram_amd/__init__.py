@@ -563,7 +563,8 @@ def moe_router_topk_losses(logits: torch.Tensor, k: int, *, renormalize: bool = 
     lse = _out(lse, "lse", torch.float32, (T,), dev)
     if counts is None and tokens is None and prob_mean is None and losses is None:
         # one allocation for the four
-        counts, tokens, prob_mean, losses = torch.empty((2 * E + 3,), dtype=torch.int32, device=dev).split((E, 1, E, 2))
+        words = torch.empty((2 * E + 3,), dtype=torch.int32, device=dev)
+        counts, tokens, prob_mean, losses = words.split_with_sizes((E, 1, E, 2))
         prob_mean, losses = prob_mean.view(torch.float32), losses.view(torch.float32)
     else:
         counts = _out(counts, "counts", torch.int32, (E,), dev)
