@@ -172,6 +172,18 @@ __device__ __forceinline__ void store_row(T* x, int64_t t, int E, int e0, bool w
   }
 }
 
+// exp(x_i - m0) of this lane's logits and their sum over the row.
+template <int G, int V>
+__device__ __forceinline__ float exponentials_from(const float (&v)[V], float m0, float (&e)[V]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    e[i] = exp_nonpositive(v[i] - m0);  // a NaN logit reaches the sum here
+    s += e[i];
+  }
+  return group_sum<G>(s);
+}
+
 // exp(x_i - m) of this lane's logits and their sum over the row, and the logits' keys. A row of -inf
 // alone has m = -inf; it is shifted by 0 instead, so that its exponentials and sum are 0 and its lse -inf.
 template <int G, int V>
@@ -184,13 +196,18 @@ __device__ __forceinline__ float row_exponentials(const float (&v)[V], float& m0
   }
   top = group_max<G>(top);
   m0 = top == kNegInfKey ? 0.f : __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
-  float s = 0.f;
+  return exponentials_from<G, V>(v, m0, e);
+}
+
+// The same without the keys.
+template <int G, int V>
+__device__ __forceinline__ float row_exponentials(const float (&v)[V], float& m0, float (&e)[V]) {
+  float top = neg_inf();
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    e[i] = exp_nonpositive(v[i] - m0);  // a NaN logit reaches the sum here
-    s += e[i];
-  }
-  return group_sum<G>(s);
+  for (int i = 0; i < V; ++i) top = fmaxf(top, v[i]);  // a NaN loses
+  top = group_max<G>(top);
+  m0 = top == neg_inf() ? 0.f : top;
+  return exponentials_from<G, V>(v, m0, e);
 }
 
 struct RouterArgs {
@@ -487,14 +504,13 @@ __global__ __launch_bounds__(kPlainThreads) void router_backward_kernel(RouterBa
   }
   for (; t < a.T; t += stride) {
     float v[V], p[V], d[V];
-    int key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = next[i];
     const int id = next_id;
     const float slot_g = next_g, slot_w = next_w;
     if (t + stride < a.T) fetch(t + stride);
     float m0;
-    const float s = row_exponentials<G, V>(v, m0, p, key);
+    const float s = row_exponentials<G, V>(v, m0, p);
     if (s == 0.f) {  // nothing to choose from: no probability, no gradient
 #pragma unroll
       for (int i = 0; i < V; ++i) d[i] = 0.f;
