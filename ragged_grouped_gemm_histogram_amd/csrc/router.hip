@@ -21,7 +21,7 @@
 // Small calls are bound by latency (one read, log2 G exchanges a reduction, k rounds), large ones by issuing
 // instructions: a logit costs about 20 for its key and exponential and 8 per round of selection. Measured: 4
 // tokens of 128 experts 4.1 us, 8192 x 64 5.1; 65537 x 100 fp32, top-6, selection 16.9 us, with the losses
-// 23.3 + 5.5, gradient 17.8 (3 TB/s). Losses that finish in the first launch would need a counter that
+// 22.8 + 5.6, gradient 15.4 (3.4 TB/s). Losses that finish in the first launch would need a counter that
 // somebody clears before it.
 
 #include <type_traits>
@@ -571,7 +571,7 @@ int64_t router_blocks(int64_t T, int groups, int64_t cap) {
 }
 
 // Lanes per token: 8 experts a lane up to 512 experts, 16 beyond. (16 a lane also for 65537 tokens of 100
-// experts: selection with its sums 21.0 instead of 22.4 us, gradient 19.2 instead of 17.3.)
+// experts: selection with its sums 21.0 instead of 22.4 us, gradient 19.2 instead of the 17.3 it took then.)
 int lanes_of(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
 
 int loss_threads(int64_t T, int E) { return T * lanes_of(E) <= kLossBlocks * kLossThreads ? kLossThreads : kLossThreadsMany; }
@@ -640,7 +640,9 @@ hipError_t launch_router_backward(const void* logits, bool f32, int64_t T, int32
   if (T == 0) return hipSuccess;
   const bool wide = wide_rows(logits, E, f32) && wide_rows(d_logits, E, f32);
   const RouterBackwardArgs a{logits, T, E, k, renormalize, wide, ids, w, counts, tokens, d_w, d_losses, d_logits};
-  const int64_t cap = (int64_t)device_cu_count(current_device()) * 8;  // all at once on the device
+  // Three workgroups a CU: each waits once for the counts, then walks the tokens with the next row on its way. 65537
+  // tokens of 100 experts 15.4 us (2: 16.3, 4: 15.9, 6: 15.9, 8, more than fit at once: 17.5).
+  const int64_t cap = (int64_t)device_cu_count(current_device()) * 3;
   return by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
     const dim3 grid((unsigned)router_blocks(T, kPlainThreads / G, cap));
