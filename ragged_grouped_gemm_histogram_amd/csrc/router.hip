@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void router_topk_kernel(RouterArgs a) {
   __shared__ float zsum_s[LOSSES ? kGroups : 1];
   __shared__ int tokens_s[LOSSES ? kGroups : 1];
   const int tid = threadIdx.x, group = tid / G, g = tid % G, lane = tid & 63;
-  const int first_lane = lane - g;  // of the group, inside its wave
+  const uint64_t below = ((1ull << lane) - 1) & ~((1ull << (lane - g)) - 1);  // the group's lanes below this one
   const int e0 = g * V;
   float col[V];
   float zsum = 0.f;
@@ -279,10 +279,8 @@ __global__ __launch_bounds__(kThreads) void router_topk_kernel(RouterArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) best = max(best, key[i]);
       const int top = group_max<G>(best);
-      uint64_t have = __ballot(best == top) >> first_lane;
-      if constexpr (G < 64) have &= (1ull << G) - 1;
-      const int leader = __ffsll((long long)have) - 1;
-      if (g == leader) {
+      const uint64_t have = __ballot(best == top);
+      if (best == top && (have & below) == 0) {
         int at = -1;
         float part = 0.f;
         bool found = top == kNegInfKey;  // none is left
