@@ -9,6 +9,14 @@ __host__ __device__ __forceinline__ int64_t mx_blocks(int64_t K) { return (K + 3
 __host__ __device__ __forceinline__ int64_t mx_row_bytes(int64_t K) { return 16 * mx_blocks(K); }
 __host__ __device__ __forceinline__ int64_t mx_scale_bytes(int64_t K) { return 16 * ((K + 511) / 512); }
 
+// Where stage `stage` of a packed row (kMxStageBlocks blocks) starts, in bytes. Stages past the row's last take that
+// one's start: a scalar offset that passes the end of a buffer resource leaves the range check nothing to compare with.
+constexpr int kMxStageBlocks = 4;
+__host__ __device__ constexpr uint32_t mx_stage_offset(int stage, int blocks) {
+  const int last = (blocks - 1) / kMxStageBlocks;
+  return (uint32_t)(stage < last ? stage : last) * (16u * kMxStageBlocks);
+}
+
 typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
 
 template <int CTRL>

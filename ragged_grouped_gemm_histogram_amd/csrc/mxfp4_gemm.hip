@@ -594,7 +594,8 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       s_off[t2] = (r < BM ? a_row(r, slot_s[t2]) : b_row(r - BM)) * sp;
     }
     if constexpr (KTAIL) {
-      const int64_t a_range = gather ? g.a_tokens * qp : (int64_t)tc.rows_valid * qp;
+      // (a tile without rows still reads row 0, and no row is shorter than the scalar offsets)
+      const int64_t a_range = gather ? g.a_tokens * qp : (int64_t)max(tc.rows_valid, 1) * qp;
       a_rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a_ptr), (short)0, (int)a_range, 0x00020000);
       b_rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(b_ptr), (short)0, (int)(g.w_rows * qp), 0x00020000);
     }
@@ -615,8 +616,9 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       scale_to = scale_to == 2 * C::SCALE_BYTES ? 0 : scale_to + C::SCALE_BYTES;
     }
     if constexpr (KTAIL) {
-      // chunks past the row get an offset past the buffer resource's range and stage zeros
-      const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)ik * 64u);
+      // chunks past the row get an offset past the buffer resource's range and stage zeros; the scalar offset stays
+      // inside the row also for the stages that a short one does not have
+      const uint32_t soff = __builtin_amdgcn_readfirstlane(mx_stage_offset(ik, blocks));
       const bool in = chunk < blocks - 4 * ik;
 #pragma unroll
       for (int t2 = 0; t2 < C::A_OPS; ++t2)
