@@ -483,8 +483,10 @@ __global__ __launch_bounds__(kPlainThreads) void router_backward_kernel(RouterBa
   if (a.d_losses != nullptr) {
     const int n = a.tokens[0];
     const float d0 = a.d_losses[0], d1 = a.d_losses[1];
-    // every lane of a group holds a part of the counts: their sum is the group's
-    int counts[V], total = 0;
+    // every lane of a group holds a part of the counts: their sum is the group's (64 bits: over a batch of several
+    // ranks the slots of all experts together pass 2^31 before the tokens do)
+    int counts[V];
+    long long total = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) counts[i] = a.counts[e0 + i < a.E ? e0 + i : 0];
 #pragma unroll
