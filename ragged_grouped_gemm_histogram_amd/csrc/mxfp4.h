@@ -17,6 +17,12 @@ __host__ __device__ constexpr uint32_t mx_stage_offset(int stage, int blocks) {
   return (uint32_t)(stage < last ? stage : last) * (16u * kMxStageBlocks);
 }
 
+// Tiles of `height` rows that the rows [lo, hi) take, 0 <= lo; none if hi is before lo. In unsigned arithmetic: a block
+// may have 2^31 - 1 rows.
+__host__ __device__ constexpr uint32_t mx_row_tiles(int lo, int hi, int height) {
+  return hi > lo ? ((uint32_t)hi - (uint32_t)lo + (uint32_t)height - 1u) / (uint32_t)height : 0u;
+}
+
 typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
 
 template <int CTRL>

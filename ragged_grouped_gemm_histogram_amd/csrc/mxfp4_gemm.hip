@@ -72,7 +72,7 @@ template <bool GATED, bool QUANT, int BATCH>
 __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs g) {
   __shared__ int mt_prefix[MOE_MAX_EXPERTS + 1];
   __shared__ int offs[MOE_MAX_EXPERTS + 1];  // clamped to the capacity
-  __shared__ int wave_total[kThinWaves];
+  __shared__ uint32_t wave_total[kThinWaves];
   __shared__ float4 red[kThinWaves * 4 * 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 31, hh = lane >> 5;
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
   // prefix of the experts' 32-row tile counts
   {
     constexpr int kPer = MOE_MAX_EXPERTS / kThinThreads;
-    int mt[kPer], sum = 0;
+    uint32_t mt[kPer], sum = 0;  // (unsigned: offsets that are no running sum can wrap the counts)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid + i * kThinThreads;
@@ -91,27 +91,26 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
-      mt[i] = 0;
-      if (e < g.E) mt[i] = offs[e + 1] > offs[e] ? (offs[e + 1] - offs[e] + 31) / 32 : 0;
+      mt[i] = e < g.E ? mx_row_tiles(offs[e], offs[e + 1], 32) : 0u;
       sum += mt[i];
     }
-    int incl = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int up = __shfl_up(incl, off, 64);
+      const uint32_t up = __shfl_up(incl, off, 64);
       if (lane >= off) incl += up;
     }
     if (lane == 63) wave_total[wave] = incl;
     __syncthreads();
-    int run = incl - sum;
+    uint32_t run = incl - sum;
     for (int w = 0; w < wave; ++w) run += wave_total[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
-      if (e <= g.E) mt_prefix[e] = run;
+      if (e <= g.E) mt_prefix[e] = (int)run;
       run += mt[i];
     }
-    if (tid == kThinThreads - 1 && g.E == MOE_MAX_EXPERTS) mt_prefix[g.E] = run;
+    if (tid == kThinThreads - 1 && g.E == MOE_MAX_EXPERTS) mt_prefix[g.E] = (int)run;
     __syncthreads();
   }
   constexpr int kCols = kThinCols<GATED>;
@@ -132,8 +131,8 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
       if (mt_prefix[mid] <= gm) e = mid; else hi_e = mid;
     }
     const int64_t lo = offs[e], hi = offs[e + 1];
-    const int64_t row0 = lo + (int64_t)(gm - mt_prefix[e]) * 32;
-    if (row0 < lo || row0 >= hi) continue;  // offsets that are no running sum can wrap the tile counts
+    const int64_t row0 = lo + ((int64_t)gm - mt_prefix[e]) * 32;
+    if (row0 < lo || row0 >= hi) continue;  // wrapped counts
     const int valid = (int)(hi - row0 < 32 ? hi - row0 : 32);
     // sources: rows past the block repeat its last, columns past N the tile's first; neither is stored
     int64_t a_row = row0 + (r < valid ? r : valid - 1);
@@ -314,7 +313,7 @@ struct MxTile {
 
 struct MxProblems {
   int mt_prefix[MOE_MAX_EXPERTS + 1];
-  int wave_total[8];
+  uint32_t wave_total[8];
   int4 table[kTableTiles];  // expert, first row, rows, first column
 };
 
@@ -458,7 +457,7 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
   int2* first_offsets = reinterpret_cast<int2*>(smem);
   {
     constexpr int kPer = MOE_MAX_EXPERTS / C::THREADS;
-    int mt[kPer], sum = 0;
+    uint32_t mt[kPer], sum = 0;  // (unsigned: offsets that are no running sum can wrap the counts)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
@@ -466,28 +465,28 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       if (e < g.E) {
         const int64_t lo = clamp_row(g.offsets[e], g.cap_rows), hi = clamp_row(g.offsets[e + 1], g.cap_rows);
         first_offsets[e] = int2{(int)lo, (int)hi};
-        mt[i] = hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0;
+        mt[i] = mx_row_tiles((int)lo, (int)hi, BM);
       }
       sum += mt[i];
     }
-    int incl = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int up = __shfl_up(incl, off, 64);
+      const uint32_t up = __shfl_up(incl, off, 64);
       if (lane >= off) incl += up;
     }
     if (lane == 63) pl.wave_total[wave] = incl;
     __syncthreads();
-    int run = incl - sum;
+    uint32_t run = incl - sum;
 #pragma unroll
-    for (int w = 0; w < C::NWAVES; ++w) run += w < wave ? pl.wave_total[w] : 0;
+    for (int w = 0; w < C::NWAVES; ++w) run += w < wave ? pl.wave_total[w] : 0u;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
-      if (e <= g.E) pl.mt_prefix[e] = run;
+      if (e <= g.E) pl.mt_prefix[e] = (int)run;
       run += mt[i];
     }
-    if (tid == C::THREADS - 1 && g.E == MOE_MAX_EXPERTS) pl.mt_prefix[g.E] = run;
+    if (tid == C::THREADS - 1 && g.E == MOE_MAX_EXPERTS) pl.mt_prefix[g.E] = (int)run;
     __syncthreads();
   }
   const int total_mt = pl.mt_prefix[g.E];
@@ -517,9 +516,9 @@ __global__ __launch_bounds__(C::THREADS) void mxfp4_pipe_kernel(MxGemmArgs g) {
       }
       const int2 block = block_of(e);
       const int64_t lo = block.x, hi = block.y;
-      int64_t row0 = lo + (int64_t)(gm - pl.mt_prefix[e]) * BM;
+      int64_t row0 = lo + ((int64_t)gm - pl.mt_prefix[e]) * BM;
       int64_t rows = hi - row0 < BM ? hi - row0 : BM;
-      if (row0 < lo || row0 >= hi) row0 = rows = 0;  // offsets that are no running sum can wrap the tile counts
+      if (row0 < lo || row0 >= hi) row0 = rows = 0;  // wrapped counts
       pl.table[tid] = int4{e, (int)row0, (int)rows, nt * TILE_N};
     }
     __syncthreads();

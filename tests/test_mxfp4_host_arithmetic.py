@@ -47,3 +47,16 @@ def test_scalar_offsets_of_stages_stay_inside_the_row(tmp_path):
       if (stage < real) CHECK(off == (uint32_t)stage * 64u, "K %lld stage %d: %u", (long long)K, stage, off);
     }
   }""")
+
+
+def test_row_tiles_of_the_largest_blocks(tmp_path):
+    """Tiles of a block that ends at the largest capacity, 2^31 - 1 rows."""
+    run_on_host(tmp_path, """
+  const int top = 0x7FFFFFFF;
+  for (int height : {32, 256})
+    for (int64_t lo : {0ll, 1ll, 30ll, 31ll, 255ll, (long long)top - 300, (long long)top - 1, (long long)top})
+      for (int64_t hi : {0ll, 1ll, 32ll, 33ll, 257ll, (long long)top - 257, (long long)top - 31, (long long)top}) {
+        const int64_t want = hi > lo ? (hi - lo + height - 1) / height : 0;
+        CHECK((int64_t)mx_row_tiles((int)lo, (int)hi, height) == want, "[%lld, %lld) by %d: %u", (long long)lo,
+              (long long)hi, height, mx_row_tiles((int)lo, (int)hi, height));
+      }""")
