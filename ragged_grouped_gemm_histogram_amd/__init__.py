@@ -102,15 +102,19 @@ def _check(status: int, call: str) -> None:
         raise MoeError(status, call)
 
 
-# Names that every call looks up, bound once.
+def _public_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# Names that every call looks up, bound once. The two device queries are those behind torch.cuda.current_device() and
+# current_stream(), two microseconds a call less; a torch that lacks them (one without a GPU backend) has the public ones.
 _Tensor = torch.Tensor
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 
 
 def _stream(t: torch.Tensor) -> int:
     # The library launches on the current HIP device; a stream of another device would fail the launch.
-    # (The raw queries behind torch.cuda.current_device() and current_stream(): two microseconds less a call.)
     index = t.get_device()
     if index != _current_device():
         raise ValueError(f"tensors are on {t.device} but the current device is cuda:{torch.cuda.current_device()}; "
