@@ -437,7 +437,8 @@ moe_status moe_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t K, uint8_
 moe_status moe_mxfp4_quantize_weights(const uint16_t* w, int32_t w_layout, int64_t d_in, int64_t d_out, int32_t E,
                                       uint8_t* q, uint8_t* scales, hipStream_t stream);
 
-/* Packed rows back to bf16 [rows, K] (exact), one launch (several from 2^36 values). */
+/* Packed rows back to bf16 [rows, K], one launch (several from 2^36 values). Exact for scale bytes up to 252, which
+ * the quantising calls do not pass; at 253 and 254 (rows from elsewhere) a value past bf16's range is an infinity. */
 moe_status moe_mxfp4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, uint16_t* x,
                                 hipStream_t stream);
 

@@ -669,7 +669,8 @@ def moe_mxfp4_quantize_weights(w: torch.Tensor, layout: str = "in_out", *, q=Non
 
 
 def moe_mxfp4_dequantize(m: Mxfp4, *, x=None) -> torch.Tensor:
-    """The bf16 values of MXFP4 rows (exact; one launch)."""
+    """The bf16 values of MXFP4 rows (one launch). Exact for scale bytes up to 252, which the quantising calls do not
+    pass; at 253 and 254 a value past bf16's range is an infinity."""
     if not isinstance(m, Mxfp4) or m.q.dim() < 1:
         raise TypeError("expected an Mxfp4")
     lead, dev = tuple(m.q.shape[:-1]), m.q.device

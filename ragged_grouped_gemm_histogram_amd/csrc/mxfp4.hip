@@ -127,8 +127,10 @@ __global__ __launch_bounds__(kThreads) void mxfp4_quantize_columns_kernel(const 
         *reinterpret_cast<const u32x4*>(bytes + tid * kTileBlocks);
 }
 
-// Packed rows back to bf16: exact, the products of a 4-bit value and a power of two have two
-// significant bits and at least 2^-128, bf16's smallest normals and subnormals hold them.
+// Packed rows back to bf16: a 4-bit value times a power of two has two significant bits and at least
+// 2^-128, which bf16's smallest normals and subnormals hold, and at most 6 * 2^(byte - 127), which
+// bf16 holds up to byte 252. Rows quantised here have at most that; beyond, values that bf16 does not
+// hold become infinities.
 __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint8_t* __restrict__ q,
                                                                     const uint8_t* __restrict__ scales, int64_t rows,
                                                                     int64_t K, uint16_t* __restrict__ x) {
