@@ -260,16 +260,16 @@ template <class C>
 constexpr bool kOpaqueEpilogue = !C::GATED && C::BM == 256;
 
 // Registers -> bf16 tile in LDS (swizzled 16-byte chunks) -> global. For the
-// gated projection, SwiGLU is applied here: g and u are rounded to bf16 first
-// (ROUND_U), then SiLU(g) * u is evaluated in fp32 with the hardware exponential
-// and reciprocal (a few fp32 ulps, far below the bf16 rounding of the result).
+// gated projection, SwiGLU is applied here: g and u are rounded to bf16 first,
+// then SiLU(g) * u is evaluated in fp32 with the hardware exponential and
+// reciprocal (a few fp32 ulps, far below the bf16 rounding of the result).
 // acc[i][j][4q+s] is output row (wm*WTM + i*32 + lane%32), column
 // (block column base + 8q + 4*(lane/32) + s).
-template <class C, bool ROUND_U = true, class Args>
+template <class C, class Args>
 __device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::FM][C::FN], unsigned char* smem, const Args& g,
                                          const TileCoord& tc) {
   constexpr int BM = C::BM, BN = C::BN;
-  const int tid = epilogue_tid<kOpaqueEpilogue<C> || !ROUND_U>(), lane = tid & 63, wave = tid >> 6;
+  const int tid = epilogue_tid<kOpaqueEpilogue<C>>(), lane = tid & 63, wave = tid >> 6;
   const int wm = wave / C::WGN, wn = wave % C::WGN;
   unsigned char* ot = smem;  // [BM][OUTW] bf16
   constexpr int OUT_ROW_BYTES = C::OUTW * 2;
@@ -284,18 +284,13 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[C::FM][C::FN], unsi
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float hv[4];
-          if constexpr (ROUND_U) {
-            // g and u rounded to bf16 two at a time (one packed convert per pair)
+          // g and u rounded to bf16 two at a time (one packed convert per pair)
 #pragma unroll
-            for (int s = 0; s < 4; s += 2) {
-              const uint32_t g2 = pack_bf16x2(acc[i][j][4 * q + s], acc[i][j][4 * q + s + 1]);
-              const uint32_t u2 = pack_bf16x2(acc[i][j + half_fn][4 * q + s], acc[i][j + half_fn][4 * q + s + 1]);
-              hv[s] = swiglu(bf16_bits_to_f32(g2 & 0xFFFFu), bf16_bits_to_f32(u2 & 0xFFFFu));
-              hv[s + 1] = swiglu(bf16_bits_to_f32(g2 >> 16), bf16_bits_to_f32(u2 >> 16));
-            }
-          } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) hv[s] = swiglu(acc[i][j][4 * q + s], acc[i][j + half_fn][4 * q + s]);
+          for (int s = 0; s < 4; s += 2) {
+            const uint32_t g2 = pack_bf16x2(acc[i][j][4 * q + s], acc[i][j][4 * q + s + 1]);
+            const uint32_t u2 = pack_bf16x2(acc[i][j + half_fn][4 * q + s], acc[i][j + half_fn][4 * q + s + 1]);
+            hv[s] = swiglu(bf16_bits_to_f32(g2 & 0xFFFFu), bf16_bits_to_f32(u2 & 0xFFFFu));
+            hv[s + 1] = swiglu(bf16_bits_to_f32(g2 >> 16), bf16_bits_to_f32(u2 >> 16));
           }
           const int col = wn * (BN / 2 / C::WGN) + j * 32 + 8 * q + 4 * half_lane;
           const int c = col >> 3;
