@@ -347,7 +347,8 @@ moe_status moe_unpermute_backward(const uint16_t* dy, const uint16_t* y_perm, co
  * slots left over when fewer than k experts remain get id -1 (a dropped slot
  * to moe_permute) and weight 0. A row of -inf alone (padding) chooses nothing
  * and has lse = -inf. The type's lowest finite value is a logit like any
- * other. A row with a NaN or +inf has NaN weights and lse; a NaN is not chosen.
+ * other. A row with a NaN or +inf has NaN weights (0 in slots that are left
+ * over) and lse; a NaN is not chosen.
  *
  *   routing_w[t, j] = p_{id_j}                    (renormalize = 0)
  *                   = p_{id_j} / sum_l p_{id_l}   (renormalize = 1)
@@ -460,7 +461,9 @@ moe_status moe_grouped_projection_mxfp4(const uint8_t* x_q, const uint8_t* x_sca
  *
  *   x_q, x_scales  [T] token rows of d values
  *   perm           int32 [T*k] as written by moe_permute; NULL with k = 1 when
- *                  the T rows are sorted already
+ *                  the T rows are sorted already. Token rows of 2 GiB and more
+ *                  gathered through it take several times longer for many rows
+ *                  (small tiles); sorted rows without perm do not
  *   w_q, w_scales  [E, 2h] rows of d values, gate rows first
  *   h_buf          bf16 [T*k, h] out (rows past M untouched) */
 moe_status moe_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_scales, const int32_t* perm, int64_t T,

@@ -55,12 +55,14 @@ __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t cap) { return v 
 // before it multiplies them, the weights first, since they do not wait for the dispatch order, and
 // four workgroups share a CU.
 //
-// Measured: gate/up of 4 tokens, 32 experts of 2 x 768 x 2048 with a row each (53 MB) 16 us,
-// of which about 5.5 us pass whatever the size (offsets, prefix, first load, join) and the rest runs
-// at 5.1 TB/s. Tried and slower: 16 x 16 x 128 products (64 consecutive bytes a row and load) 16.7 us
-// and 44 instead of 31 us at 2048 rows; 8 waves 17.2 us; non-temporal weight loads 25 us (a line is
-// read by several loads); all units of a wave asked for at once 21 us (189 registers, so two
-// workgroups a CU).
+// Measured: gate/up of 4 tokens, 32 of 128 experts of 2 x 768 x 2048 (53 MB), 18.9 us with the weights of 24
+// layers in turn, so from HBM, 15.7 us with one layer's again and again, so from the last-level cache. About
+// 5.5 us pass whatever the size (offsets, prefix, first load, join); from HBM the rest runs at 4.0 TB/s (16
+// tokens, all 128 experts, 214 MB: 58.5 us). The projection of the same tokens (27 MB) 12.6 and 10.0 us. Tried, from
+// HBM and from cache: batches of 1 19.6 and 16.4 us (the projection 12.3 and 9.5), of 4 with two workgroups
+// a CU 25.3 and 21.7, non-temporal weight loads 24.1 and 22.8 (a line is read by several loads). From
+// cache alone, 16.2 us at the time: 16 x 16 x 128 products (64 consecutive bytes a row and load) 16.7 us and
+// 44 instead of 31 us at 2048 rows; 8 waves 17.2 us.
 // ---------------------------------------------------------------------------------------------
 constexpr int kThinThreads = 256;
 constexpr int kThinWaves = 4;
@@ -273,11 +275,11 @@ __global__ __launch_bounds__(kThinThreads, 4) void mxfp4_thin_kernel(MxGemmArgs 
 // four are loaded, and the results leave from registers (exchanges between lanes make whole lines)
 // instead of through the ring's memory, so the loads of a new tile have no gap before them.
 //
-// Measured: gate/up of 8192 tokens, top-8 of 64 experts 2048 -> 2 x 768, skewed (392 GFLOP) 133 us; down
-// projection of 65536 rows 768 -> 2048 of the same experts (206 GFLOP, 268 MB written) 89 us; 16 experts
-// 4096 -> 4096, 65536 rows, 3.5 PFLOP/s. The matrix unit is busy 37 and 28% of 279 and 198 thousand cycles
-// (the first two). What the rest is, in thousand cycles: 241 and 135 without SwiGLU and stores, 243 and 160
-// without loads, 232 and 188 without LDS reads, 160 and 99 with products and barriers alone, 11 of them
+// Measured: gate/up of 8192 tokens, top-8 of 64 experts 2048 -> 2 x 768, skewed (392 GFLOP) 129 to 139 us from
+// one card to the next; down projection of 65536 rows 768 -> 2048 of the same experts (206 GFLOP, 268 MB written) 87
+// to 94 us; 16 experts 4096 -> 4096, 65536 rows, 3.5 PFLOP/s. The matrix unit is busy 37 and 28% of 279 and 198
+// thousand cycles (the first two). What the rest is, in thousand cycles: 241 and 135 without SwiGLU and stores, 243
+// and 160 without loads, 232 and 188 without LDS reads, 160 and 99 with products and barriers alone, 11 of them
 // before the first product. So the down projection is bound by its stores, which HBM alone takes 120
 // thousand cycles to write and which overlap half with the next tile's products, gate/up by LDS, loads and
 // matrix unit sharing a stage. Tried and slower: 128 x 128 tiles, two workgroups a CU (gate/up 220, down
@@ -805,7 +807,8 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   if (g.cap_rows == 0) return hipSuccess;
   const int cus = device_cu_count(current_device());
   // The pipelined tiles address values and scales by 32-bit offsets: from the tile's first row (gathered: the first
-  // token), and from one expert's weights. Below 2 GiB also where offset 2^31 marks a chunk past the row.
+  // token), and from one expert's weights. Below 2 GiB also where offset 2^31 marks a chunk past the row. What does not
+  // fit takes the small tiles whatever its size, several times slower where there are many rows (532 and 108 us below).
   const int64_t qp = mx_row_bytes(g.K);
   const int64_t a_span = (g.a_rows != nullptr ? g.a_tokens : 256) * qp;
   const bool fits = a_span <= 0x7FFFFFFFll && g.w_rows * qp <= 0x7FFFFFFFll;
@@ -817,7 +820,7 @@ hipError_t launch_products(const MxGemmArgs& g, hipStream_t stream) {
   // rows of 11 experts 1528 -> 2480 (1248) 27 and 20; 65536 rows of 64 experts 768 -> 2048 532 and 108. And below a mean
   // of 32 rows per expert, where pipelined tiles are mostly empty: gate/up of 64 experts 2048 -> 2 x 768, evenly spread /
   // skewed, 16 rows 30 and 42 / 36 and 42 us, 32 rows 35 and 42 / 45 and 43, 64 rows 60 and 44 / 70 and 45. Over 430
-  // calls of random sizes the choice costs 0.3% against the better of the two (the second condition alone 10%).
+  // calls of random sizes the choice costs 0.2% against the better of the two (always small 8%, always pipelined 78%).
   const int64_t used = g.cap_rows < g.E ? g.cap_rows : g.E;
   const int64_t small_tiles = (g.cap_rows / 32 + used / 2) * ((g.N + kThinCols<GATED> - 1) / kThinCols<GATED>);
   const bool small = small_tiles * (g.K + 256) <= cus * (3 * (g.K + 256) + 3000) || g.cap_rows < (int64_t)32 * g.E;

@@ -21,8 +21,9 @@
 // Small calls are bound by latency (one read, log2 G exchanges a reduction, k rounds), large ones by issuing
 // instructions: a logit costs about 20 for its key and exponential and 8 per round of selection. Measured: 4
 // tokens of 128 experts 4.1 us, 8192 x 64 5.1; 65537 x 100 fp32, top-6, selection 16.9 us, with the losses
-// 22.8 + 5.6, gradient 15.4 (3.4 TB/s). Losses that finish in the first launch would need a counter that
-// somebody clears before it.
+// 23.2 + 5.4, gradient 15.5 (3.4 TB/s; a profiler's times, about a microsecond a launch above those of calls back
+// to back). The second launch stands because a call's workspace may hold anything: a last workgroup that adds the
+// partial sums would count arrivals in it, which asks for a workspace zeroed once (it could set the count back itself).
 
 #include <type_traits>
 
@@ -96,8 +97,8 @@ __device__ __forceinline__ int order_key(float v) {
 }
 
 // e^x for x <= 0: with t = x log2 e = n + f, n whole, e^x = 2^n 2^f. The rounding of t and of log2 e
-// is put back into f, and the scaling by 2^n keeps results below 2^-126, which the hardware's
-// exponential alone would flush. Off by under two units in the last place like the library's, in 11
+// is put back into f (Cody and Waite's reduction: log2 e as the nearest float and the float nearest its
+// remainder), and the scaling by 2^n keeps results below 2^-126, which the hardware's exponential alone would flush. Off by under two units in the last place like the library's, in 11
 // instructions instead of over 20. Below -200 the result is 0 in any case; a NaN stays one.
 __device__ __forceinline__ float exp_nonpositive(float x) {
   x = x < -200.f ? -200.f : x;
@@ -446,10 +447,10 @@ struct RouterBackwardArgs {
   bool renormalize, wide;
   const int32_t* ids;
   const float* w;
-  const int32_t* counts;  // null: no gradient of the losses
+  const int32_t* counts;  // these two are read for the gradient of the losses alone
   const int32_t* tokens;
   const float* d_w;       // null: no gradient of the weights
-  const float* d_losses;
+  const float* d_losses;  // null: no gradient of the losses
   void* d_logits;
 };
 
@@ -641,7 +642,10 @@ hipError_t launch_router_backward(const void* logits, bool f32, int64_t T, int32
   const bool wide = wide_rows(logits, E, f32) && wide_rows(d_logits, E, f32);
   const RouterBackwardArgs a{logits, T, E, k, renormalize, wide, ids, w, counts, tokens, d_w, d_losses, d_logits};
   // Three workgroups a CU: each waits once for the counts, then walks the tokens with the next row on its way. 65537
-  // tokens of 100 experts 15.4 us (2: 16.3, 4: 15.9, 6: 15.9, 8, more than fit at once: 17.5).
+  // tokens, us with 2 / 3 / 4 / 6 / 8 a CU: 100 experts fp32 15.5 / 14.7 / 15.1 / 15.3 / 16.9, bf16 25.9 / 23.8 / 22.7 /
+  // 22.6 / 27.0 (rows of 100 bf16 are read two bytes at a time); 32 bf16 8.5 / 7.6 / 7.6 / 7.4 / 8.0; 64 fp32 11.6 / 10.9 /
+  // 11.5 / 11.3 / 11.7; 128 bf16 17.2 / 16.0 / 16.1 / 16.2 / 17.7; 256 fp32 27.9 / 26.6 / 26.9 / 26.7 / 27.8; 512 bf16 56.4 /
+  // 45.2 / 41.6 / 38.4 / 40.6; 1000 fp32 136 / 143 / 144 / 146 / 146; 8192 tokens of 512 bf16 10.8 / 9.9 / 10.6 / 10.6 / 13.0.
   const int64_t cap = (int64_t)device_cu_count(current_device()) * 3;
   return by_width(E, [&](auto g, auto v) {
     constexpr int G = decltype(g)::value, V = decltype(v)::value;
