@@ -17,7 +17,9 @@
  * experts and their weights; for training its balance and z-losses and the
  * gradient of the logits). The expert step also runs on MXFP4 experts: rows and
  * weights quantised to 4-bit floats with shared scales, their grouped products
- * with fp32 accumulation.
+ * with fp32 accumulation; and on bf16 rows with 4-bit integer weights and group
+ * scales. Around the block stand the norms on the residual stream (forward and
+ * backward) and, for training, the AdamW step over all of a layer's tensors.
  *
  * The grouped expert also comes as its two single-launch halves and with the
  * permuted gather fused into the gate/up projection's loads. The backward
@@ -81,8 +83,10 @@ typedef enum moe_status {
   MOE_ERR_WORKSPACE = 4,          /* workspace_bytes below the call's *_workspace_bytes()       */
   MOE_ERR_UNSUPPORTED_DEVICE = 5, /* the current HIP device is not gfx950, or no device         */
   MOE_ERR_LAUNCH = 6,             /* a HIP error was reported while launching                    */
-  MOE_ERR_TOO_LARGE = 7           /* moe_permute_noalloc only: E * ceil(T*k / 256) exceeds its
+  MOE_ERR_TOO_LARGE = 7,          /* moe_permute_noalloc only: E * ceil(T*k / 256) exceeds its
                                      fixed table of MOE_PERMUTE_NOALLOC_TABLE_ENTRIES            */
+  MOE_ERR_BAD_VALUE = 8           /* a scalar that is no size is out of range (norms: eps, scales;
+                                     AdamW: its settings)                                        */
 } moe_status;
 
 /* Bytes of device workspace moe_permute needs for T tokens, k slots per token
@@ -478,6 +482,190 @@ moe_status moe_gemm_up_swiglu_mxfp4_q(const uint8_t* x_q, const uint8_t* x_scale
                                       int32_t k, const int32_t* offsets, const uint8_t* w_q, const uint8_t* w_scales,
                                       int64_t d, int64_t h, int32_t E, uint8_t* h_q, uint8_t* h_scales,
                                       hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms before and after a block, on the residual stream. With
+ * rs(x) = 1 / sqrt(mean(x^2) + eps) of a row:
+ *
+ *   before   y = x rs(x) w                                       (moe_rmsnorm)
+ *   after    u = y rs(y) w_post  (MOE_NORM_POST), else y  (moe_residual_norm)
+ *            r' = residual_scale r + branch_scale gate u
+ *            n  = r' rs(r') w_next  (MOE_NORM_NEXT: the norm before the block behind)
+ *
+ * The stream (x, r, r' and their gradients) is bf16 or fp32 per its dtype, the
+ * block's side (y, n and their gradients) bf16. Weights are bf16 or fp32 per
+ * w_dtype, a NULL weight is ones. The gate is none, a number a token
+ * (fp32 [T]) or a number a channel ([d], w_dtype). All arithmetic is fp32,
+ * every output is rounded once: n is taken of r' before it is rounded.
+ *
+ * d: a multiple of 8 up to MOE_NORM_MAX_WIDTH. Every tensor 16-byte aligned, the
+ * gate per token 4. A call may write its result over an input of the same type
+ * and shape (the stream in place: r_out = r, d_r = d_r_out).
+ * ------------------------------------------------------------------------- */
+#define MOE_NORM_MAX_WIDTH 16384
+typedef enum moe_norm_flags { MOE_NORM_POST = 1, MOE_NORM_NEXT = 2 } moe_norm_flags;
+typedef enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate;
+
+/* y bf16 [T, d] = RMSNorm(x) w, one launch. */
+moe_status moe_rmsnorm(const void* x, int32_t x_dtype, const void* w, int32_t w_dtype, float eps, int64_t T, int64_t d,
+                       uint16_t* y, hipStream_t stream);
+
+/* After the block, one launch.
+ *
+ *   y       bf16   [T, d]  the block's output
+ *   r       stream [T, d]
+ *   flags   of moe_norm_flags; w_post and w_next are read with theirs only
+ *   r_out   stream [T, d]  out
+ *   n_out   bf16   [T, d]  out, with MOE_NORM_NEXT only */
+moe_status moe_residual_norm(const uint16_t* y, const void* r, int32_t r_dtype, int32_t flags, const void* w_post,
+                             const void* w_next, int32_t w_dtype, const void* gate, int32_t gate_kind,
+                             float residual_scale, float branch_scale, float eps, int64_t T, int64_t d, void* r_out,
+                             uint16_t* n_out, hipStream_t stream);
+
+/* Bytes of device workspace the two backward calls need (the weights' and the
+ * gate's partial sums); 0 for invalid shapes. */
+size_t moe_norm_workspace_bytes(int64_t T, int64_t d);
+
+/* Backward of moe_rmsnorm, two launches (dy + dy_add below for dy, where it is given):
+ * dx = dx_add + rs (dy w - x rs mean(dy w x rs)), dw = sum over rows of dy x rs.
+ *
+ *   dy_add     bf16   [T, d]  a second part of y's gradient (y goes to the router and to
+ *                             the experts); NULL: none
+ *   dx_add     stream [T, d]  gradient that reaches x past the norm; NULL: none
+ *   dx         stream [T, d]  out
+ *   dw         fp32   [d]     out; NULL: not needed (one launch)
+ *   workspace  at least moe_norm_workspace_bytes(T, d) bytes, 16-byte aligned;
+ *              calls and graphs that may run at the same time need one each
+ *
+ * Sums are taken in a fixed order: results repeat bit for bit. */
+moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, const void* x, int32_t x_dtype, const void* w, int32_t w_dtype,
+                                float eps, const void* dx_add, int64_t T, int64_t d, void* dx, float* dw,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Backward of moe_residual_norm from its inputs' y, its output r_out and the
+ * gradients of r_out and n (the rounding of r_out is taken as an identity).
+ *
+ *   d_r_out   stream [T, d]  NULL: none (with MOE_NORM_NEXT only)
+ *   d_n       bf16   [T, d]  with MOE_NORM_NEXT only; d_n_add a second part, or NULL
+ *   y         bf16   [T, d]  read with MOE_NORM_POST or a gate only
+ *   r_out     stream [T, d]  read with MOE_NORM_NEXT only
+ *   d_r       stream [T, d]  out
+ *   d_y       bf16   [T, d]  out
+ *   d_gate    fp32   [T] or [d] as the gate, out; with a gate only
+ *   d_w_post, d_w_next  fp32 [d], out; NULL: not needed */
+moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, const uint16_t* d_n_add,
+                                      const uint16_t* y, const void* r_out, int32_t r_dtype, int32_t flags, const void* w_post, const void* w_next,
+                                      int32_t w_dtype, const void* gate, int32_t gate_kind, float residual_scale,
+                                      float branch_scale, float eps, int64_t T, int64_t d, void* d_r, uint16_t* d_y,
+                                      float* d_gate, float* d_w_post, float* d_w_next, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * AdamW over a list of tensors. For every value p with gradient g, in fp32:
+ *
+ *   m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2
+ *   p = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ * Parameters and gradients are bf16 or fp32, each tensor as it says. The
+ * moments of all tensors lie in two buffers, tensor i's from place `offset` on,
+ * a multiple of 32; so does the optional fp32 copy of the parameters (master),
+ * which the step then reads instead of them. Zeros are the initial moments, and
+ * stay zero between the tensors.
+ *
+ * bits = 32: m, v fp32 [len]. bits = 8: m, v uint8 [len] and a scale byte per 32
+ * values, m_scales, v_scales uint8 [len / 32]; a block's values are multiples of
+ * 2^(byte - 127):
+ *   m  float8 e4m3, the block's largest magnitude in [128, 256), nearest even;
+ *   v  code c: (1 + (c % 8) / 8) 2^(c / 8), 0 for c = 0, the largest with c / 8 = 30;
+ *      nearest even, or at random when stochastic; above zero at least code 1.
+ * A block with an infinity or a NaN gets byte 255 and reads as NaN from then on.
+ *
+ * stochastic: v in 8 bits and bf16 parameters without a master round up or down
+ * at random in proportion to what is dropped; the random bits are a hash of
+ * seed, step and place (offset + index), so a step repeats bit for bit.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_adamw_tensor {
+  void* param;         /* aligned to its element size (16 bytes: whole vectors) */
+  const void* grad;    /* the same */
+  int64_t n;           /* values, 0 allowed */
+  int64_t offset;      /* place of the first value's moments; ascending, not overlapping */
+  int32_t param_dtype; /* moe_dtype */
+  int32_t grad_dtype;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_hyper {
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, eps and weight_decay >= 0 */
+  int64_t step;                               /* t, from 1; below 2^31 */
+  uint32_t seed;
+  int32_t stochastic;
+} moe_adamw_hyper;
+
+/* One step, a launch per 80 tensors. `tensors` and `hyper` are HOST memory and are
+ * free again when the call returns.
+ *
+ *   len            values the moments' buffers hold, a multiple of 32
+ *   master         fp32 [len] or NULL
+ *   lr_ptr         fp32 [1] on the device: the rate instead of hyper->lr; or NULL
+ *   step_ptr       int32 [1] on the device: t instead of hyper->step; or NULL
+ *   grad_scale     fp32 [1] on the device, multiplied to every gradient; or NULL
+ *
+ * The three let a captured step follow what changes from replay to replay. */
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t bits, int64_t len, void* m,
+                          uint8_t* m_scales, void* v, uint8_t* v_scales, float* master, const moe_adamw_hyper* hyper,
+                          const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream);
+
+/* The values of 8-bit moments as bf16 [len] (exact unless below bf16's range), one launch. */
+moe_status moe_adamw_moments(const uint8_t* m, const uint8_t* m_scales, const uint8_t* v, const uint8_t* v_scales,
+                             int64_t len, uint16_t* m_out, uint16_t* v_out, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Expert weights in 4 bits with group scales, W = s (q - z), and the grouped
+ * products of bf16 rows with them: for decode, a few rows an expert, where
+ * reading the weights is the work. For many rows an expert read the weights back
+ * to bf16 and use the bf16 calls.
+ *
+ *   q       uint8 [E, d_out, 16 * ceil(d_in / 32)]  value 2i in the low half of byte i,
+ *                                                   16-byte aligned; what stands behind
+ *                                                   value d_in - 1 is not used (written as 0)
+ *   scales  bf16  [E, ceil(d_in / group), d_out]    16-byte aligned
+ *   zeros   uint8, the same shape, values 0 to 15, 8-byte aligned; NULL: 8 everywhere
+ *   group   32, 64 or 128 consecutive values of the contraction; the last may be shorter
+ * ------------------------------------------------------------------------- */
+
+/* bf16 weights of either layout to q, scales and zeros (NULL: symmetric), one launch.
+ * Symmetric: s = bf16(max |w| / 7), q = 8 + round(w / s). Otherwise, with the range
+ * lo <= 0 <= hi of the group: s = bf16((hi - lo) / 15), z = round(-lo / s),
+ * q = z + round(w / s). Both cut to 0 .. 15; halves round to even. A group with an
+ * infinity or a NaN (or hi - lo past fp32) has a NaN for its scale. */
+moe_status moe_int4_quantize_weights(const uint16_t* w, int32_t w_layout, int64_t d_in, int64_t d_out, int32_t E,
+                                     int32_t group, uint8_t* q, uint16_t* scales, uint8_t* zeros, hipStream_t stream);
+
+/* w bf16 [E, d_out, d_in] (MOE_W_OUT_IN) = bf16(s (q - z)), one launch. */
+moe_status moe_int4_dequantize_weights(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t d_in,
+                                       int64_t d_out, int32_t E, int32_t group, uint16_t* w, hipStream_t stream);
+
+/* moe_grouped_projection with 4-bit weights: y[rows_e] = bf16(x[rows_e] W_e^T), one launch.
+ * Weights enter the products exactly; sums and scales are fp32.
+ *
+ *   x        bf16  [cap_rows, d_in]
+ *   offsets  int32 [E+1], clamped as in the bf16 calls
+ *   y        bf16  [cap_rows, d_out] out (rows past M untouched)
+ *
+ * A row with an infinity gives NaN. */
+moe_status moe_grouped_projection_int4(const uint16_t* x, const int32_t* offsets, const uint8_t* q,
+                                       const uint16_t* scales, const uint8_t* zeros, int32_t group, int64_t cap_rows,
+                                       int64_t d_in, int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream);
+
+/* moe_gemm_up_swiglu(_gather) with 4-bit weights [E, 2h], gate rows first:
+ * h_buf[p] = bf16(SiLU(g) * u), [g | u] = x[perm[p] / k] W_ug[e]^T, SiLU taken of the
+ * fp32 sums, one launch.
+ *
+ *   x      bf16  [T, d]
+ *   perm   int32 [T*k] as written by moe_permute; NULL with k = 1 when the T rows are sorted already
+ *   h_buf  bf16  [T*k, h] out (rows past M untouched) */
+moe_status moe_gemm_up_swiglu_int4(const uint16_t* x, const int32_t* perm, int64_t T, int32_t k, const int32_t* offsets,
+                                   const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int32_t group,
+                                   int64_t d, int64_t h, int32_t E, uint16_t* h_buf, hipStream_t stream);
 
 /* A static, human-readable name for a status code. */
 const char* moe_status_string(moe_status s);

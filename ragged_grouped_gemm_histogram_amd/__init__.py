@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import torch
 
@@ -26,6 +26,7 @@ MAX_EXPERTS = 1024
 MOE_OK = 0
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_f32 = ctypes.c_float
 _SIGNATURES = {
     "moe_permute_workspace_bytes": (_sz, [_i64, _i32, _i32]),
     "moe_permute": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -59,6 +60,22 @@ _SIGNATURES = {
     "moe_gemm_up_swiglu_mxfp4": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp]),
     "moe_gemm_up_swiglu_mxfp4_q": (ctypes.c_int,
                                    [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "moe_rmsnorm": (ctypes.c_int, [_vp, _i32, _vp, _i32, _f32, _i64, _i64, _vp, _vp]),
+    "moe_residual_norm": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _f32, _f32, _f32, _i64, _i64,
+                                         _vp, _vp, _vp]),
+    "moe_norm_workspace_bytes": (_sz, [_i64, _i64]),
+    "moe_rmsnorm_backward": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i32, _f32, _vp, _i64, _i64, _vp, _vp, _vp, _sz,
+                                            _vp]),
+    "moe_residual_norm_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _f32, _f32,
+                                                  _f32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_adamw_step": (ctypes.c_int, [_vp, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_adamw_moments": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "moe_int4_quantize_weights": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "moe_int4_dequantize_weights": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp]),
+    "moe_grouped_projection_int4": (ctypes.c_int,
+                                    [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "moe_gemm_up_swiglu_int4": (ctypes.c_int,
+                                [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -761,6 +778,498 @@ def moe_expert_forward_mxfp4(x: torch.Tensor, expert_ids: torch.Tensor, routing_
     return moe_unpermute(y_perm, p.inv_map, routing_w), p
 
 
+# ------------------------------------------------------------------ 4-bit weights with group scales
+
+
+@dataclass
+class Int4:
+    """Expert weights [E, d_out, width] as s (q - z): q uint8 [E, d_out, 16 * ceil(width / 32)], scales bf16 and zeros
+    uint8 (None: 8 everywhere) [E, ceil(width / group), d_out]."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    zeros: torch.Tensor | None
+    width: int
+    group: int = 128
+
+
+INT4_GROUPS = (32, 64, 128)
+
+
+def _int4_shapes(E: int, d_out: int, width: int, group: int):
+    if group not in INT4_GROUPS:
+        raise ValueError(f"group must be one of {INT4_GROUPS}, got {group}")
+    return (E, d_out, 16 * ((width + 31) // 32)), (E, (width + group - 1) // group, d_out)
+
+
+def _want_int4(w: Int4, name: str, device):
+    if not isinstance(w, Int4):
+        raise TypeError(f"{name} must be an Int4")
+    if not isinstance(w.q, torch.Tensor) or w.q.dim() != 3:
+        raise ValueError(f"{name}.q must be [E, d_out, .]")
+    E, d_out, _ = w.q.shape
+    q, s = _int4_shapes(E, d_out, w.width, w.group)
+    _want(w.q, f"{name}.q", torch.uint8, q, device)
+    _want(w.scales, f"{name}.scales", torch.bfloat16, s, device)
+    if w.zeros is not None:
+        _want(w.zeros, f"{name}.zeros", torch.uint8, s, device)
+    return E, d_out
+
+
+def moe_int4_quantize_weights(w: torch.Tensor, layout: str = "in_out", *, group: int = 128, symmetric: bool = False,
+                              q=None, scales=None, zeros=None) -> Int4:
+    """Expert weights [E, d_in, d_out] ("in_out") or [E, d_out, d_in] ("out_in") rounded to 4 bits with a scale, and
+    unless ``symmetric`` a zero, for every ``group`` values of the contraction (one launch)."""
+    E, d_in, d_out = _w_dims(w, layout)
+    dev = w.device
+    _want(w, "w", torch.bfloat16, tuple(w.shape), dev)
+    q_shape, s_shape = _int4_shapes(E, d_out, d_in, group)
+    q = _out(q, "q", torch.uint8, q_shape, dev)
+    scales = _out(scales, "scales", torch.bfloat16, s_shape, dev)
+    if symmetric and zeros is not None:
+        raise ValueError("symmetric weights have no zeros")
+    zeros = None if symmetric else _out(zeros, "zeros", torch.uint8, s_shape, dev)
+    _check(load_library().moe_int4_quantize_weights(w.data_ptr(), W_LAYOUTS[layout], d_in, d_out, E, group, q.data_ptr(),
+                                                    scales.data_ptr(), _ptr(zeros), _stream(w)),
+           "moe_int4_quantize_weights")
+    return Int4(q, scales, zeros, d_in, group)
+
+
+def moe_int4_dequantize_weights(m: Int4, *, w=None) -> torch.Tensor:
+    """The bf16 weights [E, d_out, d_in] ("out_in") of packed ones, for the bf16 calls (one launch)."""
+    if not isinstance(m, Int4):
+        raise TypeError("expected an Int4")
+    dev = m.q.device
+    E, d_out = _want_int4(m, "m", dev)
+    w = _out(w, "w", torch.bfloat16, (E, d_out, m.width), dev)
+    _check(load_library().moe_int4_dequantize_weights(m.q.data_ptr(), m.scales.data_ptr(), _ptr(m.zeros), m.width, d_out,
+                                                      E, m.group, w.data_ptr(), _stream(m.q)),
+           "moe_int4_dequantize_weights")
+    return w
+
+
+def moe_grouped_projection_int4(x: torch.Tensor, offsets: torch.Tensor, w: Int4, *, y=None) -> torch.Tensor:
+    """Y[rows_e] = bf16(X[rows_e] @ W_e^T) of bf16 rows [cap, d_in] and 4-bit weights [E, d_out, d_in] (one launch).
+    Made for few rows an expert; for many, moe_int4_dequantize_weights and moe_grouped_projection are faster."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [cap_rows, d_in]")
+    dev = x.device
+    E, d_out = _want_int4(w, "w", dev)
+    cap = x.shape[0]
+    _want(x, "x", torch.bfloat16, (cap, w.width), dev)
+    _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    y = _out(y, "y", torch.bfloat16, (cap, d_out), dev)
+    _check(load_library().moe_grouped_projection_int4(x.data_ptr(), offsets.data_ptr(), w.q.data_ptr(),
+                                                      w.scales.data_ptr(), _ptr(w.zeros), w.group, cap, w.width, d_out,
+                                                      E, y.data_ptr(), _stream(x)), "moe_grouped_projection_int4")
+    return y
+
+
+def moe_gemm_up_swiglu_int4(x: torch.Tensor, offsets: torch.Tensor, w_ug: Int4, *, perm=None, k: int = 1,
+                            h_buf=None) -> torch.Tensor:
+    """h_buf[p] = bf16(SiLU(g) * u), [g | u] = X[perm[p] // k] @ W_ug[e]^T, of bf16 token rows [T, d] and 4-bit weights
+    [E, 2h, d] (one launch). Without ``perm`` the rows are sorted already and k is 1."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    dev = x.device
+    E, two_h = _want_int4(w_ug, "w_ug", dev)
+    T, k = x.shape[0], int(k)
+    _want(x, "x", torch.bfloat16, (T, w_ug.width), dev)
+    _want(offsets, "offsets", torch.int32, (E + 1,), dev)
+    if two_h % 2:
+        raise ValueError("w_ug must hold as many gate as up rows")
+    if perm is not None:
+        _want(perm, "perm", torch.int32, (T * k,), dev)
+    elif k != 1:
+        raise ValueError("k other than 1 needs perm")
+    h_buf = _out(h_buf, "h_buf", torch.bfloat16, (T * k, two_h // 2), dev)
+    _check(load_library().moe_gemm_up_swiglu_int4(x.data_ptr(), _ptr(perm), T, k, offsets.data_ptr(), w_ug.q.data_ptr(),
+                                                  w_ug.scales.data_ptr(), _ptr(w_ug.zeros), w_ug.group, w_ug.width,
+                                                  two_h // 2, E, h_buf.data_ptr(), _stream(x)),
+           "moe_gemm_up_swiglu_int4")
+    return h_buf
+
+
+def moe_expert_forward_int4(x: torch.Tensor, expert_ids: torch.Tensor, routing_w: torch.Tensor, w_ug: Int4,
+                            w_down: Int4):
+    """The whole step on 4-bit experts, from bf16 token rows. ``w_ug`` holds [E, 2h] rows of d values, ``w_down``
+    [E, d] rows of h (moe_int4_quantize_weights of the bf16 weights). Returns (y, Permuted)."""
+    k = expert_ids.shape[1]
+    p = moe_permute(x, expert_ids, w_ug.q.shape[0], gather=False)
+    h = moe_gemm_up_swiglu_int4(x, p.offsets, w_ug, perm=p.perm, k=k)
+    y_perm = moe_grouped_projection_int4(h, p.offsets, w_down)
+    return moe_unpermute(y_perm, p.inv_map, routing_w), p
+
+
+# ------------------------------------------------------------------ norms around a block
+
+NORM_MAX_WIDTH = 16384
+_NORM_POST, _NORM_NEXT = 1, 2
+_GATE_NONE, _GATE_TOKEN, _GATE_CHANNEL = 0, 1, 2
+
+
+def _stream_rows(r: torch.Tensor, name: str):
+    """(T, d, dtype code, device) of rows of the residual stream."""
+    if not isinstance(r, torch.Tensor) or r.dim() != 2:
+        raise ValueError(f"{name} must be [T, d]")
+    code = _LOGITS.get(r.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {r.dtype}")
+    T, d = r.shape
+    _want(r, name, r.dtype, (T, d), r.device)
+    return T, d, code, r.device
+
+
+def _norm_weights(d: int, dev, **weights) -> int:
+    """dtype code of the weights that are given, all of one dtype."""
+    dtype = None
+    for name, w in weights.items():
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.dtype not in _LOGITS:
+            raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+        dtype = dtype or w.dtype
+        _want(w, name, dtype, (d,), dev)
+    return _LOGITS[dtype or torch.bfloat16]
+
+
+def _norm_gate(gate, T: int, d: int, dev):
+    """(kind, the gate if it is one per channel)"""
+    if gate is None:
+        return _GATE_NONE, None
+    if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+        _want(gate, "gate", torch.float32, (T, 1), dev)
+        return _GATE_TOKEN, None
+    return _GATE_CHANNEL, gate
+
+
+def norm_workspace_bytes(T: int, d: int) -> int:
+    return int(load_library().moe_norm_workspace_bytes(T, d))
+
+
+def _norm_workspace(workspace, T: int, d: int, dev):
+    if workspace is None:
+        return torch.empty((norm_workspace_bytes(T, d),), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    return workspace
+
+
+def moe_rmsnorm(x: torch.Tensor, w: torch.Tensor | None = None, *, eps: float = 1e-6, y=None) -> torch.Tensor:
+    """The norm before a block: bf16 rows x / sqrt(mean(x^2) + eps) * w of the stream's bf16 or fp32 rows (one launch)."""
+    T, d, dtype, dev = _stream_rows(x, "x")
+    w_dtype = _norm_weights(d, dev, w=w)
+    y = _out(y, "y", torch.bfloat16, (T, d), dev)
+    _check(load_library().moe_rmsnorm(x.data_ptr(), dtype, _ptr(w), w_dtype, eps, T, d, y.data_ptr(), _stream(x)),
+           "moe_rmsnorm")
+    return y
+
+
+def moe_rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor | None = None, *, eps: float = 1e-6,
+                         dy_add=None, dx_add=None, dx=None, dw=None, workspace=None):
+    """(dx, dw) of moe_rmsnorm: dx in the stream's type with ``dx_add``, the gradient that reaches x past the norm,
+    added; dw fp32, None without a weight (two launches). ``dy_add`` is a second part of y's gradient."""
+    T, d, dtype, dev = _stream_rows(x, "x")
+    w_dtype = _norm_weights(d, dev, w=w)
+    _want(dy, "dy", torch.bfloat16, (T, d), dev)
+    if dy_add is not None:
+        _want(dy_add, "dy_add", torch.bfloat16, (T, d), dev)
+    if dx_add is not None:
+        _want(dx_add, "dx_add", x.dtype, (T, d), dev)
+    dx = _out(dx, "dx", x.dtype, (T, d), dev)
+    dw = None if w is None else _out(dw, "dw", torch.float32, (d,), dev)
+    workspace = _norm_workspace(workspace, T, d, dev)
+    _check(load_library().moe_rmsnorm_backward(dy.data_ptr(), _ptr(dy_add), x.data_ptr(), dtype, _ptr(w), w_dtype, eps,
+                                               _ptr(dx_add), T, d, dx.data_ptr(), _ptr(dw), workspace.data_ptr(), workspace.numel(),
+                                               _stream(x)), "moe_rmsnorm_backward")
+    return dx, dw
+
+
+def moe_residual_norm(y: torch.Tensor, r: torch.Tensor, *, post_norm: bool = False, w_post=None, gate=None,
+                      residual_scale: float = 1.0, branch_scale: float = 1.0, next_norm: bool = True, w_next=None,
+                      eps: float = 1e-6, r_out=None, n_out=None):
+    """What follows a block: r' = residual_scale * r + branch_scale * gate * u with u = RMSNorm(y) * w_post
+    (``post_norm``) or y, and n = RMSNorm(r') * w_next for the block behind (``next_norm``). ``gate`` is fp32 [T, 1],
+    a number a token, or [d], a number a channel. Returns (r', n), n None without the next norm (one launch)."""
+    T, d, dtype, dev = _stream_rows(r, "r")
+    _want(y, "y", torch.bfloat16, (T, d), dev)
+    kind, channel = _norm_gate(gate, T, d, dev)
+    if (w_post is not None and not post_norm) or (w_next is not None and not next_norm):
+        raise ValueError("a weight of a norm that is not asked for")
+    w_dtype = _norm_weights(d, dev, w_post=w_post, w_next=w_next, gate=channel)
+    r_out = _out(r_out, "r_out", r.dtype, (T, d), dev)
+    n_out = _out(n_out, "n_out", torch.bfloat16, (T, d), dev) if next_norm else None
+    flags = (_NORM_POST if post_norm else 0) | (_NORM_NEXT if next_norm else 0)
+    _check(load_library().moe_residual_norm(y.data_ptr(), r.data_ptr(), dtype, flags, _ptr(w_post), _ptr(w_next), w_dtype,
+                                            _ptr(gate), kind, residual_scale, branch_scale, eps, T, d, r_out.data_ptr(),
+                                            _ptr(n_out), _stream(r)), "moe_residual_norm")
+    return r_out, n_out
+
+
+@dataclass
+class ResidualNormGrads:
+    d_r: torch.Tensor  # the stream's type [T, d]
+    d_y: torch.Tensor  # bf16 [T, d]
+    d_gate: torch.Tensor | None  # fp32, the gate's shape
+    d_w_post: torch.Tensor | None  # fp32 [d]
+    d_w_next: torch.Tensor | None  # fp32 [d]
+
+
+def moe_residual_norm_backward(d_r_out: torch.Tensor | None, d_n: torch.Tensor | None, y: torch.Tensor,
+                               r_out: torch.Tensor, *, post_norm: bool = False, w_post=None, gate=None,
+                               residual_scale: float = 1.0, branch_scale: float = 1.0, next_norm: bool = True,
+                               w_next=None, eps: float = 1e-6, d_n_add=None, d_r=None, d_y=None, d_gate=None,
+                               d_w_post=None, d_w_next=None, workspace=None) -> ResidualNormGrads:
+    """Gradients of moe_residual_norm from those of r' (None: none) and n (``d_n_add``: a second part of it), with the
+    block's output y and r' as the forward wrote it; weights' and gate's in fp32 (two launches)."""
+    T, d, dtype, dev = _stream_rows(r_out, "r_out")
+    _want(y, "y", torch.bfloat16, (T, d), dev)
+    kind, channel = _norm_gate(gate, T, d, dev)
+    if (w_post is not None and not post_norm) or (w_next is not None and not next_norm):
+        raise ValueError("a weight of a norm that is not asked for")
+    w_dtype = _norm_weights(d, dev, w_post=w_post, w_next=w_next, gate=channel)
+    if d_r_out is not None:
+        _want(d_r_out, "d_r_out", r_out.dtype, (T, d), dev)
+    elif not next_norm:
+        raise ValueError("without the next norm the only gradient is that of r_out")
+    if next_norm:
+        _want(d_n, "d_n", torch.bfloat16, (T, d), dev)
+        if d_n_add is not None:
+            _want(d_n_add, "d_n_add", torch.bfloat16, (T, d), dev)
+    elif d_n is not None or d_n_add is not None:
+        raise ValueError("a gradient of a norm that is not asked for")
+    d_r = _out(d_r, "d_r", r_out.dtype, (T, d), dev)
+    d_y = _out(d_y, "d_y", torch.bfloat16, (T, d), dev)
+    d_gate = None if gate is None else _out(d_gate, "d_gate", torch.float32, tuple(gate.shape), dev)
+    d_w_post = None if w_post is None else _out(d_w_post, "d_w_post", torch.float32, (d,), dev)
+    d_w_next = None if w_next is None else _out(d_w_next, "d_w_next", torch.float32, (d,), dev)
+    workspace = _norm_workspace(workspace, T, d, dev)
+    flags = (_NORM_POST if post_norm else 0) | (_NORM_NEXT if next_norm else 0)
+    _check(load_library().moe_residual_norm_backward(
+        _ptr(d_r_out), _ptr(d_n), _ptr(d_n_add), y.data_ptr(), r_out.data_ptr(), dtype, flags, _ptr(w_post),
+        _ptr(w_next), w_dtype, _ptr(gate), kind, residual_scale, branch_scale, eps, T, d, d_r.data_ptr(), d_y.data_ptr(),
+        _ptr(d_gate), _ptr(d_w_post), _ptr(d_w_next), workspace.data_ptr(), workspace.numel(), _stream(r_out)),
+        "moe_residual_norm_backward")
+    return ResidualNormGrads(d_r, d_y, d_gate, d_w_post, d_w_next)
+
+
+# ------------------------------------------------------------------ a layer on the residual stream
+
+
+@dataclass
+class MoeLayer:
+    """What moe_layer_forward gives: the stream behind the layer, the next norm's rows if asked for, and what the backward
+    reads."""
+    r_out: torch.Tensor
+    n_out: torch.Tensor | None
+    routed: Routed
+    p: Permuted
+    r: torch.Tensor
+    n: torch.Tensor  # the rows the router and the experts read
+    logits: torch.Tensor
+    rows: torch.Tensor  # int32 [2]: the router's product has one group
+    h_buf: torch.Tensor
+    u: torch.Tensor
+    y_perm: torch.Tensor
+    y: torch.Tensor
+    eps: float
+    after: dict  # arguments of moe_residual_norm
+
+
+def moe_layer_forward(r: torch.Tensor, w_norm, w_router: torch.Tensor, w_ug: torch.Tensor, w_down: torch.Tensor, k: int,
+                      *, renormalize: bool = True, eps: float = 1e-6, post_norm: bool = False, w_post=None, gate=None,
+                      residual_scale: float = 1.0, branch_scale: float = 1.0, next_norm: bool = False,
+                      w_next=None) -> MoeLayer:
+    """A routed layer on the residual stream ``r``, bf16 or fp32 [T, d]: norm, router (``w_router`` bf16 [E, d], E a
+    multiple of 8), experts, and moe_residual_norm with the arguments after ``eps``. Its losses are in ``routed``."""
+    n = moe_rmsnorm(r, w_norm, eps=eps)
+    rows = torch.arange(2, dtype=torch.int32, device=r.device) * r.shape[0]
+    logits = moe_grouped_projection(n, rows, w_router[None], "out_in")
+    routed = moe_router_topk_losses(logits, k, renormalize=renormalize)
+    p = moe_permute(n, routed.expert_ids, w_ug.shape[0])
+    h_buf, u = moe_gemm_up_swiglu_u(p.x_perm, p.offsets, w_ug)
+    y_perm = moe_gemm_down(h_buf, p.offsets, w_down)
+    y = moe_unpermute(y_perm, p.inv_map, routed.routing_w)
+    after = dict(post_norm=post_norm, w_post=w_post, gate=gate, residual_scale=residual_scale, branch_scale=branch_scale,
+                 next_norm=next_norm, w_next=w_next, eps=eps)
+    r_out, n_out = moe_residual_norm(y, r, **after)
+    return MoeLayer(r_out, n_out, routed, p, r, n, logits, rows, h_buf, u, y_perm, y, eps, after)
+
+
+def moe_layer_backward(d_r_out: torch.Tensor | None, f: MoeLayer, w_norm, w_router: torch.Tensor, w_ug: torch.Tensor,
+                       w_down: torch.Tensor, *, d_n_out=None, d_n_add=None, d_losses=None) -> dict:
+    """Gradients of moe_layer_forward from those of its r_out, its n_out (in up to two parts) and its losses: dr in the
+    stream's type; dw_router, dw_ug, dw_down bf16; dw_norm, dw_post, dw_next and d_gate fp32, None where there is none."""
+    b = moe_residual_norm_backward(d_r_out, d_n_out, f.y, f.r_out, d_n_add=d_n_add, **f.after)
+    e = moe_expert_backward(b.d_y, f.p, f.routed.routing_w, w_ug, w_down, f.h_buf, f.y_perm, f.u)
+    d_logits = moe_router_backward(f.logits, f.routed, e["d_routing_w"], d_losses)
+    dw_router = moe_grouped_wgrad(f.n, d_logits, f.rows, "out_in")[0]
+    by_router = moe_grouped_dgrad(d_logits, f.rows, w_router[None], "out_in")
+    dr, dw_norm = moe_rmsnorm_backward(e["dx"], f.r, w_norm, eps=f.eps, dy_add=by_router, dx_add=b.d_r)
+    return {"dr": dr, "dw_norm": dw_norm, "dw_router": dw_router, "dw_ug": e["dw_ug"], "dw_down": e["dw_down"],
+            "dw_post": b.d_w_post, "dw_next": b.d_w_next, "d_gate": b.d_gate, "d_logits": d_logits}
+
+
+# ------------------------------------------------------------------ AdamW
+
+
+class _AdamTensor(ctypes.Structure):
+    _fields_ = [("param", _vp), ("grad", _vp), ("n", _i64), ("offset", _i64), ("param_dtype", _i32), ("grad_dtype", _i32)]
+
+
+class _AdamHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", _i64), ("seed", ctypes.c_uint32), ("stochastic", _i32)]
+
+
+@dataclass
+class Blocks8:
+    """Moments in 8 bits: q uint8 [len] and a scale byte per 32 values, scales uint8 [len / 32]."""
+    q: torch.Tensor
+    scales: torch.Tensor
+
+
+def _moment_places(params) -> tuple[list[int], int]:
+    places, n = [], 0
+    for p in params:
+        places.append(n)
+        n += (p.numel() + 31) // 32 * 32
+    return places, n
+
+
+@dataclass
+class AdamW:
+    """What AdamW keeps for a list of parameters: one buffer a moment, fp32 [len] or Blocks8 of len values, with tensor
+    i's values from ``places[i]`` on (the sizes before it, each rounded up to 32), and with ``master`` a fp32 copy of
+    the parameters at the same places. moe_adamw_state makes one."""
+    params: list
+    exp_avg: torch.Tensor | Blocks8
+    exp_avg_sq: torch.Tensor | Blocks8
+    master: torch.Tensor | None = None
+    places: list = field(init=False, repr=False)
+    len: int = field(init=False, repr=False)
+    bits: int = field(init=False)
+
+    def __post_init__(self):
+        self.params = list(self.params)
+        if not self.params:
+            raise ValueError("no parameters")
+        dev = self.params[0].device
+        spans = []
+        for i, p in enumerate(self.params):
+            if not isinstance(p, torch.Tensor) or p.dtype not in _LOGITS:
+                raise TypeError(f"params[{i}] must be a bfloat16 or float32 tensor")
+            _want(p, f"params[{i}]", p.dtype, tuple(p.shape), dev)
+            if p.numel():
+                spans.append((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()))
+        spans.sort()
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters share memory: each value is stepped once")
+        self.places, self.len = _moment_places(self.params)
+        self.bits = 8 if isinstance(self.exp_avg, Blocks8) else 32
+        for name in ("exp_avg", "exp_avg_sq"):
+            m = getattr(self, name)
+            if self.bits == 32:
+                _want(m, name, torch.float32, (self.len,), dev)
+            else:
+                if not isinstance(m, Blocks8):
+                    raise TypeError(f"{name} must be a Blocks8 as exp_avg is")
+                _want(m.q, f"{name}.q", torch.uint8, (self.len,), dev)
+                _want(m.scales, f"{name}.scales", torch.uint8, (self.len // 32,), dev)
+        if self.master is not None:
+            _want(self.master, "master", torch.float32, (self.len,), dev)
+        self._table = (_AdamTensor * len(self.params))()
+        self._hyper = _AdamHyper()
+        self._specs = []
+        for t, p, at in zip(self._table, self.params, self.places):
+            t.n, t.offset, t.param_dtype = p.numel(), at, _LOGITS[p.dtype]
+            self._specs.append((p.dtype, p.shape))
+
+
+def moe_adamw_state(params, *, bits: int = 32, master: bool = False) -> AdamW:
+    """Zero moments in 32 or 8 bits for a list of parameters, and with ``master`` a fp32 copy of them, which the steps
+    then read and write besides the parameters."""
+    params = list(params)
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+    if not params:
+        raise ValueError("no parameters")
+    dev = params[0].device
+    places, n = _moment_places(params)
+
+    def zeros():
+        if bits == 32:
+            return torch.zeros(n, device=dev)
+        return Blocks8(torch.zeros(n, dtype=torch.uint8, device=dev), torch.zeros(n // 32, dtype=torch.uint8, device=dev))
+
+    copy = None
+    if master:
+        copy = torch.zeros(n, device=dev)
+        for p, at in zip(params, places):
+            copy[at:at + p.numel()] = p.detach().reshape(-1)
+    return AdamW(params, zeros(), zeros(), copy)
+
+
+def _device_scalar(v, name: str, dtype: torch.dtype, device):
+    """The pointer of a one-value tensor."""
+    return _want(v, name, dtype, (1,), device).data_ptr()
+
+
+def moe_adamw_step(state: AdamW, grads, *, lr, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, step=1,
+                   grad_scale: torch.Tensor | None = None, seed: int | None = None) -> None:
+    """One AdamW step of ``state.params`` in place, a launch per 80 tensors. ``step`` counts from 1. ``lr`` may be a
+    number or a fp32 [1] tensor on the device, ``step`` an int or an int32 [1] tensor, for steps captured in a graph;
+    ``grad_scale`` fp32 [1] is multiplied to the gradients (a clipping factor). A ``seed`` rounds the second moment in 8
+    bits, and bf16 parameters without a master, at random in proportion; without one they round to nearest."""
+    params, table, h = state.params, state._table, state._hyper
+    if len(grads) != len(params):
+        raise ValueError(f"{len(params)} parameters but {len(grads)} gradients")
+    dev = params[0].device
+    index = dev.index
+    # (the common case of a tensor that fits, in one expression; _want names what does not)
+    for t, p, g, (dtype, shape) in zip(table, params, grads, state._specs):
+        if not (p.dtype is dtype and p.shape == shape and p.get_device() == index and p.is_contiguous()):
+            _want(p, "a parameter", dtype, tuple(shape), dev)
+        code = _LOGITS.get(g.dtype) if isinstance(g, _Tensor) else None
+        if code is None:
+            raise TypeError("gradients must be bfloat16 or float32 tensors")
+        if not (g.shape == shape and g.get_device() == index and g.is_contiguous()):
+            _want(g, "a gradient", g.dtype, tuple(shape), dev)
+        t.param, t.grad, t.grad_dtype = p.data_ptr(), g.data_ptr(), code
+    lr_ptr = step_ptr = None
+    if isinstance(lr, _Tensor):
+        lr_ptr, lr = _device_scalar(lr, "lr", torch.float32, dev), 0.0
+    if isinstance(step, _Tensor):
+        step_ptr, step = _device_scalar(step, "step", torch.int32, dev), 1
+    if grad_scale is not None:
+        grad_scale = _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
+    if seed is not None and not 0 <= seed < 1 << 32:
+        raise ValueError("seed must fit 32 bits")
+    h.lr, (h.beta1, h.beta2), h.eps, h.weight_decay, h.step = lr, betas, eps, weight_decay, step
+    h.seed, h.stochastic = (0, 0) if seed is None else (seed, 1)
+    if state.bits == 32:
+        m, ms, v, vs = state.exp_avg.data_ptr(), None, state.exp_avg_sq.data_ptr(), None
+    else:
+        m, ms = state.exp_avg.q.data_ptr(), state.exp_avg.scales.data_ptr()
+        v, vs = state.exp_avg_sq.q.data_ptr(), state.exp_avg_sq.scales.data_ptr()
+    _check(load_library().moe_adamw_step(ctypes.addressof(table), len(params), state.bits, state.len, m, ms, v, vs,
+                                         _ptr(state.master), ctypes.addressof(h), lr_ptr, step_ptr, grad_scale,
+                                         _stream(params[0])), "moe_adamw_step")
+
+
+def moe_adamw_moments(state: AdamW, *, exp_avg=None, exp_avg_sq=None):
+    """The values of both moments, [len]: the fp32 buffers themselves, or bf16 of 8-bit ones (one launch)."""
+    if state.bits == 32:
+        return state.exp_avg, state.exp_avg_sq
+    dev = state.exp_avg.q.device
+    exp_avg = _out(exp_avg, "exp_avg", torch.bfloat16, (state.len,), dev)
+    exp_avg_sq = _out(exp_avg_sq, "exp_avg_sq", torch.bfloat16, (state.len,), dev)
+    _check(load_library().moe_adamw_moments(state.exp_avg.q.data_ptr(), state.exp_avg.scales.data_ptr(),
+                                            state.exp_avg_sq.q.data_ptr(), state.exp_avg_sq.scales.data_ptr(), state.len,
+                                            exp_avg.data_ptr(), exp_avg_sq.data_ptr(), _stream(state.exp_avg.q)),
+           "moe_adamw_moments")
+    return exp_avg, exp_avg_sq
+
+
 __all__ = [
     "LIB_PATH", "MAX_EXPERTS", "MoeError", "Permuted", "grouped_swiglu_expert", "header_functions", "load_library",
     "grouped_swiglu_expert_gather", "moe_expert_forward", "moe_gemm_down", "moe_gemm_up_swiglu",
@@ -772,4 +1281,9 @@ __all__ = [
     "router_workspace_bytes", "Mxfp4", "mxfp4_row_bytes", "mxfp4_scale_bytes", "moe_mxfp4_quantize",
     "moe_mxfp4_quantize_weights", "moe_mxfp4_dequantize", "moe_grouped_projection_mxfp4", "moe_gemm_up_swiglu_mxfp4",
     "moe_gemm_up_swiglu_mxfp4_q", "moe_expert_forward_mxfp4",
+    "Int4", "INT4_GROUPS", "moe_int4_quantize_weights", "moe_int4_dequantize_weights", "moe_grouped_projection_int4",
+    "moe_gemm_up_swiglu_int4", "moe_expert_forward_int4",
+    "NORM_MAX_WIDTH", "ResidualNormGrads", "moe_rmsnorm", "moe_rmsnorm_backward", "moe_residual_norm",
+    "moe_residual_norm_backward", "norm_workspace_bytes", "MoeLayer", "moe_layer_forward", "moe_layer_backward",
+    "AdamW", "Blocks8", "moe_adamw_state", "moe_adamw_step", "moe_adamw_moments",
 ]

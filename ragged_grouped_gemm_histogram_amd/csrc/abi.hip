@@ -2,6 +2,7 @@
 // Nothing here allocates, synchronises or reads device data.
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "common.h"
@@ -50,6 +51,8 @@ moe_status check_gemm_shape(int64_t cap_rows, int64_t d, int64_t h, int32_t E) {
   return MOE_OK;
 }
 
+constexpr int64_t kMaxMoments = int64_t(1) << 40;  // values of AdamW's moments, more than memory holds
+
 inline uintptr_t logit_bytes(int32_t dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
 moe_status check_router_shape(int32_t dtype, int64_t T, int32_t E, int32_t k) {
@@ -78,6 +81,46 @@ moe_status check_up_mxfp4(const void* x_q, const void* x_scales, const void* per
       misaligned(out, 16) || misaligned(out2, 16) || misaligned(offsets, 4) || misaligned(perm, 4))
     return MOE_ERR_MISALIGNED;
   return check_device();
+}
+
+// Scalars of the norms: eps not negative, everything finite.
+inline bool bad_norm_values(float a, float b, float eps) {
+  return !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(eps) || eps < 0.0f;
+}
+
+inline bool bad_dtype(int32_t dtype) { return dtype != MOE_BF16 && dtype != MOE_F32; }
+
+moe_status check_norm_shape(int32_t x_dtype, int32_t w_dtype, int64_t T, int64_t d) {
+  if (bad_dtype(x_dtype) || bad_dtype(w_dtype) || T < 0 || T > kMaxSlots || bad_width(d) || d > MOE_NORM_MAX_WIDTH)
+    return MOE_ERR_BAD_SHAPE;
+  return MOE_OK;
+}
+
+// What moe_residual_norm and its backward read as flags and gate say.
+moe_status check_residual_norm(int32_t r_dtype, int32_t flags, const void* w_post, const void* w_next, int32_t w_dtype,
+                               const void* gate, int32_t gate_kind, float a, float b, float eps, int64_t T, int64_t d) {
+  const moe_status st = check_norm_shape(r_dtype, w_dtype, T, d);
+  if (st != MOE_OK) return st;
+  if ((flags & ~(MOE_NORM_POST | MOE_NORM_NEXT)) != 0 || gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_CHANNEL)
+    return MOE_ERR_BAD_SHAPE;
+  if (bad_norm_values(a, b, eps)) return MOE_ERR_BAD_VALUE;
+  if ((gate_kind == MOE_GATE_TOKEN && missing(gate, T)) || (gate_kind == MOE_GATE_CHANNEL && gate == nullptr))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(w_post, 16) || misaligned(w_next, 16) || misaligned(gate, gate_kind == MOE_GATE_TOKEN ? 4 : 16))
+    return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+moe_status check_int4(int64_t cap_rows, int64_t d_in, int64_t d_out, int32_t E, int32_t group) {
+  if (group != 32 && group != 64 && group != 128) return MOE_ERR_BAD_SHAPE;
+  return check_gemm_shape(cap_rows, d_in, d_out, E);
+}
+
+// Pointers of the packed weights.
+moe_status check_int4_weights(const void* q, const void* scales, const void* zeros) {
+  if (q == nullptr || scales == nullptr) return MOE_ERR_NULL_POINTER;
+  if (misaligned(q, 16) || misaligned(scales, 16) || misaligned(zeros, 8)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
 }
 
 }  // namespace
@@ -501,6 +544,195 @@ moe_status moe_gemm_up_swiglu_mxfp4_q(const uint8_t* x_q, const uint8_t* x_scale
                                               h_q, h_scales, stream));
 }
 
+// ------------------------------------------------------------------ norms around a block
+
+moe_status moe_rmsnorm(const void* x, int32_t x_dtype, const void* w, int32_t w_dtype, float eps, int64_t T, int64_t d,
+                       uint16_t* y, hipStream_t stream) {
+  moe_status st = check_norm_shape(x_dtype, w_dtype, T, d);
+  if (st != MOE_OK) return st;
+  if (bad_norm_values(1.0f, 1.0f, eps)) return MOE_ERR_BAD_VALUE;
+  if (missing(x, T) || missing(y, T)) return MOE_ERR_NULL_POINTER;
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(y, 16)) return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_norm(x, x_dtype == MOE_F32, nullptr, nullptr, w, nullptr, MOE_GATE_NONE, w_dtype == MOE_F32,
+                              false, true, 1.0f, 1.0f, eps, T, d, nullptr, y, stream));
+}
+
+moe_status moe_residual_norm(const uint16_t* y, const void* r, int32_t r_dtype, int32_t flags, const void* w_post,
+                             const void* w_next, int32_t w_dtype, const void* gate, int32_t gate_kind,
+                             float residual_scale, float branch_scale, float eps, int64_t T, int64_t d, void* r_out,
+                             uint16_t* n_out, hipStream_t stream) {
+  moe_status st = check_residual_norm(r_dtype, flags, w_post, w_next, w_dtype, gate, gate_kind, residual_scale,
+                                      branch_scale, eps, T, d);
+  if (st != MOE_OK) return st;
+  const bool next = (flags & MOE_NORM_NEXT) != 0;
+  if (missing(y, T) || missing(r, T) || missing(r_out, T) || (next && missing(n_out, T))) return MOE_ERR_NULL_POINTER;
+  if (misaligned(y, 16) || misaligned(r, 16) || misaligned(r_out, 16) || misaligned(n_out, 16)) return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_norm(r, r_dtype == MOE_F32, y, w_post, w_next, gate, gate_kind, w_dtype == MOE_F32,
+                              (flags & MOE_NORM_POST) != 0, next, residual_scale, branch_scale, eps, T, d, r_out, n_out,
+                              stream));
+}
+
+size_t moe_norm_workspace_bytes(int64_t T, int64_t d) {
+  if (check_norm_shape(MOE_BF16, MOE_BF16, T, d) != MOE_OK) return 0;
+  return (size_t)norm_partial_rows(T, d) * (size_t)d * 3 * sizeof(float);
+}
+
+moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, const void* x, int32_t x_dtype, const void* w, int32_t w_dtype,
+                                float eps, const void* dx_add, int64_t T, int64_t d, void* dx, float* dw,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe_status st = check_norm_shape(x_dtype, w_dtype, T, d);
+  if (st != MOE_OK) return st;
+  if (bad_norm_values(1.0f, 1.0f, eps)) return MOE_ERR_BAD_VALUE;
+  if (missing(dy, T) || missing(x, T) || missing(dx, T) || missing(workspace, T)) return MOE_ERR_NULL_POINTER;
+  if (misaligned(dy, 16) || misaligned(dy_add, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(dx_add, 16) || misaligned(dx, 16) ||
+      misaligned(dw, 4) || misaligned(workspace, 16))
+    return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < moe_norm_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_norm_backward(dx_add, dy, dy_add, nullptr, x, x_dtype == MOE_F32, nullptr, w, nullptr, MOE_GATE_NONE,
+                                       w_dtype == MOE_F32, false, false, true, 1.0f, 1.0f, eps, T, d, dx, nullptr,
+                                       nullptr, nullptr, dw, static_cast<float*>(workspace), stream));
+}
+
+moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, const uint16_t* d_n_add,
+                                      const uint16_t* y, const void* r_out, int32_t r_dtype, int32_t flags, const void* w_post, const void* w_next,
+                                      int32_t w_dtype, const void* gate, int32_t gate_kind, float residual_scale,
+                                      float branch_scale, float eps, int64_t T, int64_t d, void* d_r, uint16_t* d_y,
+                                      float* d_gate, float* d_w_post, float* d_w_next, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream) {
+  moe_status st = check_residual_norm(r_dtype, flags, w_post, w_next, w_dtype, gate, gate_kind, residual_scale,
+                                      branch_scale, eps, T, d);
+  if (st != MOE_OK) return st;
+  const bool post = (flags & MOE_NORM_POST) != 0, next = (flags & MOE_NORM_NEXT) != 0;
+  const bool gated = gate_kind != MOE_GATE_NONE;
+  if ((!next && missing(d_r_out, T)) || (next && (missing(d_n, T) || missing(r_out, T))) ||
+      ((post || gated) && missing(y, T)) || missing(d_r, T) || missing(d_y, T) || missing(workspace, T) ||
+      (gated && missing(d_gate, gate_kind == MOE_GATE_TOKEN ? T : d)))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(d_r_out, 16) || misaligned(d_n, 16) || misaligned(d_n_add, 16) || misaligned(y, 16) || misaligned(r_out, 16) ||
+      misaligned(d_r, 16) || misaligned(d_y, 16) || misaligned(d_gate, 4) || misaligned(d_w_post, 4) ||
+      misaligned(d_w_next, 4) || misaligned(workspace, 16))
+    return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < moe_norm_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_norm_backward(d_r_out, d_n, d_n_add, y, r_out, r_dtype == MOE_F32, w_post, w_next, gate, gate_kind,
+                                       w_dtype == MOE_F32, true, post, next, residual_scale, branch_scale, eps, T, d, d_r,
+                                       d_y, d_gate, d_w_post, d_w_next, static_cast<float*>(workspace), stream));
+}
+
+// ------------------------------------------------------------------ AdamW
+
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t bits, int64_t len, void* m,
+                          uint8_t* m_scales, void* v, uint8_t* v_scales, float* master, const moe_adamw_hyper* hyper,
+                          const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream) {
+  if (count < 0 || len < 0 || len > kMaxMoments || len % 32 != 0 || (bits != 8 && bits != 32)) return MOE_ERR_BAD_SHAPE;
+  if (hyper == nullptr || missing(tensors, count) || missing(m, len) || missing(v, len) ||
+      (bits == 8 && (missing(m_scales, len) || missing(v_scales, len))))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(m, 16) || misaligned(v, 16) || misaligned(master, 16) || misaligned(lr_ptr, 4) ||
+      misaligned(step_ptr, 4) || misaligned(grad_scale, 4))
+    return MOE_ERR_MISALIGNED;
+  const moe_adamw_hyper& h = *hyper;
+  if (!std::isfinite(h.lr) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0) ||
+      !std::isfinite(h.eps) || h.eps < 0.0 || !std::isfinite(h.weight_decay) || h.weight_decay < 0.0 || h.step < 1 ||
+      h.step > kMaxSlots)
+    return MOE_ERR_BAD_VALUE;
+  int64_t free_from = 0;  // places before it belong to earlier tensors
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (bad_dtype(t.param_dtype) || bad_dtype(t.grad_dtype) || t.n < 0 || t.offset < free_from || t.offset % 32 != 0 ||
+        t.offset > len || t.n > len - t.offset)
+      return MOE_ERR_BAD_SHAPE;
+    if (missing(t.param, t.n) || missing(t.grad, t.n)) return MOE_ERR_NULL_POINTER;
+    if (misaligned(t.param, logit_bytes(t.param_dtype)) || misaligned(t.grad, logit_bytes(t.grad_dtype)))
+      return MOE_ERR_MISALIGNED;
+    free_from = t.offset + (t.n + 31) / 32 * 32;
+  }
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_adamw(tensors, count, bits == 8, m, m_scales, v, v_scales, master, h, lr_ptr, step_ptr,
+                               grad_scale, stream));
+}
+
+moe_status moe_adamw_moments(const uint8_t* m, const uint8_t* m_scales, const uint8_t* v, const uint8_t* v_scales,
+                             int64_t len, uint16_t* m_out, uint16_t* v_out, hipStream_t stream) {
+  if (len < 0 || len > kMaxMoments || len % 32 != 0) return MOE_ERR_BAD_SHAPE;
+  if (missing(m, len) || missing(m_scales, len) || missing(v, len) || missing(v_scales, len) || missing(m_out, len) ||
+      missing(v_out, len))
+    return MOE_ERR_NULL_POINTER;
+  if (misaligned(m, 16) || misaligned(v, 16) || misaligned(m_out, 16) || misaligned(v_out, 16)) return MOE_ERR_MISALIGNED;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_adamw_moments(m, m_scales, v, v_scales, len, m_out, v_out, stream));
+}
+
+// ------------------------------------------------------------------ 4-bit weights with group scales
+
+moe_status moe_int4_quantize_weights(const uint16_t* w, int32_t w_layout, int64_t d_in, int64_t d_out, int32_t E,
+                                     int32_t group, uint8_t* q, uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
+  if (w_layout != MOE_W_IN_OUT && w_layout != MOE_W_OUT_IN) return MOE_ERR_BAD_SHAPE;
+  moe_status st = check_int4(0, d_in, d_out, E, group);
+  if (st != MOE_OK) return st;
+  if (w == nullptr) return MOE_ERR_NULL_POINTER;
+  if ((st = check_int4_weights(q, scales, zeros)) != MOE_OK) return st;
+  if (misaligned(w, 16)) return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_int4_quantize(w, w_layout == MOE_W_OUT_IN, d_in, d_out, E, group, q, scales, zeros, stream));
+}
+
+moe_status moe_int4_dequantize_weights(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t d_in,
+                                       int64_t d_out, int32_t E, int32_t group, uint16_t* w, hipStream_t stream) {
+  moe_status st = check_int4(0, d_in, d_out, E, group);
+  if (st != MOE_OK) return st;
+  if (w == nullptr) return MOE_ERR_NULL_POINTER;
+  if ((st = check_int4_weights(q, scales, zeros)) != MOE_OK) return st;
+  if (misaligned(w, 16)) return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return launched(launch_int4_dequantize(q, scales, zeros, d_in, d_out, E, group, w, stream));
+}
+
+moe_status moe_grouped_projection_int4(const uint16_t* x, const int32_t* offsets, const uint8_t* q,
+                                       const uint16_t* scales, const uint8_t* zeros, int32_t group, int64_t cap_rows,
+                                       int64_t d_in, int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream) {
+  moe_status st = check_int4(cap_rows, d_in, d_out, E, group);
+  if (st != MOE_OK) return st;
+  if (missing(x, cap_rows) || offsets == nullptr || missing(y, cap_rows)) return MOE_ERR_NULL_POINTER;
+  if ((st = check_int4_weights(q, scales, zeros)) != MOE_OK) return st;
+  if (misaligned(x, 16) || misaligned(y, 16) || misaligned(offsets, 4)) return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  if (cap_rows == 0) return MOE_OK;
+  (void)hipGetLastError();
+  return launched(launch_int4_product(x, nullptr, 1, cap_rows, offsets, q, scales, zeros, group, false, cap_rows, d_in,
+                                      d_out, E, y, stream));
+}
+
+moe_status moe_gemm_up_swiglu_int4(const uint16_t* x, const int32_t* perm, int64_t T, int32_t k, const int32_t* offsets,
+                                   const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int32_t group,
+                                   int64_t d, int64_t h, int32_t E, uint16_t* h_buf, hipStream_t stream) {
+  if (T < 0 || k < 1 || T > kMaxSlots / k || (perm == nullptr && k != 1 && T != 0)) return MOE_ERR_BAD_SHAPE;
+  moe_status st = check_int4(T * k, d, h, E, group);
+  if (st != MOE_OK) return st;
+  if (missing(x, T) || offsets == nullptr || missing(h_buf, T)) return MOE_ERR_NULL_POINTER;
+  if ((st = check_int4_weights(q, scales, zeros)) != MOE_OK) return st;
+  if (misaligned(x, 16) || misaligned(h_buf, 16) || misaligned(offsets, 4) || misaligned(perm, 4))
+    return MOE_ERR_MISALIGNED;
+  if ((st = check_device()) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  (void)hipGetLastError();
+  return launched(launch_int4_product(x, perm, k, T, offsets, q, scales, zeros, group, true, T * k, d, h, E, h_buf,
+                                      stream));
+}
+
 static_assert(sizeof(moe_status) == sizeof(int), "moe_status travels as a C int");
 
 const char* moe_status_string(moe_status s) {
@@ -516,6 +748,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE: workspace smaller than the call's *_workspace_bytes()";
     case MOE_ERR_UNSUPPORTED_DEVICE: return "MOE_ERR_UNSUPPORTED_DEVICE: the current HIP device is not gfx950";
     case MOE_ERR_LAUNCH: return "MOE_ERR_LAUNCH: a kernel launch reported a HIP error";
+    case MOE_ERR_BAD_VALUE: return "MOE_ERR_BAD_VALUE: a scalar that is no size is out of range (eps, a scale, a setting of AdamW)";
     case MOE_ERR_TOO_LARGE: return "MOE_ERR_TOO_LARGE: the call needs more than the fixed table of moe_permute_noalloc (E * ceil(T*k/256) > 2^20)";
   }
   return "unknown moe_status";

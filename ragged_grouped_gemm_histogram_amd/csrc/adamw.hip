@@ -1,0 +1,365 @@
+// One AdamW step over a list of tensors, one launch per kListed tensors. For a value p with gradient g:
+//
+//   m = b1 m + (1 - b1) g      v = b2 v + (1 - b2) g^2
+//   p = (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// all in fp32 (gradients are read as they are, parameters from their fp32 copy where there is one). Bound
+// by HBM: 28 bytes a value with bf16 parameters, fp32 copies and moments, 10 with 8-bit moments alone.
+//
+// Moments in 8 bits: 32 consecutive values share a power of two 2^(byte - 127). The first moment is
+// float8 e4m3, the block's largest magnitude in [128, 256) so that nothing saturates, to nearest even. The
+// second needs range and no sign: code c stands for (1 + (c % 8) / 8) 2^(c / 8), 0 for c = 0, the largest
+// with c / 8 = 30; anything above zero keeps at least code 1, so that a small second moment never
+// vanishes under its first. Both scale by powers of two alone and the moments are taken in separate,
+// unfused operations, so that the codes are determined to the bit. With (1 - b2) far below a code's step
+// rounding to nearest would hold v where it is: a seed makes its rounding random, with a mean of v.
+// The step itself uses m and v before they are rounded. A block with an infinity or a NaN gets byte 255
+// and reads as NaN.
+
+#include <cmath>
+
+#include "common.h"
+
+// Sums and products of the moments are rounded one by one.
+#pragma clang fp contract(off)
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kListed = 80;  // tensors per launch: their table travels in the kernel's arguments (4 KB)
+constexpr int kPer = 8;      // consecutive values of a thread
+constexpr int kChunk = kThreads * kPer * 2;  // values of a workgroup's step, within one tensor
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+struct Listed {
+  void* param;
+  const void* grad;
+  int64_t n;
+  int64_t at;       // first value's place in the moments
+  int32_t flags;
+  int32_t pad;
+};
+constexpr int kParamF32 = 1, kGradF32 = 2, kParamAligned = 4, kGradAligned = 8;
+
+struct AdamArgs {
+  void* m;
+  uint8_t* m_scales;
+  void* v;
+  uint8_t* v_scales;
+  float* master;
+  const float* lr_ptr;
+  const int32_t* step_ptr;
+  const float* grad_scale;
+  double lr, decay, log_b1, log_b2;  // for a step or a rate that is on the device
+  float b1, not_b1, b2, not_b2, eps;
+  float keep, rate, root;            // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t seed, step;
+  int32_t random;
+  int32_t count;
+  uint32_t first[kListed];           // first chunk of each tensor
+  uint32_t chunks;
+  Listed t[kListed];
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
+
+__host__ __device__ inline uint32_t mix32(uint32_t h) {
+  h = (h ^ (h >> 16)) * 0x6A09E667u;  // odd fractions of the square roots of 2 and 3
+  h = (h ^ (h >> 15)) * 0xBB67AE85u;
+  return h ^ (h >> 16);
+}
+
+__device__ __forceinline__ float bits_f32(uint32_t b) { return __builtin_bit_cast(float, b); }
+__device__ __forceinline__ uint32_t f32_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
+
+// Eight values of a tensor from place i on; zeros behind its end.
+__device__ __forceinline__ void load_values(const void* base, bool f32, bool aligned, int64_t i, int64_t n,
+                                            float (&x)[kPer]) {
+  if (aligned && i + kPer <= n) {
+    if (f32) {
+      const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + i);
+      const f32x4_t a = p[0], b = p[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+    } else {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[2 * j] = bits_f32(a[j] << 16), x[2 * j + 1] = bits_f32(a[j] & 0xFFFF0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    x[j] = 0.0f;
+    if (i + j < n)
+      x[j] = f32 ? static_cast<const float*>(base)[i + j]
+                 : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[i + j]);
+  }
+}
+
+// bf16 of p with the dropped half added to a random 16 bits: rounds up with the probability of what it drops.
+__device__ __forceinline__ uint32_t random_bf16(float p, uint32_t r) {
+  const uint32_t b = f32_bits(p);
+  const bool finite = (b & 0x7F800000u) != 0x7F800000u;
+  return finite ? (b + (r & 0xFFFFu)) >> 16 : (uint32_t)f32_to_bf16_bits(p);
+}
+
+__device__ __forceinline__ void store_values(void* base, bool f32, bool aligned, int64_t i, int64_t n,
+                                             const float (&x)[kPer], bool random, const uint32_t (&r)[kPer]) {
+  if (f32) {
+    float* p = static_cast<float*>(base) + i;
+    if (aligned && i + kPer <= n) {
+      reinterpret_cast<f32x4_t*>(p)[0] = f32x4_t{x[0], x[1], x[2], x[3]};
+      reinterpret_cast<f32x4_t*>(p)[1] = f32x4_t{x[4], x[5], x[6], x[7]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (i + j < n) p[j] = x[j];
+    }
+    return;
+  }
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = random ? random_bf16(x[2 * j], r[2 * j]) | random_bf16(x[2 * j + 1], r[2 * j + 1]) << 16
+                  : pack_bf16x2(x[2 * j], x[2 * j + 1]);
+  uint16_t* p = static_cast<uint16_t*>(base) + i;
+  if (aligned && i + kPer <= n) {
+    *reinterpret_cast<u32x4*>(p) = o;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (i + j < n) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+  const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
+  return x > y ? x : y;
+}
+
+// The largest magnitude of a block, as bits (a NaN's above all), in each of the four lanes that hold it.
+__device__ __forceinline__ uint32_t block_max(const float (&x)[kPer]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t b = f32_bits(x[j]) & 0x7FFFFFFFu;
+    top = b > top ? b : top;
+  }
+  return dpp_max<0x4E>(dpp_max<0xB1>(top));
+}
+
+// The scale byte for a block's largest magnitude, `up` powers of two below it, at least 1.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top, uint32_t up) {
+  const uint32_t field = top >> 23;
+  return field == 255 ? 255u : (field > up ? field - up : 1u);
+}
+
+__device__ __forceinline__ void decode_m(u32x2_t q, uint32_t s, float (&x)[kPer]) {
+  const float scale = bits_f32(s << 23);  // byte 255: an infinity, which makes NaN of the zero codes
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[h], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[h], true);
+    x[4 * h] = lo[0] * scale, x[4 * h + 1] = lo[1] * scale, x[4 * h + 2] = hi[0] * scale, x[4 * h + 3] = hi[1] * scale;
+  }
+}
+
+__device__ __forceinline__ uint32_t encode_m(const float (&x)[kPer], u32x2_t& q) {
+  const uint32_t s = scale_byte(block_max(x), 7);
+  const float inverse = bits_f32((254u - (s == 255 ? 254u : s)) << 23);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h] * inverse, x[4 * h + 1] * inverse, 0, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2] * inverse, x[4 * h + 3] * inverse, c, true);
+    q[h] = s == 255 ? 0u : (uint32_t)c;
+  }
+  return s;
+}
+
+__device__ __forceinline__ void decode_v(u32x2_t q, uint32_t s, float (&x)[kPer]) {
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t c = (q[j >> 2] >> (8 * (j & 3))) & 0xFFu;
+    const uint32_t b = (c << 20) + (s << 23);
+    x[j] = bits_f32(s == 255 ? 0x7FC00000u : (c == 0 ? 0u : b));
+  }
+}
+
+__device__ __forceinline__ uint32_t encode_v(const float (&x)[kPer], bool random, const uint32_t (&r)[kPer],
+                                             u32x2_t& q) {
+  const uint32_t s = scale_byte(block_max(x), 30);
+  q = u32x2_t{0u, 0u};
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t b = f32_bits(x[j]);
+    int32_t c = (int32_t)(b - (s << 23));
+    c = (c + (int32_t)(random ? (r[j] >> 16) << 4 : 0x7FFFFu + ((b >> 20) & 1u))) >> 20;
+    c = c < 1 ? 1 : c;
+    c = b == 0 || s == 255 ? 0 : c;
+    q[j >> 2] |= (uint32_t)c << (8 * (j & 3));
+  }
+  return s;
+}
+
+// A chunk is two passes of 8 consecutive values a thread; a tensor's moments begin at a multiple of 32, so a
+// block of 32 lies in four neighbouring lanes.
+template <bool Q8, bool MASTER>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
+  const int lane = threadIdx.x & 63;
+  float keep = g.keep, rate = g.rate, root = g.root, gs = 1.0f;
+  uint32_t step = g.step;
+  if (g.lr_ptr != nullptr || g.step_ptr != nullptr) {
+    const double lr = g.lr_ptr != nullptr ? (double)*g.lr_ptr : g.lr;
+    const int32_t t = g.step_ptr != nullptr ? *g.step_ptr : (int32_t)g.step;
+    step = (uint32_t)(t < 1 ? 1 : t);
+    keep = (float)(1.0 - lr * g.decay);
+    rate = (float)(lr / -expm1(step * g.log_b1));
+    root = (float)(1.0 / sqrt(-expm1(step * g.log_b2)));
+  }
+  if (g.grad_scale != nullptr) gs = *g.grad_scale;
+  const uint32_t key = mix32(g.seed ^ mix32(step));
+  // first chunks of the tensors, for the search
+  const uint32_t first0 = lane < g.count ? g.first[lane] : ~0u;
+  const uint32_t first1 = 64 + lane < g.count ? g.first[lane + 64 < kListed ? lane + 64 : 0] : ~0u;
+  for (uint32_t chunk = blockIdx.x; chunk < g.chunks; chunk += gridDim.x) {
+    const int e = __builtin_amdgcn_readfirstlane(__popcll(__ballot(first0 <= chunk)) + __popcll(__ballot(first1 <= chunk))) - 1;
+    const Listed t = g.t[e];
+    const bool p_f32 = t.flags & kParamF32, g_f32 = t.flags & kGradF32;
+    const bool p_al = t.flags & kParamAligned, g_al = t.flags & kGradAligned;
+    const bool random_p = !MASTER && !p_f32 && g.random != 0;
+    const int64_t base = (int64_t)(chunk - g.first[e]) * kChunk + threadIdx.x * kPer;
+#pragma unroll
+    for (int pass = 0; pass < kChunk / (kThreads * kPer); ++pass) {
+      const int64_t i = base + pass * (kThreads * kPer);
+      const int64_t at = t.at + i;
+      // whole blocks: what lies behind the last value, up to a multiple of 32, is held at zero
+      if (i >= ((t.n + 31) & ~(int64_t)31)) continue;
+      float gr[kPer], p[kPer], m[kPer], v[kPer];
+      uint32_t r[kPer];
+      load_values(t.grad, g_f32, g_al, i, t.n, gr);
+      if constexpr (MASTER) load_values(g.master + t.at, true, true, i, (t.n + 31) & ~(int64_t)31, p);
+      else load_values(t.param, p_f32, p_al, i, t.n, p);
+      if constexpr (Q8) {
+        const u32x2_t mq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.m) + at);
+        const u32x2_t vq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.v) + at);
+        decode_m(mq, g.m_scales[at >> 5], m);
+        decode_v(vq, g.v_scales[at >> 5], v);
+      } else {
+        load_values(static_cast<const float*>(g.m), true, true, at, at + kPer, m);
+        load_values(static_cast<const float*>(g.v), true, true, at, at + kPer, v);
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float x = gr[j] * gs;
+        m[j] = m[j] * g.b1 + x * g.not_b1;
+        v[j] = v[j] * g.b2 + (x * x) * g.not_b2;
+        p[j] = p[j] * keep - m[j] / (sqrtf(v[j]) * root + g.eps) * rate;
+        if (i + j >= t.n) m[j] = v[j] = p[j] = 0.0f;
+        if (g.random != 0) {
+          const uint64_t place = (uint64_t)(at + j);
+          r[j] = mix32((uint32_t)place + (uint32_t)(place >> 32) * 0x9E3779B1u + key);
+        } else {
+          r[j] = 0;
+        }
+      }
+      store_values(t.param, p_f32, p_al, i, t.n, p, random_p, r);
+      if constexpr (MASTER) store_values(g.master, true, true, at, at + kPer, p, false, r);
+      if constexpr (Q8) {
+        u32x2_t mq, vq;
+        const uint32_t ms = encode_m(m, mq), vs = encode_v(v, g.random != 0, r, vq);
+        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.m) + at) = mq;
+        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.v) + at) = vq;
+        if ((threadIdx.x & 3) == 0) {
+          g.m_scales[at >> 5] = (uint8_t)ms;
+          g.v_scales[at >> 5] = (uint8_t)vs;
+        }
+      } else {
+        store_values(g.m, true, true, at, at + kPer, m, false, r);
+        store_values(g.v, true, true, at, at + kPer, v, false, r);
+      }
+    }
+  }
+}
+
+// The values of 8-bit moments as bf16 (exact: three bits of mantissa), 8 a thread.
+__global__ __launch_bounds__(kThreads) void moments_kernel(const uint8_t* __restrict__ m, const uint8_t* __restrict__ ms,
+                                                           const uint8_t* __restrict__ v, const uint8_t* __restrict__ vs,
+                                                           int64_t n, uint16_t* __restrict__ m_out,
+                                                           uint16_t* __restrict__ v_out) {
+  const int64_t step = (int64_t)gridDim.x * kThreads * kPer;
+  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPer; i < n; i += step) {
+    float x[kPer];
+    u32x4 o;
+    decode_m(*reinterpret_cast<const u32x2_t*>(m + i), ms[i >> 5], x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<u32x4*>(m_out + i) = o;
+    decode_v(*reinterpret_cast<const u32x2_t*>(v + i), vs[i >> 5], x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<u32x4*>(v_out + i) = o;
+  }
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, void* m, uint8_t* m_scales, void* v,
+                        uint8_t* v_scales, float* master, const moe_adamw_hyper& h, const float* lr_ptr,
+                        const int32_t* step_ptr, const float* grad_scale, hipStream_t stream) {
+  AdamArgs g;
+  g.m = m, g.m_scales = m_scales, g.v = v, g.v_scales = v_scales, g.master = master;
+  g.lr_ptr = lr_ptr, g.step_ptr = step_ptr, g.grad_scale = grad_scale;
+  g.lr = h.lr, g.decay = h.weight_decay, g.log_b1 = std::log(h.beta1), g.log_b2 = std::log(h.beta2);
+  g.b1 = (float)h.beta1, g.not_b1 = (float)(1.0 - h.beta1), g.b2 = (float)h.beta2, g.not_b2 = (float)(1.0 - h.beta2);
+  g.eps = (float)h.eps;
+  g.keep = (float)(1.0 - h.lr * h.weight_decay);
+  g.rate = (float)(h.lr / -std::expm1(h.step * g.log_b1));
+  g.root = (float)(1.0 / std::sqrt(-std::expm1(h.step * g.log_b2)));
+  g.seed = h.seed, g.step = (uint32_t)h.step, g.random = h.stochastic != 0;
+  const int64_t most = (int64_t)device_cu_count(current_device()) * 8;
+  int32_t i = 0;
+  while (i < count) {
+    // as many tensors as the table holds and whose chunks a launch can count
+    int64_t chunks = 0;
+    g.count = 0;
+    for (; i < count && g.count < kListed; ++i) {
+      const int64_t n = (list[i].n + kChunk - 1) / kChunk;
+      if (n == 0) continue;
+      if (chunks + n > INT32_MAX) break;
+      Listed& t = g.t[g.count];
+      t.param = list[i].param, t.grad = list[i].grad, t.n = list[i].n, t.at = list[i].offset, t.pad = 0;
+      t.flags = (list[i].param_dtype == MOE_F32 ? kParamF32 : 0) | (list[i].grad_dtype == MOE_F32 ? kGradF32 : 0) |
+                (aligned16(t.param) ? kParamAligned : 0) | (aligned16(t.grad) ? kGradAligned : 0);
+      g.first[g.count++] = (uint32_t)chunks;
+      chunks += n;
+    }
+    if (g.count == 0) break;
+    g.chunks = (uint32_t)chunks;
+    const dim3 grid((unsigned)(chunks < most ? chunks : most)), block(kThreads);
+    if (q8 && master != nullptr) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, stream, g);
+    else if (q8) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, stream, g);
+    else if (master != nullptr) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, stream, g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_adamw_moments(const uint8_t* m, const uint8_t* ms, const uint8_t* v, const uint8_t* vs, int64_t n,
+                                uint16_t* m_out, uint16_t* v_out, hipStream_t stream) {
+  if (n == 0) return hipSuccess;
+  int64_t blocks = (n / kPer + kThreads - 1) / kThreads;
+  const int64_t most = (int64_t)device_cu_count(current_device()) * 16;
+  hipLaunchKernelGGL(moments_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, stream, m, ms, v,
+                     vs, n, m_out, v_out);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -121,4 +121,31 @@ hipError_t launch_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_s, i
                                        int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf, uint8_t* h_q,
                                        uint8_t* h_s, hipStream_t stream);  // to h_buf, or without one to h_q and h_s
 
+// Norms around a block. The backward leaves norm_partial_rows(T, d) rows of up to three partial column sums.
+int64_t norm_partial_rows(int64_t T, int64_t d);
+hipError_t launch_norm(const void* r, bool r_f32, const uint16_t* y, const void* w_post, const void* w_next,
+                       const void* gate, int gate_kind, bool w_f32, bool post, bool next, float a, float b, float eps,
+                       int64_t T, int64_t d, void* r_out, uint16_t* n_out, hipStream_t stream);  // without y: before
+hipError_t launch_norm_backward(const void* dr, const uint16_t* dn, const uint16_t* dn_add, const uint16_t* y, const void* r,
+                                bool r_f32, const void* w_post, const void* w_next, const void* gate, int gate_kind,
+                                bool w_f32, bool branch, bool post, bool next, float a, float b, float eps, int64_t T, int64_t d,
+                                void* dr_out, uint16_t* dy, float* d_gate, float* d_w_post, float* d_w_next,
+                                float* partial, hipStream_t stream);
+
+// AdamW.
+hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, void* m, uint8_t* m_scales, void* v,
+                        uint8_t* v_scales, float* master, const moe_adamw_hyper& h, const float* lr_ptr,
+                        const int32_t* step_ptr, const float* grad_scale, hipStream_t stream);
+hipError_t launch_adamw_moments(const uint8_t* m, const uint8_t* ms, const uint8_t* v, const uint8_t* vs, int64_t n,
+                                uint16_t* m_out, uint16_t* v_out, hipStream_t stream);
+
+// 4-bit weights with group scales.
+hipError_t launch_int4_quantize(const uint16_t* w, bool w_out_in, int64_t d_in, int64_t d_out, int32_t E, int32_t group,
+                                uint8_t* q, uint16_t* scales, uint8_t* zeros, hipStream_t stream);
+hipError_t launch_int4_dequantize(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t d_in,
+                                  int64_t d_out, int32_t E, int32_t group, uint16_t* w, hipStream_t stream);
+hipError_t launch_int4_product(const uint16_t* x, const int32_t* perm, int32_t k, int64_t tokens, const int32_t* offsets,
+                               const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int32_t group, bool gated,
+                               int64_t cap_rows, int64_t K, int64_t N, int32_t E, uint16_t* out, hipStream_t stream);
+
 }  // namespace moe
