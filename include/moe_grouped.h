@@ -585,8 +585,6 @@ moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, 
  * seed, step and place (offset + index), so a step repeats bit for bit.
  * ------------------------------------------------------------------------- */
 typedef struct moe_adamw_tensor {
-  void* param;         /* aligned to its element size (16 bytes: whole vectors) */
-  const void* grad;    /* the same */
   int64_t n;           /* values, 0 allowed */
   int64_t offset;      /* place of the first value's moments; ascending, not overlapping */
   int32_t param_dtype; /* moe_dtype */
@@ -600,9 +598,11 @@ typedef struct moe_adamw_hyper {
   int32_t stochastic;
 } moe_adamw_hyper;
 
-/* One step, a launch per 80 tensors. `tensors` and `hyper` are HOST memory and are
- * free again when the call returns.
+/* One step, a launch per 80 tensors. `tensors`, `params`, `grads` (the two arrays,
+ * count long) and `hyper` are HOST memory and are free again when the call returns.
  *
+ *   params, grads  each tensor's values, aligned to their element size (16 bytes
+ *                  let whole vectors be read)
  *   len            values the moments' buffers hold, a multiple of 32
  *   master         fp32 [len] or NULL
  *   lr_ptr         fp32 [1] on the device: the rate instead of hyper->lr; or NULL
@@ -610,9 +610,9 @@ typedef struct moe_adamw_hyper {
  *   grad_scale     fp32 [1] on the device, multiplied to every gradient; or NULL
  *
  * The three let a captured step follow what changes from replay to replay. */
-moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t bits, int64_t len, void* m,
-                          uint8_t* m_scales, void* v, uint8_t* v_scales, float* master, const moe_adamw_hyper* hyper,
-                          const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream);
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, void* const* params, const void* const* grads, int32_t count,
+                          int32_t bits, int64_t len, void* m, uint8_t* m_scales, void* v, uint8_t* v_scales,
+                          float* master, const moe_adamw_hyper* hyper, const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream);
 
 /* The values of 8-bit moments as bf16 [len] (exact unless below bf16's range), one launch. */
 moe_status moe_adamw_moments(const uint8_t* m, const uint8_t* m_scales, const uint8_t* v, const uint8_t* v_scales,

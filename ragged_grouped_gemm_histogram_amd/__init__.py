@@ -68,7 +68,7 @@ _SIGNATURES = {
                                             _vp]),
     "moe_residual_norm_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _f32, _f32,
                                                   _f32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
-    "moe_adamw_step": (ctypes.c_int, [_vp, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_adamw_step": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_adamw_moments": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
     "moe_int4_quantize_weights": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
     "moe_int4_dequantize_weights": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp]),
@@ -1113,7 +1113,7 @@ def moe_layer_backward(d_r_out: torch.Tensor | None, f: MoeLayer, w_norm, w_rout
 
 
 class _AdamTensor(ctypes.Structure):
-    _fields_ = [("param", _vp), ("grad", _vp), ("n", _i64), ("offset", _i64), ("param_dtype", _i32), ("grad_dtype", _i32)]
+    _fields_ = [("n", _i64), ("offset", _i64), ("param_dtype", _i32), ("grad_dtype", _i32)]
 
 
 class _AdamHyper(ctypes.Structure):
@@ -1177,12 +1177,45 @@ class AdamW:
                 _want(m.scales, f"{name}.scales", torch.uint8, (self.len // 32,), dev)
         if self.master is not None:
             _want(self.master, "master", torch.float32, (self.len,), dev)
-        self._table = (_AdamTensor * len(self.params))()
-        self._hyper = _AdamHyper()
-        self._specs = []
-        for t, p, at in zip(self._table, self.params, self.places):
-            t.n, t.offset, t.param_dtype = p.numel(), at, _LOGITS[p.dtype]
-            self._specs.append((p.dtype, p.shape))
+        count = len(self.params)
+        self._device = dev
+        self._table, self._hyper = (_AdamTensor * count)(), _AdamHyper()
+        self._param_ptrs, self._grad_ptrs = (ctypes.c_uint64 * count)(), (ctypes.c_uint64 * count)()
+        self._dtypes, self._shapes = [p.dtype for p in self.params], [p.shape for p in self.params]
+        self._sizes, self._addresses = [p.numel() for p in self.params], [p.data_ptr() for p in self.params]
+        self._param_ptrs[:] = self._addresses
+        self._grad_dtypes = None
+        for t, n, at, dtype in zip(self._table, self._sizes, self.places, self._dtypes):
+            t.n, t.offset, t.param_dtype = n, at, _LOGITS[dtype]
+
+    def _take_params(self):
+        """Parameters' addresses, checked again where one has moved."""
+        addresses = [p.data_ptr() for p in self.params]
+        if addresses != self._addresses or [p.numel() for p in self.params] != self._sizes:
+            for i, (p, dtype, shape) in enumerate(zip(self.params, self._dtypes, self._shapes)):
+                _want(p, f"params[{i}]", dtype, tuple(shape), self._device)
+            self._param_ptrs[:] = self._addresses = addresses
+
+    def _take_grads(self, grads):
+        if len(grads) != len(self._sizes):
+            raise ValueError(f"{len(self._sizes)} parameters but {len(grads)} gradients")
+        for i, g in enumerate(grads):
+            if not isinstance(g, _Tensor):
+                raise TypeError(f"grads[{i}] must be a torch.Tensor")
+        dtypes = [g.dtype for g in grads]
+        if dtypes != self._grad_dtypes:
+            for i, dtype in enumerate(dtypes):
+                if dtype not in _LOGITS:
+                    raise TypeError(f"grads[{i}] must be bfloat16 or float32, got {dtype}")
+            for t, dtype in zip(self._table, dtypes):
+                t.grad_dtype = _LOGITS[dtype]
+            self._grad_dtypes = dtypes
+        index = self._device.index
+        if ([g.shape for g in grads] != self._shapes or [g.get_device() for g in grads] != [index] * len(grads)
+                or False in [g.is_contiguous() for g in grads]):
+            for i, (g, shape) in enumerate(zip(grads, self._shapes)):  # (names the one that does not fit)
+                _want(g, f"grads[{i}]", g.dtype, tuple(shape), self._device)
+        self._grad_ptrs[:] = [g.data_ptr() for g in grads]
 
 
 def moe_adamw_state(params, *, bits: int = 32, master: bool = False) -> AdamW:
@@ -1220,21 +1253,9 @@ def moe_adamw_step(state: AdamW, grads, *, lr, betas=(0.9, 0.999), eps: float = 
     number or a fp32 [1] tensor on the device, ``step`` an int or an int32 [1] tensor, for steps captured in a graph;
     ``grad_scale`` fp32 [1] is multiplied to the gradients (a clipping factor). A ``seed`` rounds the second moment in 8
     bits, and bf16 parameters without a master, at random in proportion; without one they round to nearest."""
-    params, table, h = state.params, state._table, state._hyper
-    if len(grads) != len(params):
-        raise ValueError(f"{len(params)} parameters but {len(grads)} gradients")
-    dev = params[0].device
-    index = dev.index
-    # (the common case of a tensor that fits, in one expression; _want names what does not)
-    for t, p, g, (dtype, shape) in zip(table, params, grads, state._specs):
-        if not (p.dtype is dtype and p.shape == shape and p.get_device() == index and p.is_contiguous()):
-            _want(p, "a parameter", dtype, tuple(shape), dev)
-        code = _LOGITS.get(g.dtype) if isinstance(g, _Tensor) else None
-        if code is None:
-            raise TypeError("gradients must be bfloat16 or float32 tensors")
-        if not (g.shape == shape and g.get_device() == index and g.is_contiguous()):
-            _want(g, "a gradient", g.dtype, tuple(shape), dev)
-        t.param, t.grad, t.grad_dtype = p.data_ptr(), g.data_ptr(), code
+    state._take_params()
+    state._take_grads(grads)
+    dev, h = state._device, state._hyper
     lr_ptr = step_ptr = None
     if isinstance(lr, _Tensor):
         lr_ptr, lr = _device_scalar(lr, "lr", torch.float32, dev), 0.0
@@ -1251,9 +1272,10 @@ def moe_adamw_step(state: AdamW, grads, *, lr, betas=(0.9, 0.999), eps: float = 
     else:
         m, ms = state.exp_avg.q.data_ptr(), state.exp_avg.scales.data_ptr()
         v, vs = state.exp_avg_sq.q.data_ptr(), state.exp_avg_sq.scales.data_ptr()
-    _check(load_library().moe_adamw_step(ctypes.addressof(table), len(params), state.bits, state.len, m, ms, v, vs,
-                                         _ptr(state.master), ctypes.addressof(h), lr_ptr, step_ptr, grad_scale,
-                                         _stream(params[0])), "moe_adamw_step")
+    _check(load_library().moe_adamw_step(ctypes.addressof(state._table), ctypes.addressof(state._param_ptrs),
+                                         ctypes.addressof(state._grad_ptrs), len(state._sizes), state.bits, state.len, m,
+                                         ms, v, vs, _ptr(state.master), ctypes.addressof(h), lr_ptr, step_ptr, grad_scale,
+                                         _stream(state.params[0])), "moe_adamw_step")
 
 
 def moe_adamw_moments(state: AdamW, *, exp_avg=None, exp_avg_sq=None):

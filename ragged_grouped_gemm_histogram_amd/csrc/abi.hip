@@ -628,11 +628,11 @@ moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, 
 
 // ------------------------------------------------------------------ AdamW
 
-moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t bits, int64_t len, void* m,
-                          uint8_t* m_scales, void* v, uint8_t* v_scales, float* master, const moe_adamw_hyper* hyper,
-                          const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream) {
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, void* const* params, const void* const* grads, int32_t count,
+                          int32_t bits, int64_t len, void* m, uint8_t* m_scales, void* v, uint8_t* v_scales,
+                          float* master, const moe_adamw_hyper* hyper, const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream) {
   if (count < 0 || len < 0 || len > kMaxMoments || len % 32 != 0 || (bits != 8 && bits != 32)) return MOE_ERR_BAD_SHAPE;
-  if (hyper == nullptr || missing(tensors, count) || missing(m, len) || missing(v, len) ||
+  if (hyper == nullptr || missing(tensors, count) || missing(params, count) || missing(grads, count) || missing(m, len) || missing(v, len) ||
       (bits == 8 && (missing(m_scales, len) || missing(v_scales, len))))
     return MOE_ERR_NULL_POINTER;
   if (misaligned(m, 16) || misaligned(v, 16) || misaligned(master, 16) || misaligned(lr_ptr, 4) ||
@@ -649,15 +649,15 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_
     if (bad_dtype(t.param_dtype) || bad_dtype(t.grad_dtype) || t.n < 0 || t.offset < free_from || t.offset % 32 != 0 ||
         t.offset > len || t.n > len - t.offset)
       return MOE_ERR_BAD_SHAPE;
-    if (missing(t.param, t.n) || missing(t.grad, t.n)) return MOE_ERR_NULL_POINTER;
-    if (misaligned(t.param, logit_bytes(t.param_dtype)) || misaligned(t.grad, logit_bytes(t.grad_dtype)))
+    if (missing(params[i], t.n) || missing(grads[i], t.n)) return MOE_ERR_NULL_POINTER;
+    if (misaligned(params[i], logit_bytes(t.param_dtype)) || misaligned(grads[i], logit_bytes(t.grad_dtype)))
       return MOE_ERR_MISALIGNED;
     free_from = t.offset + (t.n + 31) / 32 * 32;
   }
   const moe_status st = check_device();
   if (st != MOE_OK) return st;
   (void)hipGetLastError();
-  return launched(launch_adamw(tensors, count, bits == 8, m, m_scales, v, v_scales, master, h, lr_ptr, step_ptr,
+  return launched(launch_adamw(tensors, params, grads, count, bits == 8, m, m_scales, v, v_scales, master, h, lr_ptr, step_ptr,
                                grad_scale, stream));
 }
 

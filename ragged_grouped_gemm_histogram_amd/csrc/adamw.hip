@@ -42,6 +42,7 @@ struct Listed {
   int32_t flags;
   int32_t pad;
 };
+constexpr double kLeastEps = 1e-12;  // see adamw_kernel
 constexpr int kParamF32 = 1, kGradF32 = 2, kParamAligned = 4, kGradAligned = 8;
 
 struct AdamArgs {
@@ -57,7 +58,6 @@ struct AdamArgs {
   float b1, not_b1, b2, not_b2, eps;
   float keep, rate, root;            // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   uint32_t seed, step;
-  int32_t random;
   int32_t count;
   uint32_t first[kListed];           // first chunk of each tensor
   uint32_t chunks;
@@ -74,10 +74,11 @@ __host__ __device__ inline uint32_t mix32(uint32_t h) {
 __device__ __forceinline__ float bits_f32(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t f32_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
-// Eight values of a tensor from place i on; zeros behind its end.
-__device__ __forceinline__ void load_values(const void* base, bool f32, bool aligned, int64_t i, int64_t n,
+// Eight values of a tensor from place i on; where not all of the chunk's are there, or not aligned, one by one,
+// with zeros behind the end.
+__device__ __forceinline__ void load_values(const void* base, bool f32, bool whole, int64_t i, int64_t n,
                                             float (&x)[kPer]) {
-  if (aligned && i + kPer <= n) {
+  if (whole) {
     if (f32) {
       const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + i);
       const f32x4_t a = p[0], b = p[1];
@@ -99,20 +100,52 @@ __device__ __forceinline__ void load_values(const void* base, bool f32, bool ali
   }
 }
 
-// bf16 of p with the dropped half added to a random 16 bits: rounds up with the probability of what it drops.
-__device__ __forceinline__ uint32_t random_bf16(float p, uint32_t r) {
-  const uint32_t b = f32_bits(p);
-  const bool finite = (b & 0x7F800000u) != 0x7F800000u;
-  return finite ? (b + (r & 0xFFFFu)) >> 16 : (uint32_t)f32_to_bf16_bits(p);
+__device__ __forceinline__ void load_state(const float* p, float (&x)[kPer]) { load_values(p, true, true, 0, kPer, x); }
+
+__device__ __forceinline__ void store_state(float* p, const float (&x)[kPer]) {
+  reinterpret_cast<f32x4_t*>(p)[0] = f32x4_t{x[0], x[1], x[2], x[3]};
+  reinterpret_cast<f32x4_t*>(p)[1] = f32x4_t{x[4], x[5], x[6], x[7]};
 }
 
-__device__ __forceinline__ void store_values(void* base, bool f32, bool aligned, int64_t i, int64_t n,
-                                             const float (&x)[kPer], bool random, const uint32_t (&r)[kPer]) {
+// The largest magnitude of eight values; a NaN if one is.
+__device__ __forceinline__ float largest(const float (&x)[kPer]) {
+  float top = __builtin_fabsf(x[0]);
+#pragma unroll
+  for (int j = 1; j < kPer; ++j) top = __builtin_elementwise_maximum(top, __builtin_fabsf(x[j]));
+  return top;
+}
+
+// bf16 of eight values, each with its dropped half added to 16 random bits: it rounds up with the probability of
+// what it drops. What is not finite rounds as usual.
+__device__ __forceinline__ u32x4 random_bf16(const float (&x)[kPer], const uint32_t (&r)[kPer]) {
+  u32x4 o;
+  if (largest(x) < __builtin_inff()) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = __builtin_amdgcn_perm(f32_bits(x[2 * j + 1]) + (r[2 * j + 1] & 0xFFFFu),
+                                   f32_bits(x[2 * j]) + (r[2 * j] & 0xFFFFu), 0x07060302u);
+    return o;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float v = x[2 * j + k];
+      h[k] = __builtin_fabsf(v) < __builtin_inff() ? (f32_bits(v) + (r[2 * j + k] & 0xFFFFu)) >> 16 : f32_to_bf16_bits(v);
+    }
+    o[j] = h[0] | h[1] << 16;
+  }
+  return o;
+}
+
+template <bool RANDOM>
+__device__ __forceinline__ void store_values(void* base, bool f32, bool whole, int64_t i, int64_t n,
+                                             const float (&x)[kPer], const uint32_t (&r)[kPer]) {
   if (f32) {
     float* p = static_cast<float*>(base) + i;
-    if (aligned && i + kPer <= n) {
-      reinterpret_cast<f32x4_t*>(p)[0] = f32x4_t{x[0], x[1], x[2], x[3]};
-      reinterpret_cast<f32x4_t*>(p)[1] = f32x4_t{x[4], x[5], x[6], x[7]};
+    if (whole) {
+      store_state(p, x);
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
@@ -121,12 +154,14 @@ __device__ __forceinline__ void store_values(void* base, bool f32, bool aligned,
     return;
   }
   u32x4 o;
+  if constexpr (RANDOM) {
+    o = random_bf16(x, r);
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    o[j] = random ? random_bf16(x[2 * j], r[2 * j]) | random_bf16(x[2 * j + 1], r[2 * j + 1]) << 16
-                  : pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+  }
   uint16_t* p = static_cast<uint16_t*>(base) + i;
-  if (aligned && i + kPer <= n) {
+  if (whole) {
     *reinterpret_cast<u32x4*>(p) = o;
   } else {
 #pragma unroll
@@ -143,13 +178,7 @@ __device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
 
 // The largest magnitude of a block, as bits (a NaN's above all), in each of the four lanes that hold it.
 __device__ __forceinline__ uint32_t block_max(const float (&x)[kPer]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint32_t b = f32_bits(x[j]) & 0x7FFFFFFFu;
-    top = b > top ? b : top;
-  }
-  return dpp_max<0x4E>(dpp_max<0xB1>(top));
+  return dpp_max<0x4E>(dpp_max<0xB1>(f32_bits(largest(x)) & 0x7FFFFFFFu));
 }
 
 // The scale byte for a block's largest magnitude, `up` powers of two below it, at least 1.
@@ -181,33 +210,41 @@ __device__ __forceinline__ uint32_t encode_m(const float (&x)[kPer], u32x2_t& q)
 }
 
 __device__ __forceinline__ void decode_v(u32x2_t q, uint32_t s, float (&x)[kPer]) {
+  const uint32_t scale = s << 23, nothing = s == 255 ? 0x7FC00000u : 0u;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const uint32_t c = (q[j >> 2] >> (8 * (j & 3))) & 0xFFu;
-    const uint32_t b = (c << 20) + (s << 23);
-    x[j] = bits_f32(s == 255 ? 0x7FC00000u : (c == 0 ? 0u : b));
+    x[j] = bits_f32(c == 0 ? nothing : (c << 20) + scale);  // (a block of byte 255 has zero codes)
   }
 }
 
-__device__ __forceinline__ uint32_t encode_v(const float (&x)[kPer], bool random, const uint32_t (&r)[kPer],
-                                             u32x2_t& q) {
+template <bool RANDOM>
+__device__ __forceinline__ uint32_t encode_v(const float (&x)[kPer], const uint32_t (&r)[kPer], u32x2_t& q) {
   const uint32_t s = scale_byte(block_max(x), 30);
   q = u32x2_t{0u, 0u};
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const uint32_t b = f32_bits(x[j]);
-    int32_t c = (int32_t)(b - (s << 23));
-    c = (c + (int32_t)(random ? (r[j] >> 16) << 4 : 0x7FFFFu + ((b >> 20) & 1u))) >> 20;
-    c = c < 1 ? 1 : c;
-    c = b == 0 || s == 255 ? 0 : c;
+    const int32_t b = (int32_t)f32_bits(x[j]);
+    int32_t c = b - (int32_t)(s << 23);
+    if constexpr (RANDOM) c += (int32_t)((r[j] >> 16) << 4);
+    else c += 0x7FFFF + ((b >> 20) & 1);
+    c >>= 20;
+    // the middle one of c, 1 and b: at least 1, and 0 for b = 0, whose c is negative
+    c = max(min(c, max(1, b)), min(1, b));
     q[j >> 2] |= (uint32_t)c << (8 * (j & 3));
   }
+  if (s == 255) q = u32x2_t{0u, 0u};
   return s;
 }
 
 // A chunk is two passes of 8 consecutive values a thread; a tensor's moments begin at a multiple of 32, so a
-// block of 32 lies in four neighbouring lanes.
-template <bool Q8, bool MASTER>
+// block of 32 lies in four neighbouring lanes. PRECISE: root and quotient as the compiler's own; otherwise the
+// instructions themselves, each within an ulp but a second moment below 2^-126 counts as 0, which an eps from
+// kLeastEps on hides (2^-63 / sqrt(1 - b2^t) of it).
+//
+// At 28 bytes a value (bf16, fp32 copy and moments, 398 M values) 2.26 ms, 4.93 TB/s. With 8-bit moments and
+// random rounding, 10.06 bytes, the arithmetic is as long as the traffic: see the figures at launch_adamw.
+template <bool Q8, bool MASTER, bool RANDOM, bool PRECISE>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
   const int lane = threadIdx.x & 63;
   float keep = g.keep, rate = g.rate, root = g.root, gs = 1.0f;
@@ -229,48 +266,52 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
     const int e = __builtin_amdgcn_readfirstlane(__popcll(__ballot(first0 <= chunk)) + __popcll(__ballot(first1 <= chunk))) - 1;
     const Listed t = g.t[e];
     const bool p_f32 = t.flags & kParamF32, g_f32 = t.flags & kGradF32;
-    const bool p_al = t.flags & kParamAligned, g_al = t.flags & kGradAligned;
-    const bool random_p = !MASTER && !p_f32 && g.random != 0;
-    const int64_t base = (int64_t)(chunk - g.first[e]) * kChunk + threadIdx.x * kPer;
+    const int64_t base = (int64_t)(chunk - g.first[e]) * kChunk;
+    const int64_t held = (t.n + 31) & ~(int64_t)31;  // whole blocks: what lies behind the last value is held at zero
+    const bool whole = base + kChunk <= t.n;
+    const bool p_whole = whole && (t.flags & kParamAligned), g_whole = whole && (t.flags & kGradAligned);
 #pragma unroll
     for (int pass = 0; pass < kChunk / (kThreads * kPer); ++pass) {
-      const int64_t i = base + pass * (kThreads * kPer);
+      const int64_t i = base + pass * (kThreads * kPer) + threadIdx.x * kPer;
       const int64_t at = t.at + i;
-      // whole blocks: what lies behind the last value, up to a multiple of 32, is held at zero
-      if (i >= ((t.n + 31) & ~(int64_t)31)) continue;
+      if (!whole && i >= held) continue;
       float gr[kPer], p[kPer], m[kPer], v[kPer];
       uint32_t r[kPer];
-      load_values(t.grad, g_f32, g_al, i, t.n, gr);
-      if constexpr (MASTER) load_values(g.master + t.at, true, true, i, (t.n + 31) & ~(int64_t)31, p);
-      else load_values(t.param, p_f32, p_al, i, t.n, p);
+      load_values(t.grad, g_f32, g_whole, i, t.n, gr);
+      if constexpr (MASTER) load_state(g.master + at, p);
+      else load_values(t.param, p_f32, p_whole, i, t.n, p);
       if constexpr (Q8) {
         const u32x2_t mq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.m) + at);
         const u32x2_t vq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.v) + at);
         decode_m(mq, g.m_scales[at >> 5], m);
         decode_v(vq, g.v_scales[at >> 5], v);
       } else {
-        load_values(static_cast<const float*>(g.m), true, true, at, at + kPer, m);
-        load_values(static_cast<const float*>(g.v), true, true, at, at + kPer, v);
+        load_state(static_cast<const float*>(g.m) + at, m);
+        load_state(static_cast<const float*>(g.v) + at, v);
       }
+      // (places of eight values share their upper half: they begin at a multiple of 8)
+      const uint32_t place = (uint32_t)at + (uint32_t)((uint64_t)at >> 32) * 0x9E3779B1u + key;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const float x = gr[j] * gs;
         m[j] = m[j] * g.b1 + x * g.not_b1;
         v[j] = v[j] * g.b2 + (x * x) * g.not_b2;
-        p[j] = p[j] * keep - m[j] / (sqrtf(v[j]) * root + g.eps) * rate;
-        if (i + j >= t.n) m[j] = v[j] = p[j] = 0.0f;
-        if (g.random != 0) {
-          const uint64_t place = (uint64_t)(at + j);
-          r[j] = mix32((uint32_t)place + (uint32_t)(place >> 32) * 0x9E3779B1u + key);
-        } else {
-          r[j] = 0;
-        }
+        float step_of;
+        if constexpr (PRECISE) step_of = m[j] / (sqrtf(v[j]) * root + g.eps);
+        else step_of = m[j] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[j]), root, g.eps));
+        p[j] = p[j] * keep - step_of * rate;
+        if constexpr (RANDOM) r[j] = mix32(place + j);
       }
-      store_values(t.param, p_f32, p_al, i, t.n, p, random_p, r);
-      if constexpr (MASTER) store_values(g.master, true, true, at, at + kPer, p, false, r);
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (i + j >= t.n) m[j] = v[j] = p[j] = 0.0f;
+      }
+      store_values<RANDOM && !MASTER>(t.param, p_f32, p_whole, i, t.n, p, r);
+      if constexpr (MASTER) store_state(g.master + at, p);
       if constexpr (Q8) {
         u32x2_t mq, vq;
-        const uint32_t ms = encode_m(m, mq), vs = encode_v(v, g.random != 0, r, vq);
+        const uint32_t ms = encode_m(m, mq), vs = encode_v<RANDOM>(v, r, vq);
         *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.m) + at) = mq;
         *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.v) + at) = vq;
         if ((threadIdx.x & 3) == 0) {
@@ -278,8 +319,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
           g.v_scales[at >> 5] = (uint8_t)vs;
         }
       } else {
-        store_values(g.m, true, true, at, at + kPer, m, false, r);
-        store_values(g.v, true, true, at, at + kPer, v, false, r);
+        store_state(static_cast<float*>(g.m) + at, m);
+        store_state(static_cast<float*>(g.v) + at, v);
       }
     }
   }
@@ -309,9 +350,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 }  // namespace
 
-hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, void* m, uint8_t* m_scales, void* v,
-                        uint8_t* v_scales, float* master, const moe_adamw_hyper& h, const float* lr_ptr,
-                        const int32_t* step_ptr, const float* grad_scale, hipStream_t stream) {
+hipError_t launch_adamw(const moe_adamw_tensor* list, void* const* params, const void* const* grads, int32_t count,
+                        bool q8, void* m, uint8_t* m_scales, void* v, uint8_t* v_scales, float* master,
+                        const moe_adamw_hyper& h, const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale,
+                        hipStream_t stream) {
   AdamArgs g;
   g.m = m, g.m_scales = m_scales, g.v = v, g.v_scales = v_scales, g.master = master;
   g.lr_ptr = lr_ptr, g.step_ptr = step_ptr, g.grad_scale = grad_scale;
@@ -321,7 +363,7 @@ hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, vo
   g.keep = (float)(1.0 - h.lr * h.weight_decay);
   g.rate = (float)(h.lr / -std::expm1(h.step * g.log_b1));
   g.root = (float)(1.0 / std::sqrt(-std::expm1(h.step * g.log_b2)));
-  g.seed = h.seed, g.step = (uint32_t)h.step, g.random = h.stochastic != 0;
+  g.seed = h.seed, g.step = (uint32_t)h.step;
   const int64_t most = (int64_t)device_cu_count(current_device()) * 8;
   int32_t i = 0;
   while (i < count) {
@@ -333,7 +375,7 @@ hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, vo
       if (n == 0) continue;
       if (chunks + n > INT32_MAX) break;
       Listed& t = g.t[g.count];
-      t.param = list[i].param, t.grad = list[i].grad, t.n = list[i].n, t.at = list[i].offset, t.pad = 0;
+      t.param = params[i], t.grad = grads[i], t.n = list[i].n, t.at = list[i].offset, t.pad = 0;
       t.flags = (list[i].param_dtype == MOE_F32 ? kParamF32 : 0) | (list[i].grad_dtype == MOE_F32 ? kGradF32 : 0) |
                 (aligned16(t.param) ? kParamAligned : 0) | (aligned16(t.grad) ? kGradAligned : 0);
       g.first[g.count++] = (uint32_t)chunks;
@@ -342,10 +384,18 @@ hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, vo
     if (g.count == 0) break;
     g.chunks = (uint32_t)chunks;
     const dim3 grid((unsigned)(chunks < most ? chunks : most)), block(kThreads);
-    if (q8 && master != nullptr) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, stream, g);
-    else if (q8) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, stream, g);
-    else if (master != nullptr) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, stream, g);
+    const bool random = h.stochastic != 0, precise = !q8 || h.eps < kLeastEps;
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, g); };
+    if (master != nullptr) {
+      if (!q8) run(adamw_kernel<false, true, false, true>);  // (nothing left to round at random)
+      else if (random) precise ? run(adamw_kernel<true, true, true, true>) : run(adamw_kernel<true, true, true, false>);
+      else precise ? run(adamw_kernel<true, true, false, true>) : run(adamw_kernel<true, true, false, false>);
+    } else if (q8) {
+      if (random) precise ? run(adamw_kernel<true, false, true, true>) : run(adamw_kernel<true, false, true, false>);
+      else precise ? run(adamw_kernel<true, false, false, true>) : run(adamw_kernel<true, false, false, false>);
+    } else {
+      random ? run(adamw_kernel<false, false, true, true>) : run(adamw_kernel<false, false, false, true>);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

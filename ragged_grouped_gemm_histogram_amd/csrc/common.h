@@ -133,9 +133,10 @@ hipError_t launch_norm_backward(const void* dr, const uint16_t* dn, const uint16
                                 float* partial, hipStream_t stream);
 
 // AdamW.
-hipError_t launch_adamw(const moe_adamw_tensor* list, int32_t count, bool q8, void* m, uint8_t* m_scales, void* v,
-                        uint8_t* v_scales, float* master, const moe_adamw_hyper& h, const float* lr_ptr,
-                        const int32_t* step_ptr, const float* grad_scale, hipStream_t stream);
+hipError_t launch_adamw(const moe_adamw_tensor* list, void* const* params, const void* const* grads, int32_t count,
+                        bool q8, void* m, uint8_t* m_scales, void* v, uint8_t* v_scales, float* master,
+                        const moe_adamw_hyper& h, const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale,
+                        hipStream_t stream);
 hipError_t launch_adamw_moments(const uint8_t* m, const uint8_t* ms, const uint8_t* v, const uint8_t* vs, int64_t n,
                                 uint16_t* m_out, uint16_t* v_out, hipStream_t stream);
 

@@ -95,18 +95,23 @@ def test_norm_workspace_bytes(lib):
 def tensors(*rows):
     table = (moe._AdamTensor * max(1, len(rows)))()
     for t, r in zip(table, rows):
-        t.param, t.grad, t.n, t.offset, t.param_dtype, t.grad_dtype = r
+        t.n, t.offset, t.param_dtype, t.grad_dtype = r[2:]
     return table
 
 
+def addresses(rows, at):
+    return (ctypes.c_void_p * max(1, len(rows)))(*[r[at] for r in rows])
+
+
 def adamw(lib, rows=((F, F, 40, 0, 0, 1), (F, F, 3, 64, 1, 0)), count=None, bits=32, length=96, m=F, ms=F, v=F, vs=F, master=F,
-          lr_ptr=None, step_ptr=None, scale=None, hyper=True, **kw):
+          lr_ptr=None, step_ptr=None, scale=None, hyper=True, lists=True, **kw):
     h = moe._AdamHyper(1e-3, 0.9, 0.999, 1e-8, 0.1, 1, 0, 0)
     for k, val in kw.items():
         setattr(h, k, val)
-    table = tensors(*rows)
-    return lib.moe_adamw_step(ctypes.addressof(table), len(rows) if count is None else count, bits, length, m, ms, v, vs,
-                              master, ctypes.addressof(h) if hyper else None, lr_ptr, step_ptr, scale, None)
+    table, params, grads = tensors(*rows), addresses(rows, 0), addresses(rows, 1)
+    return lib.moe_adamw_step(*(ctypes.addressof(a) if lists else None for a in (table, params, grads)),
+                              len(rows) if count is None else count, bits, length, m, ms, v, vs, master,
+                              ctypes.addressof(h) if hyper else None, lr_ptr, step_ptr, scale, None)
 
 
 A = (F, F, 40, 0, 0, 1)
@@ -114,7 +119,7 @@ A = (F, F, 40, 0, 0, 1)
 
 @pytest.mark.parametrize("kw,status", [
     (dict(count=-1), SHAPE), (dict(bits=16), SHAPE), (dict(bits=0), SHAPE), (dict(length=-32), SHAPE),
-    (dict(length=100), SHAPE), (dict(length=64), SHAPE), (dict(hyper=False), NULLP), (dict(m=None), NULLP),
+    (dict(length=100), SHAPE), (dict(length=64), SHAPE), (dict(hyper=False), NULLP), (dict(lists=False), NULLP), (dict(m=None), NULLP),
     (dict(v=None), NULLP), (dict(bits=8, ms=None), NULLP), (dict(bits=8, vs=None), NULLP), (dict(m=F + 8), ALIGN),
     (dict(v=F + 4), ALIGN), (dict(master=F + 8), ALIGN), (dict(lr_ptr=F + 2), ALIGN), (dict(step_ptr=F + 1), ALIGN),
     (dict(scale=F + 2), ALIGN), (dict(rows=((F, F, 40, 0, 2, 0),)), SHAPE), (dict(rows=((F, F, 40, 0, 0, -1),)), SHAPE),
