@@ -74,33 +74,45 @@ __host__ __device__ inline uint32_t mix32(uint32_t h) {
 __device__ __forceinline__ float bits_f32(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t f32_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
-// Eight values of a tensor from place i on; where not all of the chunk's are there, or not aligned, one by one,
-// with zeros behind the end.
-__device__ __forceinline__ void load_values(const void* base, bool f32, bool whole, int64_t i, int64_t n,
-                                            float (&x)[kPer]) {
+// Eight values of a tensor as they were read: fp32, or bf16 in the first half.
+struct Eight {
+  u32x4 lo, hi;
+};
+
+// From place i on; where not all of the chunk's are there, or not aligned, one by one as fp32, with zeros behind
+// the end.
+__device__ __forceinline__ Eight read_values(const void* base, bool f32, bool whole, int64_t i, int64_t n) {
+  Eight x = {};
   if (whole) {
     if (f32) {
-      const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + i);
-      const f32x4_t a = p[0], b = p[1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + i);
+      x.lo = p[0], x.hi = p[1];
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[2 * j] = bits_f32(a[j] << 16), x[2 * j + 1] = bits_f32(a[j] & 0xFFFF0000u);
+      x.lo = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
     }
-    return;
+    return x;
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    x[j] = 0.0f;
+    uint32_t b = 0;
     if (i + j < n)
-      x[j] = f32 ? static_cast<const float*>(base)[i + j]
-                 : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[i + j]);
+      b = f32 ? static_cast<const uint32_t*>(base)[i + j] : (uint32_t)static_cast<const uint16_t*>(base)[i + j] << 16;
+    if (j < 4) x.lo[j] = b;
+    else x.hi[j - 4] = b;
   }
+  return x;
 }
 
-__device__ __forceinline__ void load_state(const float* p, float (&x)[kPer]) { load_values(p, true, true, 0, kPer, x); }
+__device__ __forceinline__ void widen(const Eight& e, bool f32, float (&x)[kPer]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (f32) {
+      x[j] = bits_f32(e.lo[j]), x[4 + j] = bits_f32(e.hi[j]);
+    } else {
+      x[2 * j] = bits_f32(e.lo[j] << 16), x[2 * j + 1] = bits_f32(e.lo[j] & 0xFFFF0000u);
+    }
+  }
+}
 
 __device__ __forceinline__ void store_state(float* p, const float (&x)[kPer]) {
   reinterpret_cast<f32x4_t*>(p)[0] = f32x4_t{x[0], x[1], x[2], x[3]};
@@ -237,13 +249,25 @@ __device__ __forceinline__ uint32_t encode_v(const float (&x)[kPer], const uint3
   return s;
 }
 
+// What a thread holds of one pass before its step.
+template <bool Q8>
+struct Held {
+  Eight grad, param;
+  Eight m, v;  // fp32 moments, or codes in the first two words
+  uint32_t m_scale, v_scale;
+};
+
+// A chunk's tensor and place.
+struct Where {
+  Listed t;
+  int64_t base;
+  bool whole, p_whole, g_whole;  // all of the chunk's values are there; and aligned
+};
+
 // A chunk is two passes of 8 consecutive values a thread; a tensor's moments begin at a multiple of 32, so a
-// block of 32 lies in four neighbouring lanes. PRECISE: root and quotient as the compiler's own; otherwise the
-// instructions themselves, each within an ulp but a second moment below 2^-126 counts as 0, which an eps from
-// kLeastEps on hides (2^-63 / sqrt(1 - b2^t) of it).
-//
-// At 28 bytes a value (bf16, fp32 copy and moments, 398 M values) 2.26 ms, 4.93 TB/s. With 8-bit moments and
-// random rounding, 10.06 bytes, the arithmetic is as long as the traffic: see the figures at launch_adamw.
+// block of 32 lies in four neighbouring lanes. The loads of a pass go out before the step of the pass before it.
+// PRECISE: root and quotient as the compiler's own; otherwise the instructions themselves, each within an ulp
+// but a second moment below 2^-126 counts as 0, which an eps from kLeastEps on hides (2^-63 / sqrt(1 - b2^t) of it).
 template <bool Q8, bool MASTER, bool RANDOM, bool PRECISE>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
   const int lane = threadIdx.x & 63;
@@ -262,68 +286,104 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
   // first chunks of the tensors, for the search
   const uint32_t first0 = lane < g.count ? g.first[lane] : ~0u;
   const uint32_t first1 = 64 + lane < g.count ? g.first[lane + 64 < kListed ? lane + 64 : 0] : ~0u;
-  for (uint32_t chunk = blockIdx.x; chunk < g.chunks; chunk += gridDim.x) {
+
+  auto find = [&](uint32_t chunk) {
     const int e = __builtin_amdgcn_readfirstlane(__popcll(__ballot(first0 <= chunk)) + __popcll(__ballot(first1 <= chunk))) - 1;
-    const Listed t = g.t[e];
-    const bool p_f32 = t.flags & kParamF32, g_f32 = t.flags & kGradF32;
-    const int64_t base = (int64_t)(chunk - g.first[e]) * kChunk;
-    const int64_t held = (t.n + 31) & ~(int64_t)31;  // whole blocks: what lies behind the last value is held at zero
-    const bool whole = base + kChunk <= t.n;
-    const bool p_whole = whole && (t.flags & kParamAligned), g_whole = whole && (t.flags & kGradAligned);
-#pragma unroll
-    for (int pass = 0; pass < kChunk / (kThreads * kPer); ++pass) {
-      const int64_t i = base + pass * (kThreads * kPer) + threadIdx.x * kPer;
-      const int64_t at = t.at + i;
-      if (!whole && i >= held) continue;
-      float gr[kPer], p[kPer], m[kPer], v[kPer];
-      uint32_t r[kPer];
-      load_values(t.grad, g_f32, g_whole, i, t.n, gr);
-      if constexpr (MASTER) load_state(g.master + at, p);
-      else load_values(t.param, p_f32, p_whole, i, t.n, p);
-      if constexpr (Q8) {
-        const u32x2_t mq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.m) + at);
-        const u32x2_t vq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.v) + at);
-        decode_m(mq, g.m_scales[at >> 5], m);
-        decode_v(vq, g.v_scales[at >> 5], v);
-      } else {
-        load_state(static_cast<const float*>(g.m) + at, m);
-        load_state(static_cast<const float*>(g.v) + at, v);
-      }
-      // (places of eight values share their upper half: they begin at a multiple of 8)
-      const uint32_t place = (uint32_t)at + (uint32_t)((uint64_t)at >> 32) * 0x9E3779B1u + key;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float x = gr[j] * gs;
-        m[j] = m[j] * g.b1 + x * g.not_b1;
-        v[j] = v[j] * g.b2 + (x * x) * g.not_b2;
-        float step_of;
-        if constexpr (PRECISE) step_of = m[j] / (sqrtf(v[j]) * root + g.eps);
-        else step_of = m[j] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[j]), root, g.eps));
-        p[j] = p[j] * keep - step_of * rate;
-        if constexpr (RANDOM) r[j] = mix32(place + j);
-      }
-      if (!whole) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (i + j >= t.n) m[j] = v[j] = p[j] = 0.0f;
-      }
-      store_values<RANDOM && !MASTER>(t.param, p_f32, p_whole, i, t.n, p, r);
-      if constexpr (MASTER) store_state(g.master + at, p);
-      if constexpr (Q8) {
-        u32x2_t mq, vq;
-        const uint32_t ms = encode_m(m, mq), vs = encode_v<RANDOM>(v, r, vq);
-        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.m) + at) = mq;
-        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.v) + at) = vq;
-        if ((threadIdx.x & 3) == 0) {
-          g.m_scales[at >> 5] = (uint8_t)ms;
-          g.v_scales[at >> 5] = (uint8_t)vs;
-        }
-      } else {
-        store_state(static_cast<float*>(g.m) + at, m);
-        store_state(static_cast<float*>(g.v) + at, v);
-      }
+    Where w;
+    w.t = g.t[e];
+    w.base = (int64_t)(chunk - g.first[e]) * kChunk;
+    w.whole = w.base + kChunk <= w.t.n;
+    w.p_whole = w.whole && (w.t.flags & kParamAligned), w.g_whole = w.whole && (w.t.flags & kGradAligned);
+    return w;
+  };
+  auto place_of = [&](const Where& w, int pass) {
+    return w.base + pass * (kThreads * kPer) + (int64_t)threadIdx.x * kPer;
+  };
+  // whole blocks: what lies behind a tensor's last value, up to a multiple of 32, is held at zero
+  auto inside = [&](const Where& w, int64_t i) { return w.whole || i < ((w.t.n + 31) & ~(int64_t)31); };
+
+  auto read = [&](Held<Q8>& h, const Where& w, int pass) {
+    const int64_t i = place_of(w, pass), at = w.t.at + i;
+    if (!inside(w, i)) return;
+    h.grad = read_values(w.t.grad, w.t.flags & kGradF32, w.g_whole, i, w.t.n);
+    if constexpr (MASTER) h.param = read_values(g.master, true, true, at, 0);
+    else h.param = read_values(w.t.param, w.t.flags & kParamF32, w.p_whole, i, w.t.n);
+    if constexpr (Q8) {
+      const u32x2_t mq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.m) + at);
+      const u32x2_t vq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.v) + at);
+      h.m.lo[0] = mq[0], h.m.lo[1] = mq[1], h.v.lo[0] = vq[0], h.v.lo[1] = vq[1];
+      h.m_scale = g.m_scales[at >> 5], h.v_scale = g.v_scales[at >> 5];
+    } else {
+      h.m = read_values(g.m, true, true, at, 0), h.v = read_values(g.v, true, true, at, 0);
     }
+  };
+
+  auto update = [&](const Held<Q8>& h, const Where& w, int pass) {
+    const int64_t i = place_of(w, pass), at = w.t.at + i;
+    if (!inside(w, i)) return;
+    float gr[kPer], p[kPer], m[kPer], v[kPer];
+    uint32_t r[kPer];
+    widen(h.grad, !w.g_whole || (w.t.flags & kGradF32), gr);
+    widen(h.param, MASTER || !w.p_whole || (w.t.flags & kParamF32), p);
+    if constexpr (Q8) {
+      decode_m(u32x2_t{h.m.lo[0], h.m.lo[1]}, h.m_scale, m);
+      decode_v(u32x2_t{h.v.lo[0], h.v.lo[1]}, h.v_scale, v);
+    } else {
+      widen(h.m, true, m);
+      widen(h.v, true, v);
+    }
+    // (places of eight values share their upper half: they begin at a multiple of 8)
+    const uint32_t place = (uint32_t)at + (uint32_t)((uint64_t)at >> 32) * 0x9E3779B1u + key;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float x = gr[j] * gs;
+      m[j] = m[j] * g.b1 + x * g.not_b1;
+      v[j] = v[j] * g.b2 + (x * x) * g.not_b2;
+      float step_of;
+      if constexpr (PRECISE) step_of = m[j] / (sqrtf(v[j]) * root + g.eps);
+      else step_of = m[j] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[j]), root, g.eps));
+      p[j] = p[j] * keep - step_of * rate;
+      if constexpr (RANDOM) r[j] = mix32(place + j);
+    }
+    if (!w.whole) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (i + j >= w.t.n) m[j] = v[j] = p[j] = 0.0f;
+    }
+    store_values<RANDOM && !MASTER>(w.t.param, w.t.flags & kParamF32, w.p_whole, i, w.t.n, p, r);
+    if constexpr (MASTER) store_state(g.master + at, p);
+    if constexpr (Q8) {
+      u32x2_t mq, vq;
+      const uint32_t ms = encode_m(m, mq), vs = encode_v<RANDOM>(v, r, vq);
+      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.m) + at) = mq;
+      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.v) + at) = vq;
+      if ((threadIdx.x & 3) == 0) {
+        g.m_scales[at >> 5] = (uint8_t)ms;
+        g.v_scales[at >> 5] = (uint8_t)vs;
+      }
+    } else {
+      store_state(static_cast<float*>(g.m) + at, m);
+      store_state(static_cast<float*>(g.v) + at, v);
+    }
+  };
+
+  static_assert(kChunk == 2 * kThreads * kPer, "two passes");
+  uint32_t chunk = blockIdx.x;
+  if (chunk >= g.chunks) return;
+  Where here = find(chunk);
+  Held<Q8> first = {}, second = {};
+  read(first, here, 0);
+  for (;;) {
+    read(second, here, 1);
+    update(first, here, 0);
+    chunk += gridDim.x;
+    if (chunk >= g.chunks) break;
+    const Where next = find(chunk);
+    read(first, next, 0);
+    update(second, here, 1);
+    here = next;
   }
+  update(second, here, 1);
 }
 
 // The values of 8-bit moments as bf16 (exact: three bits of mantissa), 8 a thread.
