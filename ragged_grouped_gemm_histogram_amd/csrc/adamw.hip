@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kListed = 80;  // tensors per launch: their table travels in the kernel's arguments (4 KB)
 constexpr int kPer = 8;      // consecutive values of a thread
-constexpr int kChunk = kThreads * kPer * 2;  // values of a workgroup's step, within one tensor
+constexpr int kPass = kThreads * kPer;  // values of a workgroup's step; a chunk is one or two, within one tensor
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -61,6 +61,7 @@ struct AdamArgs {
   int32_t count;
   uint32_t first[kListed];           // first chunk of each tensor
   uint32_t chunks;
+  int32_t passes;
   Listed t[kListed];
 };
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
@@ -74,29 +75,51 @@ __host__ __device__ inline uint32_t mix32(uint32_t h) {
 __device__ __forceinline__ float bits_f32(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t f32_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
-// Eight values of a tensor as they were read: fp32, or bf16 in the first half.
+// Eight values of a tensor, four from place i and four from place i + FAR on: next to each other (FAR 4) where
+// blocks of 32 have to lie in four lanes, a workgroup's width apart where every access shall cover whole lines with
+// 4 bytes a value. As they were read: fp32, or bf16 in the first half of lo (FAR 4: all of lo, or of lo and hi).
 struct Eight {
   u32x4 lo, hi;
 };
 
-// From place i on; where not all of the chunk's are there, or not aligned, one by one as fp32, with zeros behind
-// the end.
+template <class V>
+__device__ __forceinline__ V stream_in(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const V*>(p));
+}
+template <class V>
+__device__ __forceinline__ void stream_out(void* p, V v) {
+  __builtin_nontemporal_store(v, static_cast<V*>(p));
+}
+
+// Where not all of the chunk's values are there, or not aligned, they are read one by one as fp32, zeros from n on.
+template <int FAR>
 __device__ __forceinline__ Eight read_values(const void* base, bool f32, bool whole, int64_t i, int64_t n) {
   Eight x = {};
   if (whole) {
     if (f32) {
-      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + i);
-      x.lo = p[0], x.hi = p[1];
+      const float* p = static_cast<const float*>(base) + i;
+      if constexpr (FAR == 4) {  // (half lines: past the caches they would be fetched twice)
+        x.lo = reinterpret_cast<const u32x4*>(p)[0], x.hi = reinterpret_cast<const u32x4*>(p)[1];
+      } else {
+        x.lo = stream_in<u32x4>(p), x.hi = stream_in<u32x4>(p + FAR);
+      }
     } else {
-      x.lo = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + i);
+      const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+      if constexpr (FAR == 4) {
+        x.lo = stream_in<u32x4>(p);
+      } else {
+        const u32x2_t a = stream_in<u32x2_t>(p), b = stream_in<u32x2_t>(p + FAR);
+        x.lo = u32x4{a[0], a[1], b[0], b[1]};
+      }
     }
     return x;
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
+    const int64_t k = i + (j < 4 ? j : FAR + j - 4);
     uint32_t b = 0;
-    if (i + j < n)
-      b = f32 ? static_cast<const uint32_t*>(base)[i + j] : (uint32_t)static_cast<const uint16_t*>(base)[i + j] << 16;
+    if (k < n)
+      b = f32 ? static_cast<const uint32_t*>(base)[k] : (uint32_t)static_cast<const uint16_t*>(base)[k] << 16;
     if (j < 4) x.lo[j] = b;
     else x.hi[j - 4] = b;
   }
@@ -112,11 +135,6 @@ __device__ __forceinline__ void widen(const Eight& e, bool f32, float (&x)[kPer]
       x[2 * j] = bits_f32(e.lo[j] << 16), x[2 * j + 1] = bits_f32(e.lo[j] & 0xFFFF0000u);
     }
   }
-}
-
-__device__ __forceinline__ void store_state(float* p, const float (&x)[kPer]) {
-  reinterpret_cast<f32x4_t*>(p)[0] = f32x4_t{x[0], x[1], x[2], x[3]};
-  reinterpret_cast<f32x4_t*>(p)[1] = f32x4_t{x[4], x[5], x[6], x[7]};
 }
 
 // The largest magnitude of eight values; a NaN if one is.
@@ -151,17 +169,26 @@ __device__ __forceinline__ u32x4 random_bf16(const float (&x)[kPer], const uint3
   return o;
 }
 
-template <bool RANDOM>
+template <bool RANDOM, int FAR>
 __device__ __forceinline__ void store_values(void* base, bool f32, bool whole, int64_t i, int64_t n,
                                              const float (&x)[kPer], const uint32_t (&r)[kPer]) {
   if (f32) {
     float* p = static_cast<float*>(base) + i;
     if (whole) {
-      store_state(p, x);
+      const f32x4_t lo = {x[0], x[1], x[2], x[3]}, hi = {x[4], x[5], x[6], x[7]};
+      if constexpr (FAR == 4) {  // (half lines: past the caches they would be written twice)
+        reinterpret_cast<f32x4_t*>(p)[0] = lo;
+        reinterpret_cast<f32x4_t*>(p)[1] = hi;
+      } else {
+        stream_out(p, lo);
+        stream_out(p + FAR, hi);
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (i + j < n) p[j] = x[j];
+      for (int j = 0; j < kPer; ++j) {
+        const int k = j < 4 ? j : FAR + j - 4;
+        if (i + k < n) p[k] = x[j];
+      }
     }
     return;
   }
@@ -174,11 +201,18 @@ __device__ __forceinline__ void store_values(void* base, bool f32, bool whole, i
   }
   uint16_t* p = static_cast<uint16_t*>(base) + i;
   if (whole) {
-    *reinterpret_cast<u32x4*>(p) = o;
+    if constexpr (FAR == 4) {
+      stream_out(p, o);
+    } else {
+      stream_out(p, u32x2_t{o[0], o[1]});
+      stream_out(p + FAR, u32x2_t{o[2], o[3]});
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (i + j < n) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < kPer; ++j) {
+      const int k = j < 4 ? j : FAR + j - 4;
+      if (i + k < n) p[k] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+    }
   }
 }
 
@@ -249,7 +283,7 @@ __device__ __forceinline__ uint32_t encode_v(const float (&x)[kPer], const uint3
   return s;
 }
 
-// What a thread holds of one pass before its step.
+// What a thread holds of a pass before its step.
 template <bool Q8>
 struct Held {
   Eight grad, param;
@@ -264,8 +298,9 @@ struct Where {
   bool whole, p_whole, g_whole;  // all of the chunk's values are there; and aligned
 };
 
-// A chunk is two passes of 8 consecutive values a thread; a tensor's moments begin at a multiple of 32, so a
-// block of 32 lies in four neighbouring lanes. The loads of a pass go out before the step of the pass before it.
+// A pass is 8 values a thread; with 8-bit moments they are consecutive, and since a tensor's moments begin at a
+// multiple of 32, a block of 32 lies in four neighbouring lanes. A pass's loads go out before the step of the one
+// before it.
 // PRECISE: root and quotient as the compiler's own; otherwise the instructions themselves, each within an ulp
 // but a second moment below 2^-126 counts as 0, which an eps from kLeastEps on hides (2^-63 / sqrt(1 - b2^t) of it).
 template <bool Q8, bool MASTER, bool RANDOM, bool PRECISE>
@@ -291,36 +326,38 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
     const int e = __builtin_amdgcn_readfirstlane(__popcll(__ballot(first0 <= chunk)) + __popcll(__ballot(first1 <= chunk))) - 1;
     Where w;
     w.t = g.t[e];
-    w.base = (int64_t)(chunk - g.first[e]) * kChunk;
-    w.whole = w.base + kChunk <= w.t.n;
+    w.base = (int64_t)(chunk - g.first[e]) * (g.passes * kPass);
+    w.whole = w.base + g.passes * kPass <= w.t.n;
     w.p_whole = w.whole && (w.t.flags & kParamAligned), w.g_whole = w.whole && (w.t.flags & kGradAligned);
     return w;
   };
+  constexpr int kFar = Q8 ? 4 : 4 * kThreads;
   auto place_of = [&](const Where& w, int pass) {
-    return w.base + pass * (kThreads * kPer) + (int64_t)threadIdx.x * kPer;
+    return w.base + pass * kPass + (int64_t)threadIdx.x * (Q8 ? kPer : 4);
   };
   // whole blocks: what lies behind a tensor's last value, up to a multiple of 32, is held at zero
-  auto inside = [&](const Where& w, int64_t i) { return w.whole || i < ((w.t.n + 31) & ~(int64_t)31); };
+  auto held = [&](const Where& w) { return (w.t.n + 31) & ~(int64_t)31; };
 
   auto read = [&](Held<Q8>& h, const Where& w, int pass) {
     const int64_t i = place_of(w, pass), at = w.t.at + i;
-    if (!inside(w, i)) return;
-    h.grad = read_values(w.t.grad, w.t.flags & kGradF32, w.g_whole, i, w.t.n);
-    if constexpr (MASTER) h.param = read_values(g.master, true, true, at, 0);
-    else h.param = read_values(w.t.param, w.t.flags & kParamF32, w.p_whole, i, w.t.n);
+    if (!w.whole && i >= held(w)) return;
+    h.grad = read_values<kFar>(w.t.grad, w.t.flags & kGradF32, w.g_whole, i, w.t.n);
+    if constexpr (MASTER) h.param = read_values<kFar>(g.master + w.t.at, true, w.whole, i, held(w));
+    else h.param = read_values<kFar>(w.t.param, w.t.flags & kParamF32, w.p_whole, i, w.t.n);
     if constexpr (Q8) {
-      const u32x2_t mq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.m) + at);
-      const u32x2_t vq = *reinterpret_cast<const u32x2_t*>(static_cast<const uint8_t*>(g.v) + at);
+      const u32x2_t mq = stream_in<u32x2_t>(static_cast<const uint8_t*>(g.m) + at);
+      const u32x2_t vq = stream_in<u32x2_t>(static_cast<const uint8_t*>(g.v) + at);
       h.m.lo[0] = mq[0], h.m.lo[1] = mq[1], h.v.lo[0] = vq[0], h.v.lo[1] = vq[1];
       h.m_scale = g.m_scales[at >> 5], h.v_scale = g.v_scales[at >> 5];
     } else {
-      h.m = read_values(g.m, true, true, at, 0), h.v = read_values(g.v, true, true, at, 0);
+      h.m = read_values<kFar>(static_cast<const float*>(g.m) + w.t.at, true, w.whole, i, held(w));
+      h.v = read_values<kFar>(static_cast<const float*>(g.v) + w.t.at, true, w.whole, i, held(w));
     }
   };
 
   auto update = [&](const Held<Q8>& h, const Where& w, int pass) {
     const int64_t i = place_of(w, pass), at = w.t.at + i;
-    if (!inside(w, i)) return;
+    if (!w.whole && i >= held(w)) return;
     float gr[kPer], p[kPer], m[kPer], v[kPer];
     uint32_t r[kPer];
     widen(h.grad, !w.g_whole || (w.t.flags & kGradF32), gr);
@@ -332,8 +369,13 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
       widen(h.m, true, m);
       widen(h.v, true, v);
     }
-    // (places of eight values share their upper half: they begin at a multiple of 8)
-    const uint32_t place = (uint32_t)at + (uint32_t)((uint64_t)at >> 32) * 0x9E3779B1u + key;
+    // (the places of four values share their upper half: they begin at a multiple of 4)
+    uint32_t place[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint64_t from = (uint64_t)at + k * kFar;
+      place[k] = (uint32_t)from + (uint32_t)(from >> 32) * 0x9E3779B1u + key;
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float x = gr[j] * gs;
@@ -343,47 +385,47 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamArgs g) {
       if constexpr (PRECISE) step_of = m[j] / (sqrtf(v[j]) * root + g.eps);
       else step_of = m[j] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[j]), root, g.eps));
       p[j] = p[j] * keep - step_of * rate;
-      if constexpr (RANDOM) r[j] = mix32(place + j);
+      if constexpr (RANDOM) r[j] = mix32(place[j >> 2] + (j & 3));
     }
     if (!w.whole) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (i + j >= w.t.n) m[j] = v[j] = p[j] = 0.0f;
+        if (i + (j < 4 ? j : kFar + j - 4) >= w.t.n) m[j] = v[j] = p[j] = 0.0f;
     }
-    store_values<RANDOM && !MASTER>(w.t.param, w.t.flags & kParamF32, w.p_whole, i, w.t.n, p, r);
-    if constexpr (MASTER) store_state(g.master + at, p);
+    store_values<RANDOM && !MASTER, kFar>(w.t.param, w.t.flags & kParamF32, w.p_whole, i, w.t.n, p, r);
+    if constexpr (MASTER) store_values<false, kFar>(g.master + w.t.at, true, w.whole, i, held(w), p, r);
     if constexpr (Q8) {
       u32x2_t mq, vq;
       const uint32_t ms = encode_m(m, mq), vs = encode_v<RANDOM>(v, r, vq);
-      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.m) + at) = mq;
-      *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(g.v) + at) = vq;
+      stream_out(static_cast<uint8_t*>(g.m) + at, mq);
+      stream_out(static_cast<uint8_t*>(g.v) + at, vq);
       if ((threadIdx.x & 3) == 0) {
         g.m_scales[at >> 5] = (uint8_t)ms;
         g.v_scales[at >> 5] = (uint8_t)vs;
       }
     } else {
-      store_state(static_cast<float*>(g.m) + at, m);
-      store_state(static_cast<float*>(g.v) + at, v);
+      store_values<false, kFar>(static_cast<float*>(g.m) + w.t.at, true, w.whole, i, held(w), m, r);
+      store_values<false, kFar>(static_cast<float*>(g.v) + w.t.at, true, w.whole, i, held(w), v, r);
     }
   };
 
-  static_assert(kChunk == 2 * kThreads * kPer, "two passes");
+  const bool two = g.passes == 2;
   uint32_t chunk = blockIdx.x;
   if (chunk >= g.chunks) return;
   Where here = find(chunk);
   Held<Q8> first = {}, second = {};
   read(first, here, 0);
   for (;;) {
-    read(second, here, 1);
+    if (two) read(second, here, 1);
     update(first, here, 0);
     chunk += gridDim.x;
     if (chunk >= g.chunks) break;
     const Where next = find(chunk);
     read(first, next, 0);
-    update(second, here, 1);
+    if (two) update(second, here, 1);
     here = next;
   }
-  update(second, here, 1);
+  if (two) update(second, here, 1);
 }
 
 // The values of 8-bit moments as bf16 (exact: three bits of mantissa), 8 a thread.
@@ -425,13 +467,19 @@ hipError_t launch_adamw(const moe_adamw_tensor* list, void* const* params, const
   g.root = (float)(1.0 / std::sqrt(-std::expm1(h.step * g.log_b2)));
   g.seed = h.seed, g.step = (uint32_t)h.step;
   const int64_t most = (int64_t)device_cu_count(current_device()) * 8;
+  // Two passes a chunk hide the loads behind the steps; with too few chunks for that, one spreads the work over more
+  // CUs (268 K values, fp32 throughout: 5.5 us, two 7.4; 398 M values: 2332 us, two 2174).
+  int64_t values = 0;
+  for (int32_t i = 0; i < count; ++i) values += list[i].n;
+  g.passes = values < 2 * most * kPass ? 1 : 2;
+  const int64_t per_chunk = g.passes * kPass;
   int32_t i = 0;
   while (i < count) {
     // as many tensors as the table holds and whose chunks a launch can count
     int64_t chunks = 0;
     g.count = 0;
     for (; i < count && g.count < kListed; ++i) {
-      const int64_t n = (list[i].n + kChunk - 1) / kChunk;
+      const int64_t n = (list[i].n + per_chunk - 1) / per_chunk;
       if (n == 0) continue;
       if (chunks + n > INT32_MAX) break;
       Listed& t = g.t[g.count];
