@@ -15,8 +15,9 @@
 // forward are kept. Everything is fp32 after the loads; each output is rounded once.
 //
 // A row belongs to a team of ceil(d / 512) waves (half as many above 8192), a lane holding 8
-// consecutive columns (twice 8). The backward's teams walk the rows with the column sums in registers;
-// each leaves one row of partial sums, which a second launch adds in order, so results repeat bit for bit.
+// consecutive columns (twice 8). The backward's teams walk the rows with the column sums in registers; a
+// workgroup joins its teams' and leaves one row of partial sums, which a second launch adds in order, so
+// results repeat bit for bit.
 
 #include "common.h"
 
@@ -43,7 +44,8 @@ struct NormArgs {
   const uint16_t* dn_add;  // a second part of it, or NULL
   uint16_t* dy;
   float* d_gate_token;
-  float* partial;        // [teams][sums][d]
+  float* partial;        // [workgroups][sums][d]
+  int team_waves;
 };
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
@@ -116,10 +118,10 @@ __device__ __forceinline__ float wave_sum(float x) {
   return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }
 
-// Sums over the whole team, the same in every lane. `buf` alternates between two LDS areas, so one
+// Sums over a team of `waves` waves from wave `first` of the workgroup on, the same in every lane. `buf` alternates between two LDS areas, so one
 // barrier a round is enough: a wave reaches the round after next only behind the next one's barrier.
 template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[kMaxWaves][N], int& buf, int waves) {
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[kMaxWaves][N], int& buf, int waves, int first = 0) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if (waves == 1) return;
@@ -131,7 +133,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[kMaxWaves][
   __syncthreads();
   const int from = lane & 15;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = sum16(from < waves ? red[buf][from][i] : 0.0f);
+  for (int i = 0; i < N; ++i) v[i] = sum16(from < waves ? red[buf][first + from][i] : 0.0f);
   buf ^= 1;
 }
 
@@ -212,19 +214,105 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs g) {
   }
 }
 
-// CHANNEL: the gate is one per channel. The column sums stand in the order dw_next, dw_post, dgate, those
-// that the form has.
-template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL, int V>
-__global__ __launch_bounds__(64 * kMaxWaves) void norm_backward_kernel(NormArgs g) {
+// A row of a tensor as a buffer resource: what lies behind its `bytes` reads as zeros and is not written, so lanes
+// past the last column, rows past the last and tensors that are not there need no branches.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* base, int64_t offset, int bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base) + (uint64_t)offset;
+  // (readfirstlane gives an int: its sign must not reach the upper half)
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+__device__ __forceinline__ u32x4 read16(__amdgpu_buffer_rsrc_t row, uint32_t at) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, at, 0, 0));
+}
+
+// Eight columns as they are read, from column `col` of a row on.
+template <class S>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void read(__amdgpu_buffer_rsrc_t row, int col) { v = read16(row, col * 2); }
+  __device__ __forceinline__ float operator[](int i) const {
+    return __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+  }
+};
+template <>
+struct Raw<float> {
+  u32x4 lo, hi;
+  __device__ __forceinline__ void read(__amdgpu_buffer_rsrc_t row, int col) {
+    lo = read16(row, col * 4), hi = read16(row, col * 4 + 16);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return __builtin_bit_cast(float, i < 4 ? lo[i] : hi[i - 4]); }
+};
+
+__device__ __forceinline__ void write8(__amdgpu_buffer_rsrc_t row, int col, const float (&v)[8], uint16_t) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  __builtin_amdgcn_raw_buffer_store_b128(o, row, col * 2, 0, 0);
+}
+__device__ __forceinline__ void write8(__amdgpu_buffer_rsrc_t row, int col, const float (&v)[8], float) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x4_t o = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), row, col * 4 + 16 * i, 0, 0);
+  }
+}
+
+// One row of the backward's inputs, a lane's columns of it.
+template <class S, int V>
+struct BackRow {
+  Raw<S> x[V], d[V];
+  Raw<uint16_t> dn[V], more[V], y[V];
+};
+
+constexpr int kBackWaves = 8;  // a workgroup: as many teams as fit, one WIDE team above
+constexpr int kBackLds = 96 * 1024;  // for the weights: all three of 8192 columns
+
+// CHANNEL: the gate is one per channel. ADD: d_n comes in two parts. The column sums stand in the order dw_next,
+// dw_post, dgate, those that the form has. A row's loads go out before the row before it is computed (not with V = 2,
+// whose registers do not hold two rows); for that the weights come from LDS: loads return in order, so one of a
+// weight would wait for the whole row read ahead. WIDE: a team of more than 8 waves.
+template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL, bool ADD, bool WIDE, int V>
+__global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_backward_kernel(NormArgs g) {
   constexpr int kCols = (NEXT ? 1 : 0) + (POST ? 1 : 0) + (CHANNEL ? 1 : 0);
   constexpr int kColPost = NEXT ? 1 : 0, kColGate = kColPost + (POST ? 1 : 0);
   __shared__ float red[2][kMaxWaves][6];
-  const int waves = blockDim.x >> 6;
-  const S* x_in = static_cast<const S*>(g.r);
-  const S* dr_in = static_cast<const S*>(g.dr);
-  S* dr_out = static_cast<S*>(g.r_out);
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  float* w_lds = reinterpret_cast<float*>(lds);  // the weights in the order of their sums as fp32, 0 past the last column
+  const int waves = g.team_waves, span = 64 * waves, padded = span * 8 * V;
+  const int team = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / waves;  // the same for a whole wave
+  const int at = (int)threadIdx.x - team * span;
   const float inv_d = 1.0f / (float)g.d;
   const bool token = BRANCH && g.gate_kind == MOE_GATE_TOKEN;
+  const bool in_lds = !WIDE || kCols * padded * (int)sizeof(float) <= kBackLds;
+  const int s_bytes = g.d * (int)sizeof(S), h_bytes = g.d * 2;  // a row of the stream, of the block's side
+  const void* sources[3] = {nullptr, nullptr, nullptr};
+  if constexpr (NEXT) sources[0] = g.w_next;
+  if constexpr (POST) sources[kColPost] = g.w_post;
+  if constexpr (CHANNEL) sources[kColGate] = g.gate;
+  auto load_padded = [&](int k, int col, float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+    if (col < g.d) load_weight(sources[k], g.w_f32, col, w);
+  };
+  if (in_lds) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      for (int col = threadIdx.x * 8; col < padded; col += blockDim.x * 8) {
+        float w[8];
+        load_padded(k, col, w);
+        store8(w_lds + k * padded + col, w);
+      }
+    __syncthreads();
+  }
+  auto weight = [&](int k, int col, float (&w)[8]) {
+    if (in_lds) load8(w_lds + k * padded + col, w);
+    else load_padded(k, col, w);
+  };
   float acc[kCols > 0 ? kCols : 1][V][8];
 #pragma unroll
   for (int k = 0; k < kCols; ++k)
@@ -232,122 +320,169 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_backward_kernel(NormArgs 
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[k][j][i] = 0.0f;
+
+  auto read = [&](BackRow<S, V>& row, int64_t t) {
+    const int sb = t < g.T ? s_bytes : 0, hb = t < g.T ? h_bytes : 0;
+    const auto x = row_of(g.r, t * s_bytes, NEXT ? sb : 0), d = row_of(g.dr, t * s_bytes, g.dr != nullptr ? sb : 0);
+    const auto dn = row_of(g.dn, t * h_bytes, NEXT ? hb : 0), more = row_of(g.dn_add, t * h_bytes, ADD ? hb : 0);
+    const auto y = row_of(g.y, t * h_bytes, POST || CHANNEL || token ? hb : 0);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = (j * span + at) * 8;
+      if constexpr (NEXT) row.x[j].read(x, col), row.dn[j].read(dn, col);
+      if constexpr (ADD) row.more[j].read(more, col);
+      row.d[j].read(d, col);
+      if constexpr (BRANCH) row.y[j].read(y, col);
+    }
+  };
+
   int buf = 0;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    const int64_t row = t * g.d;
-    float x[V][8], d[V][8], dn[V][8], y[V][8];
+  auto compute = [&](const BackRow<S, V>& row, int64_t t) {
     float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
+      const int col = (j * span + at) * 8;
+      float wn[8], wp[8], gc[8];
+      if constexpr (NEXT) weight(0, col, wn);
+      if constexpr (POST) weight(kColPost, col, wp);
+      if constexpr (CHANNEL) weight(kColGate, col, gc);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = d[j][i] = dn[j][i] = y[j][i] = 0.0f;
-      if (col < g.d) {
+      for (int i = 0; i < 8; ++i) {
+        float q = 0.0f;
+        if constexpr (BRANCH) q = row.y[j][i];
+        if constexpr (POST) {
+          s[2] = fmaf(q, q, s[2]);
+          q *= wp[i];
+        }
+        if constexpr (CHANNEL) q *= gc[i];
+        if constexpr (BRANCH) s[3] = fmaf(q, row.d[j][i], s[3]);
         if constexpr (NEXT) {
-          load8(x_in + row + col, x[j]);
-          load8(g.dn + row + col, dn[j]);
-          if (g.dn_add != nullptr) {
-            float more[8];
-            load8(g.dn_add + row + col, more);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dn[j][i] += more[i];
-          }
-        }
-        if (dr_in != nullptr) load8(dr_in + row + col, d[j]);
-        if constexpr (POST || CHANNEL) load8(g.y + row + col, y[j]);
-        else if (token) load8(g.y + row + col, y[j]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
-      if (col < g.d) {
-        float wn[8], wp[8], gc[8];
-        if constexpr (NEXT) load_weight(g.w_next, g.w_f32, col, wn);
-        if constexpr (POST) load_weight(g.w_post, g.w_f32, col, wp);
-        if constexpr (CHANNEL) load_weight(g.gate, g.w_f32, col, gc);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float h = NEXT ? dn[j][i] * wn[i] : 0.0f;
-          float q = y[j][i];
-          if constexpr (POST) q *= wp[i];
-          if constexpr (CHANNEL) q *= gc[i];
-          if constexpr (NEXT) {
-            s[0] = fmaf(x[j][i], x[j][i], s[0]);
-            s[1] = fmaf(h, x[j][i], s[1]);
-          }
-          if constexpr (POST) s[2] = fmaf(y[j][i], y[j][i], s[2]);
+          const float dn = ADD ? row.dn[j][i] + row.more[j][i] : row.dn[j][i], h = dn * wn[i], x = row.x[j][i];
+          s[0] = fmaf(x, x, s[0]);
+          s[1] = fmaf(h, x, s[1]);
           if constexpr (BRANCH) {
-            s[3] = fmaf(q, d[j][i], s[3]);
-            if constexpr (NEXT) {
-              s[4] = fmaf(q, h, s[4]);
-              s[5] = fmaf(q, x[j][i], s[5]);
-            }
+            s[4] = fmaf(q, h, s[4]);
+            s[5] = fmaf(q, x, s[5]);
           }
         }
       }
     }
-    if (NEXT || POST || token) team_sum(s, red, buf, waves);
+    if (NEXT || POST || token) team_sum(s, red, buf, waves, team * waves);
+    float gate = 1.0f;
+    if (token && t < g.T) gate = static_cast<const float*>(g.gate)[t];
     const float k1 = NEXT ? rsqrtf(fmaf(s[0], inv_d, g.eps)) : 0.0f;
     const float k2 = k1 * s[1] * inv_d * k1 * k1;
     const float qg = s[3] + k1 * s[4] - k2 * s[5];  // sum of q g
     const float rsy = POST ? rsqrtf(fmaf(s[2], inv_d, g.eps)) : 1.0f;
-    const float bt = token ? g.b * static_cast<const float*>(g.gate)[t] : g.b;
+    const float bt = g.b * gate;
     const float p1 = rsy * bt, p2 = rsy * qg * inv_d * rsy * rsy * bt;
-    if (token && threadIdx.x == 0) g.d_gate_token[t] = g.b * rsy * qg;
+    if (token && at == 0 && t < g.T) g.d_gate_token[t] = g.b * rsy * qg;
+    const auto dr_row = row_of(g.r_out, t * s_bytes, t < g.T ? s_bytes : 0);
+    const auto dy_row = row_of(g.dy, t * h_bytes, BRANCH && t < g.T ? h_bytes : 0);
+    if (t >= g.T) return;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
-      if (col < g.d) {
-        float wn[8], wp[8], gc[8], dx[8], dy[8];
-        if constexpr (NEXT) load_weight(g.w_next, g.w_f32, col, wn);
-        if constexpr (POST) load_weight(g.w_post, g.w_f32, col, wp);
-        if constexpr (CHANNEL) load_weight(g.gate, g.w_f32, col, gc);
+      const int col = (j * span + at) * 8;
+      float wn[8], wp[8], gc[8], dx[8], dy[8];
+      if constexpr (NEXT) weight(0, col, wn);
+      if constexpr (POST) weight(kColPost, col, wp);
+      if constexpr (CHANNEL) weight(kColGate, col, gc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float gr = d[j][i];
-          if constexpr (NEXT) {
-            gr = fmaf(k1, dn[j][i] * wn[i], gr);
-            gr = fmaf(-k2, x[j][i], gr);
-            acc[0][j][i] = fmaf(dn[j][i], x[j][i] * k1, acc[0][j][i]);
+      for (int i = 0; i < 8; ++i) {
+        float gr = row.d[j][i];
+        if constexpr (NEXT) {
+          const float dn = ADD ? row.dn[j][i] + row.more[j][i] : row.dn[j][i], x = row.x[j][i];
+          gr = fmaf(k1, dn * wn[i], gr);
+          gr = fmaf(-k2, x, gr);
+          acc[0][j][i] = fmaf(dn, x * k1, acc[0][j][i]);
+        }
+        dx[i] = g.a * gr;
+        if constexpr (BRANCH) {
+          const float gated = CHANNEL ? gr * gc[i] : gr, y = row.y[j][i];
+          if constexpr (POST) {
+            acc[kColPost][j][i] = fmaf(p1 * gated, y, acc[kColPost][j][i]);
+            dy[i] = fmaf(p1 * gated, wp[i], -p2 * y);
+          } else {
+            dy[i] = p1 * gated;
           }
-          dx[i] = g.a * gr;
-          if constexpr (BRANCH) {
-            const float gated = CHANNEL ? gr * gc[i] : gr;
-            if constexpr (POST) {
-              acc[kColPost][j][i] = fmaf(p1 * gated, y[j][i], acc[kColPost][j][i]);
-              dy[i] = fmaf(p1 * gated, wp[i], -p2 * y[j][i]);
-            } else {
-              dy[i] = p1 * gated;
-            }
-            if constexpr (CHANNEL) {
-              const float u = POST ? y[j][i] * wp[i] : y[j][i];
-              acc[kColGate][j][i] = fmaf(p1 * gr, u, acc[kColGate][j][i]);
-            }
+          if constexpr (CHANNEL) {
+            const float u = POST ? y * wp[i] : y;
+            acc[kColGate][j][i] = fmaf(p1 * gr, u, acc[kColGate][j][i]);
           }
         }
-        store8(dr_out + row + col, dx);
-        if constexpr (BRANCH) store8(g.dy + row + col, dy);
       }
+      write8(dr_row, col, dx, S{});
+      if constexpr (BRANCH) write8(dy_row, col, dy, uint16_t{});
+    }
+  };
+
+  // rows t0 + team of every workgroup's turn; a team without a row goes along, for the barriers
+  const int teams = WIDE ? 1 : (int)blockDim.x / span;
+  const int64_t turn = (int64_t)gridDim.x * teams;
+  int64_t t0 = (int64_t)blockIdx.x * teams;
+  if constexpr (V > 1) {
+    for (; t0 < g.T; t0 += turn) {
+      BackRow<S, V> row;
+      read(row, t0 + team);
+      compute(row, t0 + team);
+    }
+  } else {
+    BackRow<S, V> even, odd;
+    read(even, t0 + team);
+    while (t0 < g.T) {
+      read(odd, t0 + turn + team);
+      compute(even, t0 + team);
+      t0 += turn;
+      if (t0 >= g.T) break;
+      read(even, t0 + turn + team);
+      compute(odd, t0 + team);
+      t0 += turn;
     }
   }
+  // the teams' sums, one after the other
+  if constexpr (kCols > 0 && !WIDE) {
+    __syncthreads();  // (the weights' last reads)
+    for (int k = 1; k < teams; ++k) {
+      if (team == k) {
 #pragma unroll
-  for (int k = 0; k < kCols; ++k) {
+        for (int c = 0; c < kCols; ++c)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
-      if (col < g.d) store8(g.partial + ((int64_t)blockIdx.x * kCols + k) * g.d + col, acc[k][j]);
+          for (int j = 0; j < V; ++j) store8(w_lds + c * padded + (j * span + at) * 8, acc[c][j]);
+      }
+      __syncthreads();
+      if (team == 0) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            float more[8];
+            load8(w_lds + c * padded + (j * span + at) * 8, more);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[c][j][i] += more[i];
+          }
+      }
+      __syncthreads();
+    }
+  }
+  if (team == 0) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int col = (j * span + at) * 8;
+        if (col < g.d) store8(g.partial + ((int64_t)blockIdx.x * kCols + k) * g.d + col, acc[k][j]);
+      }
     }
   }
 }
 
-// out[c] = sum over teams of partial[team][k][c]: 64 columns a workgroup, the teams dealt to 16 waves,
+// out[c] = sum over groups of partial[group][k][c]: 64 columns a workgroup, the groups dealt to 16 waves,
 // whose sums are joined in order.
 constexpr int kSumWaves = 16;
 struct ColumnSums {
   float* out[3];
 };
-__global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float* __restrict__ partial, int teams,
+__global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float* __restrict__ partial, int groups,
                                                                     int cols, int d, ColumnSums o) {
   __shared__ float red[kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k = blockIdx.y;
@@ -357,7 +492,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float*
     const float* p = partial + (int64_t)k * d + col;
     const int64_t pitch = (int64_t)cols * d;
 #pragma unroll 8
-    for (int i = wave; i < teams; i += kSumWaves) sum += p[i * pitch];
+    for (int i = wave; i < groups; i += kSumWaves) sum += p[i * pitch];
   }
   red[wave][lane] = sum;
   __syncthreads();
@@ -395,34 +530,60 @@ hipError_t forward(const NormArgs& g, bool branch, bool post, bool next, hipStre
   return next ? run_forward<S, true, false, true>(g, stream) : run_forward<S, true, false, false>(g, stream);
 }
 
+// Teams of a backward workgroup.
+inline int back_teams(int64_t d) {
+  const int fit = kBackWaves / team_waves(d);
+  return fit > 1 ? fit : 1;
+}
+
+template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL, bool ADD>
+hipError_t run_backward(const NormArgs& g, int groups, hipStream_t stream) {
+  constexpr int kCols = (NEXT ? 1 : 0) + (POST ? 1 : 0) + (CHANNEL ? 1 : 0);
+  const int teams = back_teams(g.d);
+  const dim3 grid(groups), block(64 * g.team_waves * teams);
+  size_t lds = (size_t)kCols * g.team_waves * 512 * vectors(g.d) * sizeof(float);  // the weights; at the end a team's sums
+  if (lds > kBackLds) lds = 0;  // (V = 2 alone)
+  auto run = [&](auto kernel) {
+    if (lds > 64 * 1024) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               kBackLds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, grid, block, lds, stream, g);
+    return hipGetLastError();
+  };
+  if (g.team_waves <= kBackWaves) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, false, 1>);
+  if (vectors(g.d) == 1) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, true, 1>);
+  return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, true, 2>);
+}
+
 template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL>
-hipError_t run_backward(const NormArgs& g, int teams, hipStream_t stream) {
-  const dim3 grid(teams), block(64 * team_waves(g.d));
-  if (vectors(g.d) == 1)
-    hipLaunchKernelGGL((norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, 1>), grid, block, 0, stream, g);
-  else
-    hipLaunchKernelGGL((norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, 2>), grid, block, 0, stream, g);
-  return hipGetLastError();
+hipError_t backward_parts(const NormArgs& g, int groups, hipStream_t stream) {
+  if constexpr (NEXT) {
+    if (g.dn_add != nullptr) return run_backward<S, BRANCH, POST, NEXT, CHANNEL, true>(g, groups, stream);
+  }
+  return run_backward<S, BRANCH, POST, NEXT, CHANNEL, false>(g, groups, stream);
 }
 
 template <class S, bool POST, bool NEXT>
-hipError_t backward_branch(const NormArgs& g, int teams, hipStream_t stream) {
-  return g.gate_kind == MOE_GATE_CHANNEL ? run_backward<S, true, POST, NEXT, true>(g, teams, stream)
-                                         : run_backward<S, true, POST, NEXT, false>(g, teams, stream);
+hipError_t backward_branch(const NormArgs& g, int groups, hipStream_t stream) {
+  return g.gate_kind == MOE_GATE_CHANNEL ? backward_parts<S, true, POST, NEXT, true>(g, groups, stream)
+                                         : backward_parts<S, true, POST, NEXT, false>(g, groups, stream);
 }
 
 template <class S>
-hipError_t backward(const NormArgs& g, bool branch, bool post, bool next, int teams, hipStream_t stream) {
-  if (!branch) return run_backward<S, false, false, true, false>(g, teams, stream);
-  if (post) return next ? backward_branch<S, true, true>(g, teams, stream) : backward_branch<S, true, false>(g, teams, stream);
-  return next ? backward_branch<S, false, true>(g, teams, stream) : backward_branch<S, false, false>(g, teams, stream);
+hipError_t backward(const NormArgs& g, bool branch, bool post, bool next, int groups, hipStream_t stream) {
+  if (!branch) return backward_parts<S, false, false, true, false>(g, groups, stream);
+  if (post) return next ? backward_branch<S, true, true>(g, groups, stream) : backward_branch<S, true, false>(g, groups, stream);
+  return next ? backward_branch<S, false, true>(g, groups, stream) : backward_branch<S, false, false>(g, groups, stream);
 }
 
 }  // namespace
 
+// As many workgroups as are resident on 256 CUs: more partial rows would cost more than they overlap.
 int64_t norm_partial_rows(int64_t T, int64_t d) {
-  const int64_t most = 32 / team_waves(d) < 3 ? 512 : 768;
-  return T < most ? T : most;
+  const int64_t groups = (T + back_teams(d) - 1) / back_teams(d), most = team_waves(d) > kBackWaves ? 256 : 512;
+  return groups < most ? groups : most;
 }
 
 hipError_t launch_norm(const void* r, bool r_f32, const uint16_t* y, const void* w_post, const void* w_next,
@@ -444,11 +605,11 @@ hipError_t launch_norm_backward(const void* dr, const uint16_t* dn, const uint16
   NormArgs g{};
   g.r = r, g.y = y, g.w_post = w_post, g.w_next = w_next, g.gate = gate, g.gate_kind = gate_kind, g.w_f32 = w_f32;
   g.a = a, g.b = b, g.eps = eps, g.T = T, g.d = (int)d, g.r_out = dr_out, g.dr = dr, g.dn = dn, g.dn_add = dn_add, g.dy = dy;
-  g.d_gate_token = d_gate, g.partial = partial;
-  const int teams = (int)norm_partial_rows(T, d);
+  g.d_gate_token = d_gate, g.partial = partial, g.team_waves = team_waves(d);
+  const int groups = (int)norm_partial_rows(T, d);
   if (T > 0) {
-    const hipError_t e = r_f32 ? backward<float>(g, branch, post, next, teams, stream)
-                               : backward<uint16_t>(g, branch, post, next, teams, stream);
+    const hipError_t e = r_f32 ? backward<float>(g, branch, post, next, groups, stream)
+                               : backward<uint16_t>(g, branch, post, next, groups, stream);
     if (e != hipSuccess) return e;
   }
   ColumnSums o{};
@@ -460,7 +621,7 @@ hipError_t launch_norm_backward(const void* dr, const uint16_t* dn, const uint16
   for (int k = 0; k < cols; ++k) any = any || o.out[k] != nullptr;
   if (!any) return hipSuccess;
   hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((d + 63) / 64), cols), dim3(64 * kSumWaves), 0, stream, partial,
-                     teams, cols, (int)d, o);
+                     groups, cols, (int)d, o);
   return hipGetLastError();
 }
 

@@ -85,7 +85,7 @@ def test_norm_takes_what_its_flags_need(lib):
 def test_norm_workspace_bytes(lib):
     f = moe.norm_workspace_bytes
     assert f(0, 64) == 0 and f(-1, 64) == 0 and f(4, 12) == 0 and f(4, 16392) == 0
-    assert f(3, 64) == 3 * 64 * 12
+    assert f(1, 64) == 64 * 12 and f(1, 16384) == 16384 * 12  # one row of three sums
     assert f(2**31 - 1, 64) == f(10**6, 64)  # bounded however many rows
 
 
