@@ -12,8 +12,8 @@
 // v_mfma_f32_16x16x32_bf16: lane l brings 8 values of row l % 16, those of lane quarter l / 16. A
 // lane loads 16 bytes, 32 weights of one row; exchanging dwords between the four quarters makes step s of
 // four cover values 32 s .. 32 s + 31 of a unit of 128, so that groups of 32, 64 and 128 all end with
-// a step. The weights are the second operand, so a lane ends with one weight row and four tokens: it needs
-// one scale and one zero a group, which the quarters load one group each and then exchange.
+// a step. The weights are the second operand, so a lane ends with one weight row and four tokens of a product and
+// needs one scale and one zero a group, which the quarters load one group each and then exchange.
 
 #include <type_traits>
 
@@ -45,11 +45,12 @@ inline __host__ __device__ int64_t int4_row_bytes(int64_t K) { return 16 * ((K +
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __builtin_bit_cast(float, x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __builtin_bit_cast(float, x & 0xFFFF0000u); }
 
-// Eight weights of a dword as bf16 16 + q, in the order 0 4, 1 5, 2 6, 3 7.
-__device__ __forceinline__ bf16x8 unpack(uint32_t w) {
-  constexpr uint32_t kBits = 0x00780078u, kSixteen = 0x41804180u;
-  const u32x4 v = {((w << 3) & kBits) | kSixteen, ((w >> 1) & kBits) | kSixteen, ((w >> 5) & kBits) | kSixteen,
-                   ((w >> 9) & kBits) | kSixteen};
+// Eight weights of a dword as bf16 16 + q, in the order 0 4, 1 5, 2 6, 3 7: a shift and one and-or for two. (One operand
+// of an instruction may be a constant or a scalar register, so the other constant is kept in a vector register.)
+__device__ __forceinline__ bf16x8 unpack(uint32_t w, uint32_t sixteen) {
+  constexpr uint32_t kBits = 0x00780078u;
+  const u32x4 v = {((w << 3) & kBits) | sixteen, ((w >> 1) & kBits) | sixteen, ((w >> 5) & kBits) | sixteen,
+                   ((w >> 9) & kBits) | sixteen};
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -124,29 +125,40 @@ __device__ __forceinline__ void find_tile(const Finder& f, int E, uint32_t tile,
   begin = base + __builtin_amdgcn_readlane(mine, in);
 }
 
-// What a wave holds of one unit: 128 values of its weight rows and tokens, and the scale and zero of the group
-// that this lane's quarter has to load.
-template <int MB>
+// What a wave holds of one unit: 128 values of its 64 weight rows, and scales and zeros of the group that this lane's
+// quarter has to load. A lane's four rows lie next to each other (gated: two gate rows and the two up rows that go with
+// them), so one load brings their scales and one their zeros, and a lane ends with neighbouring columns.
 struct Unit {
-  u32x4 w[kBlocks], x[MB][4];
-  uint32_t s[kBlocks], z[kBlocks];
+  u32x4 w[kBlocks];
+  uint32_t s[2], z[2];
 };
 
-// A value that quarter j holds for group j of a unit (GS steps a group), as all lanes need it: out[j].
+// Scales (two a word) and zeros (a byte each) of a lane's four rows.
+struct Scales {
+  uint32_t s[2], z;
+};
+
+// The groups' scales from the quarters that loaded them: of `half` 0 for a unit's steps 0 and 1, of 1 for 2 and 3; out[j]
+// for the step's parity.
 template <int GS>
-__device__ __forceinline__ void spread_groups(uint32_t v, uint32_t (&out)[4 / GS]) {
-  if constexpr (GS == 4) {
-    out[0] = v;
-  } else {
-    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // halves, each in both
-    if constexpr (GS == 2) {
-      out[0] = h[0], out[1] = h[1];
+__device__ __forceinline__ void spread_scales(const Scales& v, int half, Scales (&out)[2]) {
+  auto one = [&](uint32_t x, uint32_t& a, uint32_t& b) {
+    if constexpr (GS == 4) {
+      a = b = x;
     } else {
-      const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-      const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-      out[0] = a[0], out[1] = a[1], out[2] = b[0], out[3] = b[1];
+      const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);  // the wave's halves, each in both
+      const uint32_t mine = half == 0 ? h[0] : h[1];
+      if constexpr (GS == 2) {
+        a = b = mine;
+      } else {
+        const auto q = __builtin_amdgcn_permlane16_swap(mine, mine, false, false);
+        a = q[0], b = q[1];
+      }
     }
-  }
+  };
+  one(v.s[0], out[0].s[0], out[1].s[0]);
+  one(v.s[1], out[0].s[1], out[1].s[1]);
+  one(v.z, out[0].z, out[1].z);
 }
 
 // A buffer resource of `bytes` from a uniform address on (2 GiB at most: offsets stay below).
@@ -156,20 +168,127 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, int
                                            __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
 
-// A tile: 16 MB rows by 64 weight rows (gated: 32 columns' gate and up rows), the contraction split into a
-// range of units for each of the four waves, whose sums are joined through LDS. GS: steps of a group.
+// The 64 weight rows of a wave, through buffer resources that end with the expert's: what lies behind reads as zeros.
+template <bool GATED, int GS>
+struct WeightRows {
+  static constexpr int kParts = GATED ? 2 : 1, kGroups = 4 / GS, kCols = GATED ? 32 : 64;
+  __amdgpu_buffer_rsrc_t w[kParts];
+  int64_t s0[kParts], s_left[kParts];  // first scale of the rows, scales from there to the expert's last
+  uint32_t w_off, s_off, row_bytes;
+
+  __device__ __forceinline__ void place(const Int4Args& g, int e, int64_t n0, int groups, int lane) {
+    const int quarter = lane >> 4, first = (lane & 15) * (GATED ? 2 : 4);
+    row_bytes = (uint32_t)int4_row_bytes(g.K);
+    w_off = first * row_bytes + quarter * 16;
+    s_off = (uint32_t)(quarter / GS) * (uint32_t)g.w_rows + first;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const int64_t r0 = n0 + p * g.N;
+      w[p] = resource(g.q + ((int64_t)e * g.w_rows + r0) * row_bytes, (g.w_rows - r0) * row_bytes);
+      s0[p] = uniform_i64((int64_t)e * groups * g.w_rows + r0);
+      s_left[p] = uniform_i64((int64_t)groups * g.w_rows - r0);
+    }
+  }
+
+  __device__ __forceinline__ void load(const Int4Args& g, Unit& d, int u) const {
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+      const uint32_t at = (GATED ? b & 1 : b) * row_bytes + (uint32_t)u * 64;
+      d.w[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w[GATED ? b >> 1 : 0], w_off, at, 0));
+    }
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const int64_t skip = (int64_t)u * kGroups * g.w_rows;
+      const auto sr = resource(g.scales + s0[p] + skip, (s_left[p] - skip) * 2);
+      const auto zr = resource(g.zeros + s0[p] + skip, g.zeros != nullptr ? s_left[p] - skip : 0);
+      if constexpr (GATED) {
+        d.s[p] = __builtin_amdgcn_raw_buffer_load_b32(sr, s_off * 2, 0, 0);
+        d.z[p] = __builtin_amdgcn_raw_buffer_load_b16(zr, s_off, 0, 0);
+      } else {
+        const auto s = __builtin_amdgcn_raw_buffer_load_b64(sr, s_off * 2, 0, 0);
+        d.s[0] = s[0], d.s[1] = s[1];
+        d.z[0] = __builtin_amdgcn_raw_buffer_load_b32(zr, s_off, 0, 0), d.z[1] = 0;
+      }
+    }
+  }
+};
+
+// sum += s (q - z) x over one unit. tokens(m, s): the 8 values of this lane for step s, in the weights' order.
+template <bool GATED, int MB, int GS, class Tokens>
+__device__ __forceinline__ void multiply_unit(Unit& d, uint32_t no_zeros, const bf16x8& ones, Tokens tokens,
+                                              f32x4_t (&sum)[kBlocks][MB]) {
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) transpose_quarters(d.w[b]);
+  const Scales mine = {{d.s[0], d.s[1]}, (GATED ? d.z[0] | d.z[1] << 16 : d.z[0]) | no_zeros};
+  Scales sc[2];
+  uint32_t sixteen = 0x41804180u;
+  asm volatile("" : "+v"(sixteen));
+  f32x4_t acc[kBlocks][MB], xs[MB];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if (s % 2 == 0 && (s == 0 || GS < 4)) spread_scales<GS>(mine, s / 2, sc);
+    bf16x8 xv[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xv[m] = tokens(m, s);
+    if (s % GS == 0) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        xs[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) acc[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], ones, xs[m], 0, 0, 0);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+      const bf16x8 wv = unpack(d.w[b][s], sixteen);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], wv, acc[b][m], 0, 0, 0);
+    }
+    if (s % GS == GS - 1) {
+      const Scales& now = sc[s & 1];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const float scale = b & 1 ? bf16_hi(now.s[b >> 1]) : bf16_lo(now.s[b >> 1]);
+        const float c = 16.0f + (float)((now.z >> (8 * b)) & 0xFFu);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum[b][m][r] = fmaf(scale, fmaf(-c, xs[m][r], acc[b][m][r]), sum[b][m][r]);
+          asm volatile("" : "+v"(sum[b][m]));  // added here: put off to the next unit, it would hold all of acc
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // (a step's operands at a time: unpacked early, they would fill the registers)
+  }
+}
+
+// A lane's columns of one token: four (gated: SiLU(v0) v2 and SiLU(v1) v3) from column `col` on.
+template <bool GATED>
+__device__ __forceinline__ void store_columns(const Int4Args& g, int64_t row, int64_t col, const f32x4_t& v) {
+  if (col >= g.N) return;
+  if constexpr (GATED) {
+    float h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) h[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * v[i + 2];
+    *reinterpret_cast<uint32_t*>(g.out + row * g.N + col) = pack_bf16x2(h[0], h[1]);
+  } else {
+    *reinterpret_cast<u32x2_t*>(g.out + row * g.N + col) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+}
+
+// Few rows an expert: tiles of 16 rows by 64 weight rows, the contraction split into a range of units for each of the
+// four waves, whose sums are joined through LDS. GS: steps of a group.
 //
 // What a call of few rows waits for is the chain offsets, tile, loads, join, so all of a unit's loads (weights,
 // scales, zeros, tokens) go out together, the tile is found without a barrier, and as many waves are resident
-// as the registers allow: four workgroups a CU (three with 32 rows). Measured: gate/up of 4 tokens, 32 of 128
-// experts of 2 x 768 x 2048, groups of 64 19.1 us, the projection of the same tokens 11.1 us. Tried: scales read
-// when a group ends 24.1 and 13.8 us; two units in flight a wave, which leaves three workgroups a CU, 18.8 and
-// 19.4 us, the same at four workgroups with spilled registers 28.6 and 22.7 us.
-template <bool GATED, int MB, int GS>
-__global__ __launch_bounds__(kThreads, MB == 1 ? 4 : 3) void int4_kernel(Int4Args g) {
-  constexpr int BM = 16 * MB, kCols = GATED ? 32 : 64, kGroups = 4 / GS;
+// as the registers allow: four workgroups a CU.
+template <bool GATED, int GS>
+__global__ __launch_bounds__(kThreads, 4) void int4_kernel(Int4Args g) {
+  constexpr int BM = 16, kCols = GATED ? 32 : 64;
   __shared__ int offs[MOE_MAX_EXPERTS + 1], prefix[MOE_MAX_EXPERTS];
-  __shared__ __align__(16) float red[kWaves][kBlocks][MB][256];
+  __shared__ f32x4_t red[kWaves][4][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int quarter = lane >> 4, r16 = lane & 15;
@@ -178,9 +297,8 @@ __global__ __launch_bounds__(kThreads, MB == 1 ? 4 : 3) void int4_kernel(Int4Arg
   const int n_tiles = (int)((g.N + kCols - 1) / kCols);
   const int64_t total = (int64_t)find.total * n_tiles;
   const int K = (int)g.K;
-  const uint32_t row_bytes = (uint32_t)int4_row_bytes(g.K);
+  const uint32_t no_zeros = g.zeros != nullptr ? 0u : 0x08080808u;
   const int units = (K + kUnit - 1) / kUnit;
-  const uint32_t no_zeros = g.zeros != nullptr ? 0u : 8u << 16;
   const int u_lo = units * wave / kWaves, u_hi = units * (wave + 1) / kWaves;
   const int groups = (K + 32 * GS - 1) / (32 * GS);
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
@@ -196,159 +314,155 @@ __global__ __launch_bounds__(kThreads, MB == 1 ? 4 : 3) void int4_kernel(Int4Arg
     if (row0 < lo || row0 >= hi) continue;  // wrapped counts
     const int valid = (int)(hi - row0 < BM ? hi - row0 : BM);
 
-    // Tokens past the last repeat the first, weight rows past the last read as zeros or as what stands there;
-    // neither is stored.
-    const uint16_t* xr[MB];
+    // tokens past the last repeat the first, they are not stored
+    int64_t row = row0 + (r16 < valid ? r16 : 0);
+    if (g.perm != nullptr) row = clamp_row((int64_t)g.perm[row] / g.k, g.tokens - 1);
+    const uint16_t* xr = g.x + row * g.K;
+    WeightRows<GATED, GS> rows;
+    rows.place(g, e, n0, groups, lane);
+    f32x4_t sum[kBlocks][1];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) sum[b][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int u = u_lo; u < u_hi; ++u) {
+      Unit unit;
+      rows.load(g, unit, u);
+      u32x4 x[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int k = u * kUnit + s * 32 + quarter * 8;  // (behind the row's end: its last values, multiplied as zeros)
+        x[s] = *reinterpret_cast<const u32x4*>(xr + (k < K ? k : K - 8));
+      }
+      multiply_unit<GATED, 1, GS>(unit, no_zeros, ones, [&](int, int s) {
+        return pair_up(u * kUnit + s * 32 + quarter * 8 < K ? x[s] : u32x4{0u, 0u, 0u, 0u});
+      }, sum);
+    }
+    // Join the waves' parts: value r of a lane is token 4 (l / 16) + r; wave r adds those of all waves.
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[wave][r][lane] = f32x4_t{sum[0][0][r], sum[1][0][r], sum[2][0][r], sum[3][0][r]};
+    __syncthreads();
+    f32x4_t v = red[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += red[w][wave][lane];
+    const int t = quarter * 4 + wave;
+    if (t < valid) store_columns<GATED>(g, row0 + t, n0 + r16 * (kCols / 16), v);
+    __syncthreads();
+  }
+}
+
+// More rows an expert: tiles of 16 MB rows by 256 weight rows (gated: 128 columns' gate and up rows), 64 for each of the
+// four waves over the whole contraction. The tokens' values go through LDS, one unit ahead, already in the weights' order;
+// the weights, scales and zeros of a unit are loaded while the one before is multiplied.
+template <bool GATED, int MB, int GS>
+__global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(Int4Args g) {
+  constexpr int BM = 16 * MB, kWaveCols = GATED ? 32 : 64, kCols = kWaves * kWaveCols;
+  __shared__ int offs[MOE_MAX_EXPERTS + 1], prefix[MOE_MAX_EXPERTS];
+  // Token row t's 16-byte piece c stands at c ^ (t % 16): 16 rows' pieces of one c cover all banks.
+  __shared__ u32x4 tokens[2][BM][16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int quarter = lane >> 4, r16 = lane & 15;
+  const Finder find = find_setup<BM>(g.offsets, g.E, g.cap_rows, offs, prefix, lane);
+  const int n_tiles = (int)((g.N + kCols - 1) / kCols);
+  const int64_t total = (int64_t)find.total * n_tiles;
+  const int K = (int)g.K;
+  const uint32_t no_zeros = g.zeros != nullptr ? 0u : 0x08080808u;
+  const int units = (K + kUnit - 1) / kUnit;
+  const int groups = (K + 32 * GS - 1) / (32 * GS);
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  const int piece = tid & 15, slot = tid >> 4;  // of a token row, and which of 16 rows
+
+  for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    const uint32_t gm = (uint32_t)(tile / n_tiles);
+    const int64_t n0 = (tile - (int64_t)gm * n_tiles) * kCols + wave * kWaveCols;
+    int e;
+    uint32_t begin;
+    find_tile(find, g.E, gm, lane, e, begin);
+    const int64_t lo = offs[e], hi = offs[e + 1];
+    const int64_t row0 = lo + (int64_t)(gm - begin) * BM;
+    if (row0 < lo || row0 >= hi) continue;  // wrapped counts
+    const int valid = (int)(hi - row0 < BM ? hi - row0 : BM);
+
+    const uint16_t* xr[MB];  // (tokens past the last repeat the first, they are not stored)
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
-      const int t = m * 16 + r16;
+      const int t = m * 16 + slot;
       int64_t row = row0 + (t < valid ? t : 0);
       if (g.perm != nullptr) row = clamp_row((int64_t)g.perm[row] / g.k, g.tokens - 1);
       xr[m] = g.x + row * g.K;
     }
-    // Everything of the experts is read through buffer resources that end with the expert's rows: what lies
-    // behind reads as zeros.
-    constexpr int kParts = GATED ? 2 : 1;
-    __amdgpu_buffer_rsrc_t wr[kParts];
-    int64_t s0[kParts], s_left[kParts];  // first scale of the tile's rows, scales from there to the expert's last
-    const uint32_t w_off = (uint32_t)r16 * row_bytes + quarter * 16;
-    const uint32_t s_off = (uint32_t)(quarter / GS) * (uint32_t)g.w_rows + r16;
-#pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      const int64_t r0 = n0 + p * g.N;
-      wr[p] = resource(g.q + ((int64_t)e * g.w_rows + r0) * row_bytes, (g.w_rows - r0) * row_bytes);
-      s0[p] = uniform_i64((int64_t)e * groups * g.w_rows + r0);
-      s_left[p] = uniform_i64((int64_t)groups * g.w_rows - r0);
-    }
+    WeightRows<GATED, GS> rows;
+    rows.place(g, e, n0, groups, lane);
 
-    auto load = [&](Unit<MB>& d, int u) {
+    u32x4 next[MB];
+    auto read_tokens = [&](int u) {
+      const int k = u * kUnit + piece * 8;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const uint32_t at = w_off + (GATED ? b & 1 : b) * 16 * row_bytes + (uint32_t)u * 64;
-        d.w[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr[GATED ? b >> 1 : 0], at, 0, 0));
-      }
-#pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        const int64_t skip = (int64_t)u * kGroups * g.w_rows;
-        const auto sr = resource(g.scales + s0[p] + skip, (s_left[p] - skip) * 2);
-        const auto zr = resource(g.zeros + s0[p] + skip, g.zeros != nullptr ? s_left[p] - skip : 0);
-#pragma unroll
-        for (int c = 0; c < kBlocks / kParts; ++c) {
-          const int b = p * (kBlocks / kParts) + c;
-          d.s[b] = __builtin_amdgcn_raw_buffer_load_b16(sr, (s_off + c * 16) * 2, 0, 0);
-          d.z[b] = __builtin_amdgcn_raw_buffer_load_b8(zr, s_off + c * 16, 0, 0);
-        }
-      }
+      for (int m = 0; m < MB; ++m) next[m] = *reinterpret_cast<const u32x4*>(xr[m] + (k < K ? k : K - 8));
+    };
+    auto keep_tokens = [&](int u) {
+      const bool in = u * kUnit + piece * 8 < K;
 #pragma unroll
       for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int k = u * kUnit + s * 32 + quarter * 8;  // (behind the row's end: its last values, multiplied as zeros)
-          d.x[m][s] = *reinterpret_cast<const u32x4*>(xr[m] + (k < K ? k : K - 8));
-        }
+        tokens[u & 1][m * 16 + slot][piece ^ slot] = __builtin_bit_cast(u32x4, pair_up(in ? next[m] : u32x4{0u, 0u, 0u, 0u}));
     };
-
     f32x4_t sum[kBlocks][MB];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
       for (int m = 0; m < MB; ++m) sum[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    auto multiply = [&](Unit<MB>& d, int u) {
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) transpose_quarters(d.w[b]);
-      uint32_t sz[kBlocks][kGroups];  // scale in the low half, zero above
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) spread_groups<GS>(d.s[b] | d.z[b] << 16 | no_zeros, sz[b]);
-      f32x4_t acc[kBlocks][MB], xs[MB];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        bf16x8 xv[MB];
-        const bool in = u * kUnit + s * 32 + quarter * 8 < K;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) xv[m] = pair_up(in ? d.x[m][s] : u32x4{0u, 0u, 0u, 0u});
-        if (s % GS == 0) {
-#pragma unroll
-          for (int m = 0; m < MB; ++m) {
-            xs[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) acc[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < MB; ++m) xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], ones, xs[m], 0, 0, 0);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const bf16x8 wv = unpack(d.w[b][s]);
-#pragma unroll
-          for (int m = 0; m < MB; ++m) acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], wv, acc[b][m], 0, 0, 0);
-        }
-        if (s % GS == GS - 1) {
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b) {
-            const float scale = bf16_lo(sz[b][s / GS]), c = 16.0f + (float)(sz[b][s / GS] >> 16);
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) sum[b][m][r] = fmaf(scale, fmaf(-c, xs[m][r], acc[b][m][r]), sum[b][m][r]);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // (a step's operands at a time: unpacked early, they would fill the registers)
-      }
+    auto multiply = [&](Unit& d, int u) {
+      multiply_unit<GATED, MB, GS>(d, no_zeros, ones, [&](int m, int s) {
+        return __builtin_bit_cast(bf16x8, tokens[u & 1][m * 16 + r16][(s * 4 + quarter) ^ r16]);
+      }, sum);
     };
 
-    for (int u = u_lo; u < u_hi; ++u) {
-      Unit<MB> unit;
-      load(unit, u);
-      multiply(unit, u);
+    Unit even, odd;
+    read_tokens(0);
+    rows.load(g, even, 0);
+    keep_tokens(0);
+    lds_barrier();
+    for (int u = 0;;) {
+      bool more = u + 1 < units;
+      if (more) read_tokens(u + 1), rows.load(g, odd, u + 1);
+      multiply(even, u);
+      if (!more) break;
+      keep_tokens(++u);
+      lds_barrier();  // unit u is there, and the area of u - 1 is free
+      more = u + 1 < units;
+      if (more) read_tokens(u + 1), rows.load(g, even, u + 1);
+      multiply(odd, u);
+      if (!more) break;
+      keep_tokens(++u);
+      lds_barrier();
     }
-    // Join the waves' parts: value r of lane l is token 4 (l / 16) + r and weight row l % 16, kept at 64 r + l, so
-    // that lane l reads four consecutive columns of one token.
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][b][m][64 * r + lane] = sum[b][m][r];
-    __syncthreads();
-    auto joined = [&](int b, int m) {
-      f32x4_t v = *reinterpret_cast<const f32x4_t*>(&red[0][b][m][4 * lane]);
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&red[w][b][m][4 * lane]);
-      return v;
-    };
-    constexpr int kItems = (GATED ? 2 : 4) * MB;  // blocks of 16 tokens by 16 columns
-    for (int i = wave; i < kItems; i += kWaves) {
-      const int b = i / MB, m = i % MB;
-      f32x4_t v = joined(b, m);
-      if constexpr (GATED) {
-        const f32x4_t up = joined(b + 2, m);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = v[r] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[r])) * up[r];
+      for (int r = 0; r < 4; ++r) {
+        const int t = m * 16 + quarter * 4 + r;
+        if (t < valid)
+          store_columns<GATED>(g, row0 + t, n0 + r16 * (kWaveCols / 16),
+                               f32x4_t{sum[0][m][r], sum[1][m][r], sum[2][m][r], sum[3][m][r]});
       }
-      const int t = m * 16 + (lane >> 2 & 3) * 4 + (lane >> 4);
-      const int64_t col = n0 + b * 16 + (lane & 3) * 4;
-      if (t < valid && col < g.N)
-        *reinterpret_cast<u32x2_t*>(g.out + (row0 + t) * g.N + col) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    }
-    __syncthreads();
+    lds_barrier();  // (the tokens' last reads, before the next tile's)
   }
 }
 
-template <bool GATED, int MB, int GS>
-hipError_t launch_tiles(const Int4Args& g, hipStream_t stream) {
-  constexpr int BM = 16 * MB;
-  const int64_t n_tiles = (g.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64);
+template <class Kernel>
+hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, int resident, hipStream_t stream) {
   const int64_t most_experts = g.cap_rows < g.E ? g.cap_rows : g.E;
-  const int64_t tiles = (g.cap_rows / BM + most_experts) * n_tiles;
-  const int64_t fit = (int64_t)device_cu_count(current_device()) * (MB == 1 ? 4 : 3);
-  hipLaunchKernelGGL((int4_kernel<GATED, MB, GS>), dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), 0, stream, g);
+  const int64_t tiles = (g.cap_rows / rows + most_experts) * ((g.N + cols - 1) / cols);
+  const int64_t fit = (int64_t)device_cu_count(current_device()) * resident;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
 template <bool GATED, int GS>
 hipError_t launch_rows(const Int4Args& g, hipStream_t stream) {
-  return g.cap_rows <= 16 * (int64_t)g.E ? launch_tiles<GATED, 1, GS>(g, stream) : launch_tiles<GATED, 2, GS>(g, stream);
+  constexpr int kOut = GATED ? 32 : 64;
+  if (g.cap_rows <= 16 * (int64_t)g.E) return launch_tiles(int4_kernel<GATED, GS>, g, 16, kOut, 4, stream);
+  if (g.cap_rows <= 48 * (int64_t)g.E) return launch_tiles(int4_wide_kernel<GATED, 2, GS>, g, 32, 4 * kOut, 3, stream);
+  return launch_tiles(int4_wide_kernel<GATED, 4, GS>, g, 64, 4 * kOut, 2, stream);
 }
 
 template <bool GATED>
