@@ -621,8 +621,8 @@ moe_status moe_adamw_moments(const uint8_t* m, const uint8_t* m_scales, const ui
 /* ---------------------------------------------------------------------------
  * Expert weights in 4 bits with group scales, W = s (q - z), and the grouped
  * products of bf16 rows with them: for decode, a few rows an expert, where
- * reading the weights is the work. For many rows an expert read the weights back
- * to bf16 and use the bf16 calls.
+ * reading the weights is the work. From about 200 rows an expert on the bf16 calls
+ * are faster, on weights read back to bf16.
  *
  *   q       uint8 [E, d_out, 16 * ceil(d_in / 32)]  value 2i in the low half of byte i,
  *                                                   16-byte aligned; what stands behind

@@ -849,7 +849,7 @@ def moe_int4_dequantize_weights(m: Int4, *, w=None) -> torch.Tensor:
 
 def moe_grouped_projection_int4(x: torch.Tensor, offsets: torch.Tensor, w: Int4, *, y=None) -> torch.Tensor:
     """Y[rows_e] = bf16(X[rows_e] @ W_e^T) of bf16 rows [cap, d_in] and 4-bit weights [E, d_out, d_in] (one launch).
-    Made for few rows an expert; for many, moe_int4_dequantize_weights and moe_grouped_projection are faster."""
+    From about 200 rows an expert on, moe_int4_dequantize_weights and moe_grouped_projection are faster."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be [cap_rows, d_in]")
     dev = x.device

@@ -283,7 +283,11 @@ __device__ __forceinline__ void store_columns(const Int4Args& g, int64_t row, in
 //
 // What a call of few rows waits for is the chain offsets, tile, loads, join, so all of a unit's loads (weights,
 // scales, zeros, tokens) go out together, the tile is found without a barrier, and as many waves are resident
-// as the registers allow: four workgroups a CU.
+// as the registers allow: four workgroups a CU. Measured: gate/up of 4 tokens, 32 of 128 experts of 2 x 768 x 2048
+// in groups of 64 (53 MB) 16.4 us, the projection of the same tokens (27 MB) 10.3 us. Tried: the scales loaded when
+// a group ends 24.1 and 13.8 us; a lane's rows 16 apart, so eight loads of scales and zeros and a join by columns,
+// 18.2 and 10.6 us; the next unit's weights loaded before the products of this one 26.5 and 13.3 us (the registers
+// for them spill, and loads return in order, so a spilled value waits for them too).
 template <bool GATED, int GS>
 __global__ __launch_bounds__(kThreads, 4) void int4_kernel(Int4Args g) {
   constexpr int BM = 16, kCols = GATED ? 32 : 64;
@@ -350,8 +354,10 @@ __global__ __launch_bounds__(kThreads, 4) void int4_kernel(Int4Args g) {
 }
 
 // More rows an expert: tiles of 16 MB rows by 256 weight rows (gated: 128 columns' gate and up rows), 64 for each of the
-// four waves over the whole contraction. The tokens' values go through LDS, one unit ahead, already in the weights' order;
-// the weights, scales and zeros of a unit are loaded while the one before is multiplied.
+// four waves over the whole contraction. The tokens' values go through LDS, one unit ahead, already in the weights' order.
+// Bound by unpacking (267 vector operations a unit and wave, 40 matrix instructions) and by how evenly the tiles fall on
+// the CUs. Measured: gate/up of 256 tokens, top-8 of 64 experts, skewed, 2048 -> 2 x 768 49 us (with the narrow
+// tiles 57; with the next unit's weights loaded ahead 55 us, two workgroups a CU and no spilled registers 58).
 template <bool GATED, int MB, int GS>
 __global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(Int4Args g) {
   constexpr int BM = 16 * MB, kWaveCols = GATED ? 32 : 64, kCols = kWaves * kWaveCols;
@@ -416,24 +422,14 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(In
       }, sum);
     };
 
-    Unit even, odd;
     read_tokens(0);
-    rows.load(g, even, 0);
-    keep_tokens(0);
-    lds_barrier();
-    for (int u = 0;;) {
-      bool more = u + 1 < units;
-      if (more) read_tokens(u + 1), rows.load(g, odd, u + 1);
-      multiply(even, u);
-      if (!more) break;
-      keep_tokens(++u);
+    for (int u = 0; u < units; ++u) {
+      Unit unit;
+      rows.load(g, unit, u);
+      keep_tokens(u);
       lds_barrier();  // unit u is there, and the area of u - 1 is free
-      more = u + 1 < units;
-      if (more) read_tokens(u + 1), rows.load(g, even, u + 1);
-      multiply(odd, u);
-      if (!more) break;
-      keep_tokens(++u);
-      lds_barrier();
+      if (u + 1 < units) read_tokens(u + 1);
+      multiply(unit, u);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m)
@@ -457,6 +453,9 @@ hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, in
   return hipGetLastError();
 }
 
+// By the mean of the rows per expert that the call has room for. us for 64 experts of 2048 -> 2 x 768 with 16, 32, 64
+// and 128 rows each: narrow 34, 54, 101, 191; 32 rows 38, 39, 61, 123; 64 rows -, -, 56, 90. From about 200 rows on
+// the bf16 launch on weights read back is faster (256 rows 138 against 168 us).
 template <bool GATED, int GS>
 hipError_t launch_rows(const Int4Args& g, hipStream_t stream) {
   constexpr int kOut = GATED ? 32 : 64;
