@@ -12,6 +12,7 @@ every call raises ImportError when it is missing. There is no other code path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass, field
@@ -915,21 +916,24 @@ def _stream_rows(r: torch.Tensor, name: str):
     if code is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {r.dtype}")
     T, d = r.shape
-    _want(r, name, r.dtype, (T, d), r.device)
-    return T, d, code, r.device
+    dev = r.device
+    _want(r, name, r.dtype, (T, d), dev)
+    return T, d, code, dev
 
 
-def _norm_weights(d: int, dev, **weights) -> int:
-    """dtype code of the weights that are given, all of one dtype."""
-    dtype = None
-    for name, w in weights.items():
+def _norm_weights(shape: tuple, dev, *weights) -> int:
+    """dtype code of the (weight, name) pairs whose weight is given, all of one dtype."""
+    dtype = code = None
+    for w, name in weights:
         if w is None:
             continue
-        if not isinstance(w, torch.Tensor) or w.dtype not in _LOGITS:
-            raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
-        dtype = dtype or w.dtype
-        _want(w, name, dtype, (d,), dev)
-    return _LOGITS[dtype or torch.bfloat16]
+        if code is None:
+            dtype = w.dtype if isinstance(w, _Tensor) else None
+            code = _LOGITS.get(dtype)
+            if code is None:
+                raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+        _want(w, name, dtype, shape, dev)
+    return code or 0
 
 
 def _norm_gate(gate, T: int, d: int, dev):
@@ -942,6 +946,7 @@ def _norm_gate(gate, T: int, d: int, dev):
     return _GATE_CHANNEL, gate
 
 
+@functools.lru_cache(maxsize=256)
 def norm_workspace_bytes(T: int, d: int) -> int:
     return int(load_library().moe_norm_workspace_bytes(T, d))
 
@@ -957,7 +962,7 @@ def _norm_workspace(workspace, T: int, d: int, dev):
 def moe_rmsnorm(x: torch.Tensor, w: torch.Tensor | None = None, *, eps: float = 1e-6, y=None) -> torch.Tensor:
     """The norm before a block: bf16 rows x / sqrt(mean(x^2) + eps) * w of the stream's bf16 or fp32 rows (one launch)."""
     T, d, dtype, dev = _stream_rows(x, "x")
-    w_dtype = _norm_weights(d, dev, w=w)
+    w_dtype = _norm_weights((d,), dev, (w, "w"))
     y = _out(y, "y", torch.bfloat16, (T, d), dev)
     _check(load_library().moe_rmsnorm(x.data_ptr(), dtype, _ptr(w), w_dtype, eps, T, d, y.data_ptr(), _stream(x)),
            "moe_rmsnorm")
@@ -969,7 +974,7 @@ def moe_rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor | No
     """(dx, dw) of moe_rmsnorm: dx in the stream's type with ``dx_add``, the gradient that reaches x past the norm,
     added; dw fp32, None without a weight (two launches). ``dy_add`` is a second part of y's gradient."""
     T, d, dtype, dev = _stream_rows(x, "x")
-    w_dtype = _norm_weights(d, dev, w=w)
+    w_dtype = _norm_weights((d,), dev, (w, "w"))
     _want(dy, "dy", torch.bfloat16, (T, d), dev)
     if dy_add is not None:
         _want(dy_add, "dy_add", torch.bfloat16, (T, d), dev)
@@ -995,7 +1000,7 @@ def moe_residual_norm(y: torch.Tensor, r: torch.Tensor, *, post_norm: bool = Fal
     kind, channel = _norm_gate(gate, T, d, dev)
     if (w_post is not None and not post_norm) or (w_next is not None and not next_norm):
         raise ValueError("a weight of a norm that is not asked for")
-    w_dtype = _norm_weights(d, dev, w_post=w_post, w_next=w_next, gate=channel)
+    w_dtype = _norm_weights((d,), dev, (w_post, "w_post"), (w_next, "w_next"), (channel, "gate"))
     r_out = _out(r_out, "r_out", r.dtype, (T, d), dev)
     n_out = _out(n_out, "n_out", torch.bfloat16, (T, d), dev) if next_norm else None
     flags = (_NORM_POST if post_norm else 0) | (_NORM_NEXT if next_norm else 0)
@@ -1026,7 +1031,7 @@ def moe_residual_norm_backward(d_r_out: torch.Tensor | None, d_n: torch.Tensor |
     kind, channel = _norm_gate(gate, T, d, dev)
     if (w_post is not None and not post_norm) or (w_next is not None and not next_norm):
         raise ValueError("a weight of a norm that is not asked for")
-    w_dtype = _norm_weights(d, dev, w_post=w_post, w_next=w_next, gate=channel)
+    w_dtype = _norm_weights((d,), dev, (w_post, "w_post"), (w_next, "w_next"), (channel, "gate"))
     if d_r_out is not None:
         _want(d_r_out, "d_r_out", r_out.dtype, (T, d), dev)
     elif not next_norm:

@@ -471,104 +471,232 @@ hipError_t launch_product(const Int4Args& g, int group, hipStream_t stream) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rounding weights to 4 bits and reading them back: once, when weights are loaded.
+// Rounding weights to 4 bits, once, when they are loaded, and reading them back, for calls of many rows. Bound by HBM
+// and the exact quotients: 64 x 1536 x 2048 (503 MB read and written, 102 us at a copy's rate) 193 us, with the
+// contraction outermost 205 us in groups of 32 and 314 in groups of 128; back 89 us.
 // ------------------------------------------------------------------------------------------------
 
-// A group's scale (rounded to bf16 first, the values are rounded against what is stored) and zero.
-__device__ __forceinline__ uint16_t group_scale(float lo, float hi, bool bad, bool symmetric, float& divisor, float& zero) {
+// A group's scale (rounded to bf16 first, the values are rounded against what is stored), the divisor (1 for a scale
+// of 0) and the zero.
+struct GroupCode {
+  uint16_t scale;
+  float divisor, zero;
+  bool bad;
+};
+
+__device__ __forceinline__ GroupCode group_code(float lo, float hi, bool bad, bool symmetric) {
+  GroupCode c;
+  c.bad = bad || !(hi - lo < __builtin_inff());
   const float range = symmetric ? fmaxf(-lo, hi) / 7.0f : (hi - lo) / 15.0f;
-  const uint16_t s = bad ? (uint16_t)0x7FC0u : f32_to_bf16_bits(range);
-  const float f = bf16_bits_to_f32(s);
-  divisor = f > 0.0f && f < __builtin_inff() ? f : 1.0f;
-  zero = symmetric ? 8.0f : (bad ? 0.0f : fminf(fmaxf(rintf(-lo / divisor), 0.0f), 15.0f));
-  return s;
+  c.scale = c.bad ? (uint16_t)0x7FC0u : f32_to_bf16_bits(range);
+  const float f = bf16_bits_to_f32(c.scale);
+  c.divisor = f > 0.0f && f < __builtin_inff() ? f : 1.0f;
+  c.zero = symmetric ? 8.0f : (c.bad ? 0.0f : fminf(fmaxf(rintf(-lo / c.divisor), 0.0f), 15.0f));
+  return c;
 }
 
-__device__ __forceinline__ uint32_t code(float w, float divisor, float zero, bool bad) {
-  return bad ? 8u : (uint32_t)fminf(fmaxf(rintf(w / divisor) + zero, 0.0f), 15.0f);
+__device__ __forceinline__ uint32_t code_of(float w, const GroupCode& c) {
+  return c.bad ? 8u : (uint32_t)fminf(fmaxf(rintf(w / c.divisor) + c.zero, 0.0f), 15.0f);
 }
 
-// One thread a group of one row. `sk` and `sn`: pitches of the contraction and of the rows.
-template <bool ROWS>
-__global__ __launch_bounds__(kThreads) void int4_quantize_kernel(const uint16_t* __restrict__ w, int64_t N, int64_t K,
-                                                                 int E, int group, bool symmetric,
-                                                                 uint8_t* __restrict__ q, uint16_t* __restrict__ scales,
-                                                                 uint8_t* __restrict__ zeros) {
+template <int CTRL>
+__device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_mov_dpp(x, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ void join_lanes(float& lo, float& hi, int& bad) {
+  lo = fminf(lo, __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, lo))));
+  hi = fmaxf(hi, __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, hi))));
+  bad |= dpp<CTRL>(bad);
+}
+
+// A workgroup's tile of stored weights: 32 rows by 512 values, a row to a wave at a time, 8 values a lane, so every
+// access is whole lines; the scales and zeros, whose rows run the other way, go through LDS.
+constexpr int kTileRows = 32, kTileK = 512, kTileGroups = kTileK / 32;
+struct RowTile {
+  int64_t e, n0, k0;
+};
+__device__ __forceinline__ RowTile row_tile(int64_t i, int64_t n_tiles, int64_t k_tiles) {
+  const int64_t rest = i / k_tiles;
+  return {rest / n_tiles, rest % n_tiles * kTileRows, i % k_tiles * kTileK};
+}
+
+__global__ __launch_bounds__(kThreads) void int4_quantize_rows_kernel(const uint16_t* __restrict__ w, int64_t N, int64_t K,
+                                                                      int64_t E, int group, bool symmetric,
+                                                                      uint8_t* __restrict__ q,
+                                                                      uint16_t* __restrict__ scales,
+                                                                      uint8_t* __restrict__ zeros) {
+  __shared__ uint16_t s_tile[kTileGroups][kTileRows];
+  __shared__ uint8_t z_tile[kTileGroups][kTileRows];
   const int64_t groups = (K + group - 1) / group, row_bytes = int4_row_bytes(K);
-  const int64_t sk = ROWS ? 1 : N, sn = ROWS ? K : 1;
-  const int64_t total = (int64_t)E * groups * N;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t n = i % N, gi = i / N % groups, e = i / (N * groups);
-    const int64_t k0 = gi * group, k1 = k0 + group < K ? k0 + group : K;
-    const uint16_t* p = w + e * N * K + n * sn;
-    float lo = 0.0f, hi = 0.0f;
-    bool bad = false;
-    for (int64_t k = k0; k < k1; ++k) {
-      const float v = bf16_bits_to_f32(p[k * sk]);
-      lo = fminf(lo, v), hi = fmaxf(hi, v);
-      bad = bad || !(fabsf(v) < __builtin_inff());
-    }
-    bad = bad || !(hi - lo < __builtin_inff());
-    float divisor, zero;
-    scales[i] = group_scale(lo, hi, bad, symmetric, divisor, zero);
-    if (!symmetric) zeros[i] = (uint8_t)zero;
-    uint8_t* out = q + (e * N + n) * row_bytes;
-    // whole 16 bytes, zeros behind the last value
-    for (int64_t k = k0; k < k1; k += 32) {
-      u32x4 o = {0u, 0u, 0u, 0u};
+  const int64_t n_tiles = (N + kTileRows - 1) / kTileRows, k_tiles = (K + kTileK - 1) / kTileK;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = group / 8;  // lanes of a group
+  for (int64_t i = blockIdx.x; i < E * n_tiles * k_tiles; i += gridDim.x) {
+    const RowTile t = row_tile(i, n_tiles, k_tiles);
+    const int64_t k = t.k0 + lane * 8;
+    for (int r = wave; r < kTileRows && t.n0 + r < N; r += kWaves) {
+      const int64_t row = t.e * N + t.n0 + r;
+      float v[8];
+      u32x4 x = {0u, 0u, 0u, 0u};
+      if (k < K) x = *reinterpret_cast<const u32x4*>(w + row * K + k);
+      float lo = 0.0f, hi = 0.0f;
+      int bad = 0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (k + j < k1) o[j >> 3] |= code(bf16_bits_to_f32(p[(k + j) * sk]), divisor, zero, bad) << (4 * (j & 7));
+      for (int j = 0; j < 8; ++j) {
+        v[j] = j & 1 ? bf16_hi(x[j >> 1]) : bf16_lo(x[j >> 1]);
+        lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
+        bad |= !(fabsf(v[j]) < __builtin_inff());
       }
-      *reinterpret_cast<u32x4*>(out + k / 2) = o;
+      join_lanes<0xB1>(lo, hi, bad);
+      join_lanes<0x4E>(lo, hi, bad);
+      if (per > 4) join_lanes<0x141>(lo, hi, bad);
+      if (per > 8) join_lanes<0x140>(lo, hi, bad);
+      const GroupCode c = group_code(lo, hi, bad != 0, symmetric);
+      uint32_t o = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o |= code_of(v[j], c) << (4 * j);
+      // whole 16 bytes, zeros behind the last value
+      if (k / 2 < row_bytes) *reinterpret_cast<uint32_t*>(q + row * row_bytes + k / 2) = k < K ? o : 0u;
+      if (lane % per == 0) s_tile[lane / per][r] = c.scale, z_tile[lane / per][r] = (uint8_t)c.zero;
     }
+    __syncthreads();
+    for (int j = threadIdx.x; j < kTileK / group * kTileRows; j += kThreads) {
+      const int gi = j / kTileRows, r = j % kTileRows;
+      const int64_t g = t.k0 / group + gi;
+      if (g < groups && t.n0 + r < N) {
+        const int64_t at = (t.e * groups + g) * N + t.n0 + r;
+        scales[at] = s_tile[gi][r];
+        if (!symmetric) zeros[at] = z_tile[gi][r];
+      }
+    }
+    __syncthreads();
   }
 }
 
-// bf16 [E, N, K] of packed weights, 8 values a thread.
+// Weights with the contraction outermost: a thread holds a group of two neighbouring columns, whose values it reads once.
+template <int GROUP>
+__global__ __launch_bounds__(kThreads) void int4_quantize_columns_kernel(const uint16_t* __restrict__ w, int64_t N,
+                                                                         int64_t K, int64_t E, bool symmetric,
+                                                                         uint8_t* __restrict__ q,
+                                                                         uint16_t* __restrict__ scales,
+                                                                         uint8_t* __restrict__ zeros) {
+  const int64_t groups = (K + GROUP - 1) / GROUP, row_bytes = int4_row_bytes(K), pairs = N / 2;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < E * groups * pairs; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t n = i % pairs * 2, g = i / pairs % groups, e = i / (pairs * groups);
+    const uint16_t* p = w + (e * K + g * GROUP) * N + n;
+    const int in = (int)(K - g * GROUP < GROUP ? K - g * GROUP : GROUP);  // values of the group
+    uint32_t x[GROUP];
+    float lo[2] = {0.0f, 0.0f}, hi[2] = {0.0f, 0.0f};
+    bool bad[2] = {false, false};
+#pragma unroll
+    for (int k = 0; k < GROUP; ++k) x[k] = k < in ? *reinterpret_cast<const uint32_t*>(p + k * N) : 0u;
+#pragma unroll
+    for (int k = 0; k < GROUP; ++k) {
+      const float v[2] = {bf16_lo(x[k]), bf16_hi(x[k])};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        lo[c] = fminf(lo[c], v[c]), hi[c] = fmaxf(hi[c], v[c]);
+        bad[c] = bad[c] || !(fabsf(v[c]) < __builtin_inff());
+      }
+    }
+    uint32_t s = 0, z = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const GroupCode gc = group_code(lo[c], hi[c], bad[c], symmetric);
+      s |= (uint32_t)gc.scale << (16 * c), z |= (uint32_t)gc.zero << (8 * c);
+      uint8_t* out = q + (e * N + n + c) * row_bytes + g * (GROUP / 2);
+#pragma unroll
+      for (int k = 0; k < GROUP; k += 32) {
+        if (k >= in) continue;
+        u32x4 o = {0u, 0u, 0u, 0u};  // whole 16 bytes, zeros behind the last value
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float v = c == 0 ? bf16_lo(x[k + j]) : bf16_hi(x[k + j]);
+          o[j >> 3] |= (k + j < in ? code_of(v, gc) : 0u) << (4 * (j & 7));
+        }
+        *reinterpret_cast<u32x4*>(out + k / 2) = o;
+      }
+    }
+    const int64_t at = (e * groups + g) * N + n;
+    *reinterpret_cast<uint32_t*>(scales + at) = s;
+    if (!symmetric) *reinterpret_cast<uint16_t*>(zeros + at) = (uint16_t)z;
+  }
+}
+
+// bf16 [E, N, K] of packed weights.
 __global__ __launch_bounds__(kThreads) void int4_dequantize_kernel(const uint8_t* __restrict__ q,
                                                                    const uint16_t* __restrict__ scales,
                                                                    const uint8_t* __restrict__ zeros, int64_t N,
-                                                                   int64_t K, int E, int group, uint16_t* __restrict__ w) {
-  const int64_t groups = (K + group - 1) / group, row_bytes = int4_row_bytes(K), pieces = K / 8;
-  const int64_t total = (int64_t)E * N * pieces;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t c = i % pieces, row = i / pieces, n = row % N, e = row / N;
-    const int64_t at = (e * groups + c * 8 / group) * N + n;
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(q + row * row_bytes + c * 4);
-    const float s = bf16_bits_to_f32(scales[at]);
-    const int z = zeros != nullptr ? zeros[at] : 8;
-    u32x4 o;
+                                                                   int64_t K, int64_t E, int group,
+                                                                   uint16_t* __restrict__ w) {
+  __shared__ float s_tile[kTileGroups][kTileRows + 1], z_tile[kTileGroups][kTileRows + 1];
+  const int64_t groups = (K + group - 1) / group, row_bytes = int4_row_bytes(K);
+  const int64_t n_tiles = (N + kTileRows - 1) / kTileRows, k_tiles = (K + kTileK - 1) / kTileK;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t i = blockIdx.x; i < E * n_tiles * k_tiles; i += gridDim.x) {
+    const RowTile t = row_tile(i, n_tiles, k_tiles);
+    for (int j = threadIdx.x; j < kTileK / group * kTileRows; j += kThreads) {
+      const int gi = j / kTileRows, r = j % kTileRows;
+      const int64_t g = t.k0 / group + gi;
+      if (g < groups && t.n0 + r < N) {
+        const int64_t at = (t.e * groups + g) * N + t.n0 + r;
+        s_tile[gi][r] = bf16_bits_to_f32(scales[at]);
+        z_tile[gi][r] = zeros != nullptr ? (float)zeros[at] : 8.0f;
+      }
+    }
+    __syncthreads();
+    const int64_t k = t.k0 + lane * 8;
+    if (k < K) {
+#pragma unroll 4
+      for (int r = wave; r < kTileRows; r += kWaves) {
+        if (t.n0 + r >= N) break;
+        const int64_t row = t.e * N + t.n0 + r;
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(q + row * row_bytes + k / 2);
+        const float s = s_tile[lane * 8 / group][r], z = z_tile[lane * 8 / group][r];
+        u32x4 o;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_bf16x2(s * (float)((int)((v >> (8 * j)) & 15u) - z), s * (float)((int)((v >> (8 * j + 4)) & 15u) - z));
-    *reinterpret_cast<u32x4*>(w + row * K + c * 8) = o;
+        for (int j = 0; j < 4; ++j)
+          o[j] = pack_bf16x2(s * ((float)((v >> (8 * j)) & 15u) - z), s * ((float)((v >> (8 * j + 4)) & 15u) - z));
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(w + row * K + k));
+      }
+    }
+    __syncthreads();
   }
 }
 
-unsigned grid_of(int64_t items) {
-  const int64_t blocks = (items + kThreads - 1) / kThreads, most = (int64_t)device_cu_count(current_device()) * 16;
-  return (unsigned)(blocks < most ? blocks : most);
+unsigned grid_of(int64_t workgroups, int per_cu) {
+  const int64_t most = (int64_t)device_cu_count(current_device()) * per_cu;
+  return (unsigned)(workgroups < most ? workgroups : most);
+}
+
+inline int64_t row_tiles(int64_t N, int64_t K, int64_t E) {
+  return E * ((N + kTileRows - 1) / kTileRows) * ((K + kTileK - 1) / kTileK);
 }
 
 }  // namespace
 
 hipError_t launch_int4_quantize(const uint16_t* w, bool w_out_in, int64_t d_in, int64_t d_out, int32_t E, int32_t group,
                                 uint8_t* q, uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
-  const int64_t items = (int64_t)E * ((d_in + group - 1) / group) * d_out;
   const bool symmetric = zeros == nullptr;
-  if (w_out_in)
-    hipLaunchKernelGGL((int4_quantize_kernel<true>), dim3(grid_of(items)), dim3(kThreads), 0, stream, w, d_out, d_in, E,
-                       group, symmetric, q, scales, zeros);
-  else
-    hipLaunchKernelGGL((int4_quantize_kernel<false>), dim3(grid_of(items)), dim3(kThreads), 0, stream, w, d_out, d_in, E,
-                       group, symmetric, q, scales, zeros);
-  return hipGetLastError();
+  if (w_out_in) {
+    hipLaunchKernelGGL(int4_quantize_rows_kernel, dim3(grid_of(row_tiles(d_out, d_in, E), 8)), dim3(kThreads), 0, stream, w,
+                       d_out, d_in, E, group, symmetric, q, scales, zeros);
+    return hipGetLastError();
+  }
+  const int64_t items = (int64_t)E * ((d_in + group - 1) / group) * (d_out / 2);
+  const dim3 grid(grid_of((items + kThreads - 1) / kThreads, 8));
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, w, d_out, d_in, E, symmetric, q, scales, zeros);
+    return hipGetLastError();
+  };
+  return group == 32 ? run(int4_quantize_columns_kernel<32>)
+                     : (group == 64 ? run(int4_quantize_columns_kernel<64>) : run(int4_quantize_columns_kernel<128>));
 }
 
 hipError_t launch_int4_dequantize(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t d_in,
                                   int64_t d_out, int32_t E, int32_t group, uint16_t* w, hipStream_t stream) {
-  hipLaunchKernelGGL(int4_dequantize_kernel, dim3(grid_of((int64_t)E * d_out * (d_in / 8))), dim3(kThreads), 0, stream, q,
+  hipLaunchKernelGGL(int4_dequantize_kernel, dim3(grid_of(row_tiles(d_out, d_in, E), 8)), dim3(kThreads), 0, stream, q,
                      scales, zeros, d_out, d_in, E, group, w);
   return hipGetLastError();
 }
