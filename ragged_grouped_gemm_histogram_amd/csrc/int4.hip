@@ -444,6 +444,13 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(In
   }
 }
 
+// Tiles of a call, as far as the host knows: each expert with rows ends with a tile that is half full on average.
+double expected_tiles(const Int4Args& g, int rows, int cols) {
+  const double experts = (double)(g.cap_rows < g.E ? g.cap_rows : g.E);
+  const double by_rows = (double)g.cap_rows / rows + experts / 2;
+  return (by_rows > experts ? by_rows : experts) * (double)((g.N + cols - 1) / cols);
+}
+
 template <class Kernel>
 hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, int resident, hipStream_t stream) {
   const int64_t most_experts = g.cap_rows < g.E ? g.cap_rows : g.E;
@@ -453,14 +460,23 @@ hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, in
   return hipGetLastError();
 }
 
-// By the mean of the rows per expert that the call has room for. us for 64 experts of 2048 -> 2 x 768 with 16, 32, 64
-// and 128 rows each: narrow 34, 54, 101, 191; 32 rows 38, 39, 61, 123; 64 rows -, -, 56, 90. From about 200 rows on
-// the bf16 launch on weights read back is faster (256 rows 138 against 168 us).
+// The kind of tile whose estimated time in us is least. Narrow tiles (four resident a CU) wait 3 us for each unit of
+// their longest wave; a wide one waits for each unit of the contraction, 1.85 us with 32 rows and 2.65 with 64, or as
+// long as the tiles of a CU take to unpack, 1.0 and 1.7 us a tile. Over 110 calls (1 to 128 experts, 16 to 65536 rows,
+// 64 to 3128 values by 64 to 3120 columns) the choice takes 0.4% longer than the best one in the mean, 9% at worst; by
+// the mean of the rows per expert alone (up to 16, up to 48, above) it took 33% longer. 64 experts of 2048 -> 2 x 768
+// with 16, 32, 64 and 128 rows each: narrow 34, 54, 101, 191 us; 32 rows 38, 39, 61, 123; 64 rows -, -, 56, 90.
 template <bool GATED, int GS>
 hipError_t launch_rows(const Int4Args& g, hipStream_t stream) {
   constexpr int kOut = GATED ? 32 : 64;
-  if (g.cap_rows <= 16 * (int64_t)g.E) return launch_tiles(int4_kernel<GATED, GS>, g, 16, kOut, 4, stream);
-  if (g.cap_rows <= 48 * (int64_t)g.E) return launch_tiles(int4_wide_kernel<GATED, 2, GS>, g, 32, 4 * kOut, 3, stream);
+  const double cus = (double)device_cu_count(current_device()), units = (double)((g.K + kUnit - 1) / kUnit);
+  auto larger = [](double a, double b) { return a > b ? a : b; };
+  const double longest = (double)(((g.K + kUnit - 1) / kUnit + kWaves - 1) / kWaves);
+  const double narrow = larger(1.0, expected_tiles(g, 16, kOut) / (4 * cus)) * (1.0 + 3.0 * longest);
+  const double wide32 = 3.0 + units * larger(1.85, 1.0 * expected_tiles(g, 32, 4 * kOut) / cus);
+  const double wide64 = 6.0 + units * larger(2.65, 1.7 * expected_tiles(g, 64, 4 * kOut) / cus);
+  if (narrow <= wide32 && narrow <= wide64) return launch_tiles(int4_kernel<GATED, GS>, g, 16, kOut, 4, stream);
+  if (wide32 <= wide64) return launch_tiles(int4_wide_kernel<GATED, 2, GS>, g, 32, 4 * kOut, 3, stream);
   return launch_tiles(int4_wide_kernel<GATED, 4, GS>, g, 64, 4 * kOut, 2, stream);
 }
 

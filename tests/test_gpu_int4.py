@@ -155,6 +155,15 @@ def test_gate_up(T, k, E, d, h, group, zeros, gather):
     up(T, k, p / p.sum(), E, d, h, group, zeros, drop=True, gather=gather)
 
 
+@pytest.mark.parametrize("rows", [4000, 10000])  # tiles of 32 and of 64 rows
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("K", [264, 512])
+def test_wide_tiles(rows, group, zeros, K):
+    projection([0, 1, 65, rows - 131, 33, 32], K, 2056, group, zeros, spare=1)
+    p = np.array([0.001, 0.9, 0.02, 0.06, 0.019])
+    up(rows // 2, 2, p, 5, K, 1032, group, zeros, drop=group == 64)
+
+
 def test_many_experts():
     rng = np.random.default_rng(5)
     for E in (255, 256, 257, 1024):
