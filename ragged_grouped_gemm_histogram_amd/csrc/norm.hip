@@ -15,7 +15,7 @@
 // forward are kept. Everything is fp32 after the loads; each output is rounded once.
 //
 // A row belongs to a team of ceil(d / 512) waves (half as many above 8192), a lane holding 8
-// consecutive columns (twice 8). The backward's teams walk the rows with the column sums in registers; a
+// consecutive columns (twice 8); up to 256 columns a wave takes two rows at once, up to 128 four. The backward's teams walk the rows with the column sums in registers; a
 // workgroup joins its teams' and leaves one row of partial sums, which a second launch adds in order, so
 // results repeat bit for bit.
 
@@ -118,13 +118,24 @@ __device__ __forceinline__ float wave_sum(float x) {
   return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }
 
-// Sums over a team of `waves` waves from wave `first` of the workgroup on, the same in every lane. `buf` alternates between two LDS areas, so one
-// barrier a round is enough: a wave reaches the round after next only behind the next one's barrier.
-template <int N>
+// x of this row of 16 lanes and of the one beside it, added up; and of both halves of the wave.
+__device__ __forceinline__ float add_rows(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// Sums over a team of `waves` waves from wave `first` of the workgroup on, the same in every lane; with LANES below 64
+// over the LANES lanes that hold a row. `buf` alternates between two LDS areas, so one barrier a round is enough: a wave
+// reaches the round after next only behind the next one's barrier.
+template <int LANES, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[kMaxWaves][N], int& buf, int waves, int first = 0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if (waves == 1) return;
+  for (int i = 0; i < N; ++i) v[i] = LANES == 64 ? wave_sum(v[i]) : (LANES == 32 ? add_rows(sum16(v[i])) : sum16(v[i]));
+  if (LANES < 64 || waves == 1) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (lane == 0) {
 #pragma unroll
@@ -137,7 +148,8 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[kMaxWaves][
   buf ^= 1;
 }
 
-template <class S, bool BRANCH, bool POST, bool NEXT, int V>
+// LANES: lanes that hold a row, 64 for a team of waves; with fewer a wave takes several rows.
+template <class S, bool BRANCH, bool POST, bool NEXT, int V, int LANES>
 __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs g) {
   __shared__ float red[2][kMaxWaves][1];
   const int waves = blockDim.x >> 6;
@@ -145,36 +157,42 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs g) {
   S* r_out = static_cast<S*>(g.r_out);
   const float inv_d = 1.0f / (float)g.d;
   int buf = 0;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+  constexpr int kRows = 64 / LANES;
+  const int lane = threadIdx.x & 63;
+  const int span = LANES == 64 ? (int)blockDim.x : LANES, at = LANES == 64 ? (int)threadIdx.x : lane % LANES;
+  const int64_t turn = LANES == 64 ? gridDim.x : (int64_t)gridDim.x * waves * kRows;
+  for (int64_t t0 = LANES == 64 ? blockIdx.x : ((int64_t)blockIdx.x * waves + (threadIdx.x >> 6)) * kRows; t0 < g.T; t0 += turn) {
+    const int64_t t = LANES == 64 ? t0 : t0 + lane / LANES;
     const int64_t row = t * g.d;
+    const int end = LANES == 64 || t < g.T ? g.d : 0;  // columns of this lane's row
     float x[V][8], u[V][8];
     float ss[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
+      const int col = (j * span + at) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[j][i] = u[j][i] = 0.0f;
-      if (col < g.d) {
+      if (col < end) {
         load8(r_in + row + col, x[j]);
         if constexpr (BRANCH) load8(g.y + row + col, u[j]);
       }
     }
     if constexpr (BRANCH) {
       float scale = g.b;
-      if (g.gate_kind == MOE_GATE_TOKEN) scale *= static_cast<const float*>(g.gate)[t];
+      if (g.gate_kind == MOE_GATE_TOKEN && end > 0) scale *= static_cast<const float*>(g.gate)[t];
       if constexpr (POST) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
           for (int i = 0; i < 8; ++i) ss[0] = fmaf(u[j][i], u[j][i], ss[0]);
-        team_sum(ss, red, buf, waves);
+        team_sum<LANES>(ss, red, buf, waves);
         scale *= rsqrtf(fmaf(ss[0], inv_d, g.eps));
         ss[0] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
-        if (col < g.d) {
+        const int col = (j * span + at) * 8;
+        if (col < end) {
           float w[8];
           if constexpr (POST) {
             load_weight(g.w_post, g.w_f32, col, w);
@@ -197,12 +215,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_kernel(NormArgs g) {
       for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss[0] = fmaf(x[j][i], x[j][i], ss[0]);
-      team_sum(ss, red, buf, waves);
+      team_sum<LANES>(ss, red, buf, waves);
       const float rs = rsqrtf(fmaf(ss[0], inv_d, g.eps));
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
-        if (col < g.d) {
+        const int col = (j * span + at) * 8;
+        if (col < end) {
           float w[8];
           load_weight(g.w_next, g.w_f32, col, w);
 #pragma unroll
@@ -275,17 +293,19 @@ constexpr int kBackLds = 96 * 1024;  // for the weights: all three of 8192 colum
 // CHANNEL: the gate is one per channel. ADD: d_n comes in two parts. The column sums stand in the order dw_next,
 // dw_post, dgate, those that the form has. A row's loads go out before the row before it is computed (not with V = 2,
 // whose registers do not hold two rows); for that the weights come from LDS: loads return in order, so one of a
-// weight would wait for the whole row read ahead. WIDE: a team of more than 8 waves.
-template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL, bool ADD, bool WIDE, int V>
+// weight would wait for the whole row read ahead. WIDE: a team of more than 8 waves. LANES as above.
+template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL, bool ADD, bool WIDE, int V, int LANES>
 __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_backward_kernel(NormArgs g) {
   constexpr int kCols = (NEXT ? 1 : 0) + (POST ? 1 : 0) + (CHANNEL ? 1 : 0);
   constexpr int kColPost = NEXT ? 1 : 0, kColGate = kColPost + (POST ? 1 : 0);
   __shared__ float red[2][kMaxWaves][6];
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   float* w_lds = reinterpret_cast<float*>(lds);  // the weights in the order of their sums as fp32, 0 past the last column
-  const int waves = g.team_waves, span = 64 * waves, padded = span * 8 * V;
+  constexpr int kRows = 64 / LANES;  // rows of a team's turn
+  const int waves = g.team_waves, span = LANES == 64 ? 64 * waves : LANES, padded = span * 8 * V;
   const int team = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / waves;  // the same for a whole wave
-  const int at = (int)threadIdx.x - team * span;
+  const int at = LANES == 64 ? (int)threadIdx.x - team * span : (int)threadIdx.x & (LANES - 1);
+  const int sub = LANES == 64 ? 0 : ((int)threadIdx.x & 63) / LANES;  // this lane's row of the turn
   const float inv_d = 1.0f / (float)g.d;
   const bool token = BRANCH && g.gate_kind == MOE_GATE_TOKEN;
   const bool in_lds = !WIDE || kCols * padded * (int)sizeof(float) <= kBackLds;
@@ -321,14 +341,21 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[k][j][i] = 0.0f;
 
+  // rows from t on that are there
+  auto rows_at = [&](int64_t t) { return t >= g.T ? 0 : (g.T - t < kRows ? (int)(g.T - t) : kRows); };
+  // where a column stands behind the turn's first (past the last column: behind everything)
+  auto column = [&](int j) {
+    const int col = (j * span + at) * 8;
+    return LANES == 64 ? col : (col < g.d ? sub * g.d + col : 1 << 28);
+  };
   auto read = [&](BackRow<S, V>& row, int64_t t) {
-    const int sb = t < g.T ? s_bytes : 0, hb = t < g.T ? h_bytes : 0;
+    const int sb = rows_at(t) * s_bytes, hb = rows_at(t) * h_bytes;
     const auto x = row_of(g.r, t * s_bytes, NEXT ? sb : 0), d = row_of(g.dr, t * s_bytes, g.dr != nullptr ? sb : 0);
     const auto dn = row_of(g.dn, t * h_bytes, NEXT ? hb : 0), more = row_of(g.dn_add, t * h_bytes, ADD ? hb : 0);
     const auto y = row_of(g.y, t * h_bytes, POST || CHANNEL || token ? hb : 0);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int col = (j * span + at) * 8;
+      const int col = column(j);
       if constexpr (NEXT) row.x[j].read(x, col), row.dn[j].read(dn, col);
       if constexpr (ADD) row.more[j].read(more, col);
       row.d[j].read(d, col);
@@ -338,6 +365,8 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
 
   int buf = 0;
   auto compute = [&](const BackRow<S, V>& row, int64_t t) {
+    // (the weights are read from LDS again for each use: kept over the rows, they would fill the registers)
+    if constexpr (LANES < 64) asm volatile("" : : : "memory");
     float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -367,19 +396,22 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
         }
       }
     }
-    if (NEXT || POST || token) team_sum(s, red, buf, waves, team * waves);
+    if (NEXT || POST || token) team_sum<LANES>(s, red, buf, waves, team * waves);
     float gate = 1.0f;
-    if (token && t < g.T) gate = static_cast<const float*>(g.gate)[t];
-    const float k1 = NEXT ? rsqrtf(fmaf(s[0], inv_d, g.eps)) : 0.0f;
+    const bool live = t + sub < g.T;
+    if (token && live) gate = static_cast<const float*>(g.gate)[t + sub];
+    // (a row that is not there has zeros for its sums: no factor of it may be infinite)
+    const float k1 = NEXT && live ? rsqrtf(fmaf(s[0], inv_d, g.eps)) : 0.0f;
     const float k2 = k1 * s[1] * inv_d * k1 * k1;
     const float qg = s[3] + k1 * s[4] - k2 * s[5];  // sum of q g
-    const float rsy = POST ? rsqrtf(fmaf(s[2], inv_d, g.eps)) : 1.0f;
+    const float rsy = POST ? (live ? rsqrtf(fmaf(s[2], inv_d, g.eps)) : 0.0f) : 1.0f;
     const float bt = g.b * gate;
     const float p1 = rsy * bt, p2 = rsy * qg * inv_d * rsy * rsy * bt;
-    if (token && at == 0 && t < g.T) g.d_gate_token[t] = g.b * rsy * qg;
-    const auto dr_row = row_of(g.r_out, t * s_bytes, t < g.T ? s_bytes : 0);
-    const auto dy_row = row_of(g.dy, t * h_bytes, BRANCH && t < g.T ? h_bytes : 0);
+    if (token && at == 0 && live) g.d_gate_token[t + sub] = g.b * rsy * qg;
+    const auto dr_row = row_of(g.r_out, t * s_bytes, rows_at(t) * s_bytes);
+    const auto dy_row = row_of(g.dy, t * h_bytes, BRANCH ? rows_at(t) * h_bytes : 0);
     if (t >= g.T) return;
+    if constexpr (LANES < 64) asm volatile("" : : : "memory");
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = (j * span + at) * 8;
@@ -411,33 +443,46 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
           }
         }
       }
-      write8(dr_row, col, dx, S{});
-      if constexpr (BRANCH) write8(dy_row, col, dy, uint16_t{});
+      write8(dr_row, column(j), dx, S{});
+      if constexpr (BRANCH) write8(dy_row, column(j), dy, uint16_t{});
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(acc[k][j][i]));  // added here, not put off behind the next row
     }
   };
 
-  // rows t0 + team of every workgroup's turn; a team without a row goes along, for the barriers
-  const int teams = WIDE ? 1 : (int)blockDim.x / span;
-  const int64_t turn = (int64_t)gridDim.x * teams;
-  int64_t t0 = (int64_t)blockIdx.x * teams;
-  if constexpr (V > 1) {
+  // every workgroup's turn: rows t0 on, kRows of them a team; a team without a row goes along, for the barriers
+  const int teams = WIDE ? 1 : (int)blockDim.x / (64 * waves), mine = team * kRows;
+  const int64_t turn = (int64_t)gridDim.x * teams * kRows;
+  int64_t t0 = (int64_t)blockIdx.x * teams * kRows;
+  if constexpr (V > 1 || LANES < 64) {
     for (; t0 < g.T; t0 += turn) {
       BackRow<S, V> row;
-      read(row, t0 + team);
-      compute(row, t0 + team);
+      read(row, t0 + mine);
+      compute(row, t0 + mine);
     }
   } else {
     BackRow<S, V> even, odd;
-    read(even, t0 + team);
+    read(even, t0 + mine);
     while (t0 < g.T) {
-      read(odd, t0 + turn + team);
-      compute(even, t0 + team);
+      read(odd, t0 + turn + mine);
+      compute(even, t0 + mine);
       t0 += turn;
       if (t0 >= g.T) break;
-      read(even, t0 + turn + team);
-      compute(odd, t0 + team);
+      read(even, t0 + turn + mine);
+      compute(odd, t0 + mine);
       t0 += turn;
     }
+  }
+  if constexpr (LANES < 64) {  // the rows of a wave
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (LANES == 16) acc[k][0][i] = add_rows(acc[k][0][i]);
+        acc[k][0][i] = add_halves(acc[k][0][i]);
+      }
   }
   // the teams' sums, one after the other
   if constexpr (kCols > 0 && !WIDE) {
@@ -505,6 +550,9 @@ __global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float*
   }
 }
 
+// Lanes that hold a row of 8 columns each: a quarter or half of a wave for short rows, else whole waves.
+inline int row_lanes(int64_t d) { return d <= 128 ? 16 : (d <= 256 ? 32 : 64); }
+
 // Waves of a team: V vectors of 8 columns a lane.
 inline int vectors(int64_t d) { return d > 512 * kMaxWaves ? 2 : 1; }
 inline int team_waves(int64_t d) {
@@ -514,13 +562,19 @@ inline int team_waves(int64_t d) {
 
 template <class S, bool BRANCH, bool POST, bool NEXT>
 hipError_t run_forward(const NormArgs& g, hipStream_t stream) {
-  const int waves = team_waves(g.d);
-  int64_t teams = (int64_t)device_cu_count(current_device()) * (32 / waves);
-  if (teams > g.T) teams = g.T;
-  const dim3 grid((unsigned)teams), block(64 * waves);
-  if (vectors(g.d) == 1) hipLaunchKernelGGL((norm_kernel<S, BRANCH, POST, NEXT, 1>), grid, block, 0, stream, g);
-  else hipLaunchKernelGGL((norm_kernel<S, BRANCH, POST, NEXT, 2>), grid, block, 0, stream, g);
-  return hipGetLastError();
+  const int lanes = row_lanes(g.d), waves = lanes == 64 ? team_waves(g.d) : 4;
+  const int64_t rows = lanes == 64 ? 1 : 64 / lanes * waves;  // of a workgroup's turn
+  int64_t groups = (g.T + rows - 1) / rows;
+  const int64_t fit = (int64_t)device_cu_count(current_device()) * (32 / waves);
+  const dim3 grid((unsigned)(groups < fit ? groups : fit)), block(64 * waves);
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, g);
+    return hipGetLastError();
+  };
+  if (lanes == 16) return run(norm_kernel<S, BRANCH, POST, NEXT, 1, 16>);
+  if (lanes == 32) return run(norm_kernel<S, BRANCH, POST, NEXT, 1, 32>);
+  if (vectors(g.d) == 1) return run(norm_kernel<S, BRANCH, POST, NEXT, 1, 64>);
+  return run(norm_kernel<S, BRANCH, POST, NEXT, 2, 64>);
 }
 
 template <class S>
@@ -541,7 +595,9 @@ hipError_t run_backward(const NormArgs& g, int groups, hipStream_t stream) {
   constexpr int kCols = (NEXT ? 1 : 0) + (POST ? 1 : 0) + (CHANNEL ? 1 : 0);
   const int teams = back_teams(g.d);
   const dim3 grid(groups), block(64 * g.team_waves * teams);
-  size_t lds = (size_t)kCols * g.team_waves * 512 * vectors(g.d) * sizeof(float);  // the weights; at the end a team's sums
+  const int lanes = row_lanes(g.d);
+  // the weights; at the end a team's sums
+  size_t lds = (size_t)kCols * g.team_waves * (lanes * 8) * vectors(g.d) * sizeof(float);
   if (lds > kBackLds) lds = 0;  // (V = 2 alone)
   auto run = [&](auto kernel) {
     if (lds > 64 * 1024) {
@@ -552,9 +608,11 @@ hipError_t run_backward(const NormArgs& g, int groups, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, grid, block, lds, stream, g);
     return hipGetLastError();
   };
-  if (g.team_waves <= kBackWaves) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, false, 1>);
-  if (vectors(g.d) == 1) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, true, 1>);
-  return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, true, 2>);
+  if (lanes == 16) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, false, 1, 16>);
+  if (lanes == 32) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, false, 1, 32>);
+  if (g.team_waves <= kBackWaves) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, false, 1, 64>);
+  if (vectors(g.d) == 1) return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, true, 1, 64>);
+  return run(norm_backward_kernel<S, BRANCH, POST, NEXT, CHANNEL, ADD, true, 2, 64>);
 }
 
 template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL>
@@ -582,7 +640,8 @@ hipError_t backward(const NormArgs& g, bool branch, bool post, bool next, int gr
 
 // As many workgroups as are resident on 256 CUs: more partial rows would cost more than they overlap.
 int64_t norm_partial_rows(int64_t T, int64_t d) {
-  const int64_t groups = (T + back_teams(d) - 1) / back_teams(d), most = team_waves(d) > kBackWaves ? 256 : 512;
+  const int64_t rows = back_teams(d) * (64 / row_lanes(d));  // of a workgroup's turn
+  const int64_t groups = (T + rows - 1) / rows, most = team_waves(d) > kBackWaves ? 256 : 512;
   return groups < most ? groups : most;
 }
 

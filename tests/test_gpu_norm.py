@@ -78,7 +78,8 @@ def test_forms(post, gate, nxt, stream, weights):
 
 
 @pytest.mark.parametrize("T,d", [(1, 8), (2, 16), (65, 24), (3, 504), (5, 512), (5, 520), (4, 2048), (33, 2056),
-                                 (3, 2880), (2, 8192), (3, 8200), (2, 16376), (2, 16384), (1100, 64)])
+                                 (3, 2880), (2, 8192), (3, 8200), (2, 16376), (2, 16384), (1100, 64),
+                                 (3, 120), (5, 128), (67, 136), (2, 248), (7, 256), (35, 264), (20001, 72), (9001, 200)])
 @pytest.mark.parametrize("stream", [BF16, F32])
 def test_sizes(T, d, stream):
     if d <= 4096:  # (the reference's Jacobian is a matrix of d x d)
