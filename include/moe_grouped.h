@@ -538,9 +538,9 @@ size_t moe_norm_workspace_bytes(int64_t T, int64_t d);
  *              calls and graphs that may run at the same time need one each
  *
  * Sums are taken in a fixed order: results repeat bit for bit. */
-moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, const void* x, int32_t x_dtype, const void* w, int32_t w_dtype,
-                                float eps, const void* dx_add, int64_t T, int64_t d, void* dx, float* dw,
-                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, const void* x, int32_t x_dtype,
+                                const void* w, int32_t w_dtype, float eps, const void* dx_add, int64_t T, int64_t d,
+                                void* dx, float* dw, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Backward of moe_residual_norm from its inputs' y, its output r_out and the
  * gradients of r_out and n (the rounding of r_out is taken as an identity).
@@ -554,11 +554,11 @@ moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, cons
  *   d_gate    fp32   [T] or [d] as the gate, out; with a gate only
  *   d_w_post, d_w_next  fp32 [d], out; NULL: not needed */
 moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, const uint16_t* d_n_add,
-                                      const uint16_t* y, const void* r_out, int32_t r_dtype, int32_t flags, const void* w_post, const void* w_next,
-                                      int32_t w_dtype, const void* gate, int32_t gate_kind, float residual_scale,
-                                      float branch_scale, float eps, int64_t T, int64_t d, void* d_r, uint16_t* d_y,
-                                      float* d_gate, float* d_w_post, float* d_w_next, void* workspace,
-                                      size_t workspace_bytes, hipStream_t stream);
+                                      const uint16_t* y, const void* r_out, int32_t r_dtype, int32_t flags,
+                                      const void* w_post, const void* w_next, int32_t w_dtype, const void* gate,
+                                      int32_t gate_kind, float residual_scale, float branch_scale, float eps, int64_t T,
+                                      int64_t d, void* d_r, uint16_t* d_y, float* d_gate, float* d_w_post,
+                                      float* d_w_next, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * AdamW over a list of tensors. For every value p with gradient g, in fp32:
@@ -612,7 +612,8 @@ typedef struct moe_adamw_hyper {
  * The three let a captured step follow what changes from replay to replay. */
 moe_status moe_adamw_step(const moe_adamw_tensor* tensors, void* const* params, const void* const* grads, int32_t count,
                           int32_t bits, int64_t len, void* m, uint8_t* m_scales, void* v, uint8_t* v_scales,
-                          float* master, const moe_adamw_hyper* hyper, const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream);
+                          float* master, const moe_adamw_hyper* hyper, const float* lr_ptr, const int32_t* step_ptr,
+                          const float* grad_scale, hipStream_t stream);
 
 /* The values of 8-bit moments as bf16 [len] (exact unless below bf16's range), one launch. */
 moe_status moe_adamw_moments(const uint8_t* m, const uint8_t* m_scales, const uint8_t* v, const uint8_t* v_scales,
@@ -651,7 +652,7 @@ moe_status moe_int4_dequantize_weights(const uint8_t* q, const uint16_t* scales,
  *   offsets  int32 [E+1], clamped as in the bf16 calls
  *   y        bf16  [cap_rows, d_out] out (rows past M untouched)
  *
- * A row with an infinity gives NaN. */
+ * A row with an infinity, or whose sums of 31 |x| pass fp32, gives NaN or infinity. */
 moe_status moe_grouped_projection_int4(const uint16_t* x, const int32_t* offsets, const uint8_t* q,
                                        const uint16_t* scales, const uint8_t* zeros, int32_t group, int64_t cap_rows,
                                        int64_t d_in, int64_t d_out, int32_t E, uint16_t* y, hipStream_t stream);

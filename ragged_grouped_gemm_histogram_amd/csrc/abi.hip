@@ -581,15 +581,15 @@ size_t moe_norm_workspace_bytes(int64_t T, int64_t d) {
   return (size_t)norm_partial_rows(T, d) * (size_t)d * 3 * sizeof(float);
 }
 
-moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, const void* x, int32_t x_dtype, const void* w, int32_t w_dtype,
-                                float eps, const void* dx_add, int64_t T, int64_t d, void* dx, float* dw,
-                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, const void* x, int32_t x_dtype,
+                                const void* w, int32_t w_dtype, float eps, const void* dx_add, int64_t T, int64_t d,
+                                void* dx, float* dw, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_norm_shape(x_dtype, w_dtype, T, d);
   if (st != MOE_OK) return st;
   if (bad_norm_values(1.0f, 1.0f, eps)) return MOE_ERR_BAD_VALUE;
   if (missing(dy, T) || missing(x, T) || missing(dx, T) || missing(workspace, T)) return MOE_ERR_NULL_POINTER;
-  if (misaligned(dy, 16) || misaligned(dy_add, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(dx_add, 16) || misaligned(dx, 16) ||
-      misaligned(dw, 4) || misaligned(workspace, 16))
+  if (misaligned(dy, 16) || misaligned(dy_add, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(dx_add, 16) ||
+      misaligned(dx, 16) || misaligned(dw, 4) || misaligned(workspace, 16))
     return MOE_ERR_MISALIGNED;
   if (workspace_bytes < moe_norm_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
   if ((st = check_device()) != MOE_OK) return st;
@@ -600,11 +600,11 @@ moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* dy_add, cons
 }
 
 moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, const uint16_t* d_n_add,
-                                      const uint16_t* y, const void* r_out, int32_t r_dtype, int32_t flags, const void* w_post, const void* w_next,
-                                      int32_t w_dtype, const void* gate, int32_t gate_kind, float residual_scale,
-                                      float branch_scale, float eps, int64_t T, int64_t d, void* d_r, uint16_t* d_y,
-                                      float* d_gate, float* d_w_post, float* d_w_next, void* workspace,
-                                      size_t workspace_bytes, hipStream_t stream) {
+                                      const uint16_t* y, const void* r_out, int32_t r_dtype, int32_t flags,
+                                      const void* w_post, const void* w_next, int32_t w_dtype, const void* gate,
+                                      int32_t gate_kind, float residual_scale, float branch_scale, float eps, int64_t T,
+                                      int64_t d, void* d_r, uint16_t* d_y, float* d_gate, float* d_w_post,
+                                      float* d_w_next, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_residual_norm(r_dtype, flags, w_post, w_next, w_dtype, gate, gate_kind, residual_scale,
                                       branch_scale, eps, T, d);
   if (st != MOE_OK) return st;
@@ -630,10 +630,11 @@ moe_status moe_residual_norm_backward(const void* d_r_out, const uint16_t* d_n, 
 
 moe_status moe_adamw_step(const moe_adamw_tensor* tensors, void* const* params, const void* const* grads, int32_t count,
                           int32_t bits, int64_t len, void* m, uint8_t* m_scales, void* v, uint8_t* v_scales,
-                          float* master, const moe_adamw_hyper* hyper, const float* lr_ptr, const int32_t* step_ptr, const float* grad_scale, hipStream_t stream) {
+                          float* master, const moe_adamw_hyper* hyper, const float* lr_ptr, const int32_t* step_ptr,
+                          const float* grad_scale, hipStream_t stream) {
   if (count < 0 || len < 0 || len > kMaxMoments || len % 32 != 0 || (bits != 8 && bits != 32)) return MOE_ERR_BAD_SHAPE;
-  if (hyper == nullptr || missing(tensors, count) || missing(params, count) || missing(grads, count) || missing(m, len) || missing(v, len) ||
-      (bits == 8 && (missing(m_scales, len) || missing(v_scales, len))))
+  if (hyper == nullptr || missing(tensors, count) || missing(params, count) || missing(grads, count) ||
+      missing(m, len) || missing(v, len) || (bits == 8 && (missing(m_scales, len) || missing(v_scales, len))))
     return MOE_ERR_NULL_POINTER;
   if (misaligned(m, 16) || misaligned(v, 16) || misaligned(master, 16) || misaligned(lr_ptr, 4) ||
       misaligned(step_ptr, 4) || misaligned(grad_scale, 4))

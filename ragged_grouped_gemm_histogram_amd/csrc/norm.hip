@@ -15,9 +15,18 @@
 // forward are kept. Everything is fp32 after the loads; each output is rounded once.
 //
 // A row belongs to a team of ceil(d / 512) waves (half as many above 8192), a lane holding 8
-// consecutive columns (twice 8); up to 256 columns a wave takes two rows at once, up to 128 four. The backward's teams walk the rows with the column sums in registers; a
-// workgroup joins its teams' and leaves one row of partial sums, which a second launch adds in order, so
-// results repeat bit for bit.
+// consecutive columns (twice 8); up to 256 columns a wave takes two rows at once, up to 128 four. The
+// backward's teams walk the rows with the column sums in registers; a workgroup joins its teams' and leaves
+// one row of partial sums, which a second launch adds in order, so results repeat bit for bit.
+//
+// Measured (bf16 / fp32 stream; a copy of 2 GiB runs at 4.9 TB/s, tensors that the last-level cache holds run faster):
+//                                 before              after, both norms   backward of each
+//   65536 x 64                    7.8 / 7.5 us        9.7 / 12.1          15.2 / 16.0, 22.4 / 23.4
+//   8191 x 2880                   16.5 / 22.8         30.5 / 55.4         36.1 / 64.4, 60.4 / 93.5
+//   4096 x 8192                   21.3 / 30.7         41.9 / 78.6         50.0 / 90.5, 99.7 / 136.7
+//   2048 x 16384                  21.3 / 31.7         51.4 / 87.2         55.1 / 98.8, 156 / 218
+// The last column's last row is 2.6 to 2.8 TB/s: above 8192 columns a lane's two vectors of all rows and sums leave no
+// registers to read ahead, and some spill. Small calls wait for one chain of load, sum and store, 3 us, and the backward's second launch.
 
 #include "common.h"
 
@@ -253,6 +262,7 @@ template <>
 struct Raw<uint16_t> {
   u32x4 v;
   __device__ __forceinline__ void read(__amdgpu_buffer_rsrc_t row, int col) { v = read16(row, col * 2); }
+  __device__ __forceinline__ void keep() { asm volatile("" : "+v"(v)); }
   __device__ __forceinline__ float operator[](int i) const {
     return __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
   }
@@ -263,6 +273,7 @@ struct Raw<float> {
   __device__ __forceinline__ void read(__amdgpu_buffer_rsrc_t row, int col) {
     lo = read16(row, col * 4), hi = read16(row, col * 4 + 16);
   }
+  __device__ __forceinline__ void keep() { asm volatile("" : "+v"(lo), "+v"(hi)); }
   __device__ __forceinline__ float operator[](int i) const { return __builtin_bit_cast(float, i < 4 ? lo[i] : hi[i - 4]); }
 };
 
@@ -285,15 +296,16 @@ template <class S, int V>
 struct BackRow {
   Raw<S> x[V], d[V];
   Raw<uint16_t> dn[V], more[V], y[V];
+  float gate;  // one per token
 };
 
 constexpr int kBackWaves = 8;  // a workgroup: as many teams as fit, one WIDE team above
-constexpr int kBackLds = 96 * 1024;  // for the weights: all three of 8192 columns
+constexpr int kBackLds = 128 * 1024;  // for the weights: three of 10920 columns, two of 16384
 
 // CHANNEL: the gate is one per channel. ADD: d_n comes in two parts. The column sums stand in the order dw_next,
-// dw_post, dgate, those that the form has. A row's loads go out before the row before it is computed (not with V = 2,
-// whose registers do not hold two rows); for that the weights come from LDS: loads return in order, so one of a
-// weight would wait for the whole row read ahead. WIDE: a team of more than 8 waves. LANES as above.
+// dw_post, dgate, those that the form has. A row's loads go out before the row before it is computed (not with V = 2, nor
+// with several rows a wave, whose registers do not hold two turns); for that the weights come from LDS: loads return
+// in order, so one of a weight would wait for the whole row read ahead. WIDE: a team of more than 8 waves. LANES as above.
 template <class S, bool BRANCH, bool POST, bool NEXT, bool CHANNEL, bool ADD, bool WIDE, int V, int LANES>
 __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_backward_kernel(NormArgs g) {
   constexpr int kCols = (NEXT ? 1 : 0) + (POST ? 1 : 0) + (CHANNEL ? 1 : 0);
@@ -353,6 +365,10 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
     const auto x = row_of(g.r, t * s_bytes, NEXT ? sb : 0), d = row_of(g.dr, t * s_bytes, g.dr != nullptr ? sb : 0);
     const auto dn = row_of(g.dn, t * h_bytes, NEXT ? hb : 0), more = row_of(g.dn_add, t * h_bytes, ADD ? hb : 0);
     const auto y = row_of(g.y, t * h_bytes, POST || CHANNEL || token ? hb : 0);
+    if constexpr (BRANCH && !CHANNEL) {
+      const auto gate = row_of(g.gate, t * 4, token ? rows_at(t) * 4 : 0);
+      row.gate = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(gate, sub * 4, 0, 0));
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = column(j);
@@ -363,10 +379,11 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
     }
   };
 
+  constexpr bool kKeep = WIDE;  // a row is widened again for its second use: held in fp32 over the sums, it would spill
   int buf = 0;
-  auto compute = [&](const BackRow<S, V>& row, int64_t t) {
+  auto compute = [&](BackRow<S, V>& row, int64_t t) {
     // (the weights are read from LDS again for each use: kept over the rows, they would fill the registers)
-    if constexpr (LANES < 64) asm volatile("" : : : "memory");
+    if constexpr (LANES < 64 || V > 1) asm volatile("" : : : "memory");
     float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -395,26 +412,36 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
           }
         }
       }
+      if constexpr (V > 1) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) asm volatile("" : "+v"(s[i]) : : "memory");
+        __builtin_amdgcn_sched_barrier(0);  // one vector's weights at a time
+      }
     }
     if (NEXT || POST || token) team_sum<LANES>(s, red, buf, waves, team * waves);
-    float gate = 1.0f;
     const bool live = t + sub < g.T;
-    if (token && live) gate = static_cast<const float*>(g.gate)[t + sub];
     // (a row that is not there has zeros for its sums: no factor of it may be infinite)
     const float k1 = NEXT && live ? rsqrtf(fmaf(s[0], inv_d, g.eps)) : 0.0f;
     const float k2 = k1 * s[1] * inv_d * k1 * k1;
     const float qg = s[3] + k1 * s[4] - k2 * s[5];  // sum of q g
     const float rsy = POST ? (live ? rsqrtf(fmaf(s[2], inv_d, g.eps)) : 0.0f) : 1.0f;
-    const float bt = g.b * gate;
+    float bt = g.b;
+    if constexpr (BRANCH && !CHANNEL) bt = token ? g.b * row.gate : g.b;
     const float p1 = rsy * bt, p2 = rsy * qg * inv_d * rsy * rsy * bt;
     if (token && at == 0 && live) g.d_gate_token[t + sub] = g.b * rsy * qg;
     const auto dr_row = row_of(g.r_out, t * s_bytes, rows_at(t) * s_bytes);
     const auto dy_row = row_of(g.dy, t * h_bytes, BRANCH ? rows_at(t) * h_bytes : 0);
     if (t >= g.T) return;
-    if constexpr (LANES < 64) asm volatile("" : : : "memory");
+    if constexpr (LANES < 64 || V > 1) asm volatile("" : : : "memory");
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = (j * span + at) * 8;
+      if constexpr (kKeep) {
+        if constexpr (NEXT) row.x[j].keep(), row.dn[j].keep();
+        if constexpr (ADD) row.more[j].keep();
+        row.d[j].keep();
+        if constexpr (BRANCH) row.y[j].keep();
+      }
       float wn[8], wp[8], gc[8], dx[8], dy[8];
       if constexpr (NEXT) weight(0, col, wn);
       if constexpr (POST) weight(kColPost, col, wp);
@@ -449,6 +476,10 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
       for (int k = 0; k < kCols; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(acc[k][j][i]));  // added here, not put off behind the next row
+      if constexpr (V > 1) {
+        asm volatile("" : : : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
 
@@ -550,7 +581,8 @@ __global__ __launch_bounds__(64 * kSumWaves) void column_sum_kernel(const float*
   }
 }
 
-// Lanes that hold a row of 8 columns each: a quarter or half of a wave for short rows, else whole waves.
+// Lanes that hold a row of 8 columns each: a quarter or half of a wave for short rows, else whole waves (65536 x 64, bf16:
+// with a wave a row 12.2, 25.3, 28.7 and 47.4 us for what takes 7.8, 9.7, 15.2 and 22.4 this way).
 inline int row_lanes(int64_t d) { return d <= 128 ? 16 : (d <= 256 ? 32 : 64); }
 
 // Waves of a team: V vectors of 8 columns a lane.

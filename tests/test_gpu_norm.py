@@ -79,7 +79,8 @@ def test_forms(post, gate, nxt, stream, weights):
 
 @pytest.mark.parametrize("T,d", [(1, 8), (2, 16), (65, 24), (3, 504), (5, 512), (5, 520), (4, 2048), (33, 2056),
                                  (3, 2880), (2, 8192), (3, 8200), (2, 16376), (2, 16384), (1100, 64),
-                                 (3, 120), (5, 128), (67, 136), (2, 248), (7, 256), (35, 264), (20001, 72), (9001, 200)])
+                                 (3, 120), (5, 128), (67, 136), (2, 248), (7, 256), (35, 264), (20001, 72), (9001, 200),
+                                 (5, 10912), (3, 12288)])
 @pytest.mark.parametrize("stream", [BF16, F32])
 def test_sizes(T, d, stream):
     if d <= 4096:  # (the reference's Jacobian is a matrix of d x d)
@@ -158,6 +159,20 @@ def test_in_place_and_repeatable(stream):
     assert x2.data_ptr() == r.data_ptr() and torch.equal(x, x2) and torch.equal(n, n2)
     g2 = moe.moe_residual_norm_backward(dr, dn, v["y"], x, d_r=dr, d_y=dn, **kw)
     assert torch.equal(g2.d_r, g.d_r) and torch.equal(g2.d_y, g.d_y) and g2.d_r.data_ptr() == dr.data_ptr()
+
+
+@pytest.mark.parametrize("T,d,kind", [(70, 64, "token"), (70, 200, "token"), (40, 2880, "token"), (9, 8200, "token"),
+                                      (33, 1032, "channel")])
+def test_every_gradient_over_an_input(T, d, kind):
+    v = inputs(T, d, F32, F32, kind, 12)
+    kw = dict(post_norm=True, w_post=v["w_post"], w_next=v["w_next"])
+    x, _ = moe.moe_residual_norm(v["y"], v["r"], gate=v["gate"], **kw)
+    want = moe.moe_residual_norm_backward(v["dr"], v["dn"], v["y"], x, gate=v["gate"], **kw)
+    got = moe.moe_residual_norm_backward(v["dr"], v["dn"], v["y"], x, gate=v["gate"], d_r=x, d_y=v["y"], d_gate=v["gate"],
+                                         **kw)
+    assert got.d_gate.data_ptr() == v["gate"].data_ptr() and got.d_r.data_ptr() == x.data_ptr()
+    for f in ("d_r", "d_y", "d_gate", "d_w_post", "d_w_next"):
+        assert torch.equal(getattr(got, f), getattr(want, f)), f
 
 
 def test_gradient_against_differences():
