@@ -1159,31 +1159,15 @@ class AdamW:
         if not self.params:
             raise ValueError("no parameters")
         dev = self.params[0].device
-        spans = []
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor) or p.dtype not in _LOGITS:
                 raise TypeError(f"params[{i}] must be a bfloat16 or float32 tensor")
             _want(p, f"params[{i}]", p.dtype, tuple(p.shape), dev)
-            if p.numel():
-                spans.append((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()))
-        spans.sort()
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("parameters share memory: each value is stepped once")
+        self._want_apart()
         self.places, self.len = _moment_places(self.params)
-        self.bits = 8 if isinstance(self.exp_avg, Blocks8) else 32
-        for name in ("exp_avg", "exp_avg_sq"):
-            m = getattr(self, name)
-            if self.bits == 32:
-                _want(m, name, torch.float32, (self.len,), dev)
-            else:
-                if not isinstance(m, Blocks8):
-                    raise TypeError(f"{name} must be a Blocks8 as exp_avg is")
-                _want(m.q, f"{name}.q", torch.uint8, (self.len,), dev)
-                _want(m.scales, f"{name}.scales", torch.uint8, (self.len // 32,), dev)
-        if self.master is not None:
-            _want(self.master, "master", torch.float32, (self.len,), dev)
-        count = len(self.params)
         self._device = dev
+        self._take_moments()
+        count = len(self.params)
         self._table, self._hyper = (_AdamTensor * count)(), _AdamHyper()
         self._param_ptrs, self._grad_ptrs = (ctypes.c_uint64 * count)(), (ctypes.c_uint64 * count)()
         self._dtypes, self._shapes = [p.dtype for p in self.params], [p.shape for p in self.params]
@@ -1193,12 +1177,34 @@ class AdamW:
         for t, n, at, dtype in zip(self._table, self._sizes, self.places, self._dtypes):
             t.n, t.offset, t.param_dtype = n, at, _LOGITS[dtype]
 
+    def _want_apart(self):
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in self.params if p.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters share memory: each value is stepped once")
+
+    def _take_moments(self):
+        """Addresses of the moments, their scales and the master, checked at every step: a state that is read back may
+        bring its own."""
+        m, v, dev, n = self.exp_avg, self.exp_avg_sq, self._device, self.len
+        self.bits = 8 if isinstance(m, Blocks8) else 32
+        master = None if self.master is None else _want(self.master, "master", torch.float32, (n,), dev).data_ptr()
+        if self.bits == 32:
+            return (_want(m, "exp_avg", torch.float32, (n,), dev).data_ptr(), None,
+                    _want(v, "exp_avg_sq", torch.float32, (n,), dev).data_ptr(), None, master)
+        if not isinstance(v, Blocks8):
+            raise TypeError("exp_avg_sq must be a Blocks8 as exp_avg is")
+        return (_want(m.q, "exp_avg.q", torch.uint8, (n,), dev).data_ptr(),
+                _want(m.scales, "exp_avg.scales", torch.uint8, (n // 32,), dev).data_ptr(),
+                _want(v.q, "exp_avg_sq.q", torch.uint8, (n,), dev).data_ptr(),
+                _want(v.scales, "exp_avg_sq.scales", torch.uint8, (n // 32,), dev).data_ptr(), master)
+
     def _take_params(self):
         """Parameters' addresses, checked again where one has moved."""
         addresses = [p.data_ptr() for p in self.params]
         if addresses != self._addresses or [p.numel() for p in self.params] != self._sizes:
             for i, (p, dtype, shape) in enumerate(zip(self.params, self._dtypes, self._shapes)):
                 _want(p, f"params[{i}]", dtype, tuple(shape), self._device)
+            self._want_apart()
             self._param_ptrs[:] = self._addresses = addresses
 
     def _take_grads(self, grads):
@@ -1272,28 +1278,23 @@ def moe_adamw_step(state: AdamW, grads, *, lr, betas=(0.9, 0.999), eps: float = 
         raise ValueError("seed must fit 32 bits")
     h.lr, (h.beta1, h.beta2), h.eps, h.weight_decay, h.step = lr, betas, eps, weight_decay, step
     h.seed, h.stochastic = (0, 0) if seed is None else (seed, 1)
-    if state.bits == 32:
-        m, ms, v, vs = state.exp_avg.data_ptr(), None, state.exp_avg_sq.data_ptr(), None
-    else:
-        m, ms = state.exp_avg.q.data_ptr(), state.exp_avg.scales.data_ptr()
-        v, vs = state.exp_avg_sq.q.data_ptr(), state.exp_avg_sq.scales.data_ptr()
+    m, ms, v, vs, master = state._take_moments()
     _check(load_library().moe_adamw_step(ctypes.addressof(state._table), ctypes.addressof(state._param_ptrs),
                                          ctypes.addressof(state._grad_ptrs), len(state._sizes), state.bits, state.len, m,
-                                         ms, v, vs, _ptr(state.master), ctypes.addressof(h), lr_ptr, step_ptr, grad_scale,
+                                         ms, v, vs, master, ctypes.addressof(h), lr_ptr, step_ptr, grad_scale,
                                          _stream(state.params[0])), "moe_adamw_step")
 
 
 def moe_adamw_moments(state: AdamW, *, exp_avg=None, exp_avg_sq=None):
     """The values of both moments, [len]: the fp32 buffers themselves, or bf16 of 8-bit ones (one launch)."""
+    m, ms, v, vs, _ = state._take_moments()
     if state.bits == 32:
         return state.exp_avg, state.exp_avg_sq
-    dev = state.exp_avg.q.device
+    dev = state._device
     exp_avg = _out(exp_avg, "exp_avg", torch.bfloat16, (state.len,), dev)
     exp_avg_sq = _out(exp_avg_sq, "exp_avg_sq", torch.bfloat16, (state.len,), dev)
-    _check(load_library().moe_adamw_moments(state.exp_avg.q.data_ptr(), state.exp_avg.scales.data_ptr(),
-                                            state.exp_avg_sq.q.data_ptr(), state.exp_avg_sq.scales.data_ptr(), state.len,
-                                            exp_avg.data_ptr(), exp_avg_sq.data_ptr(), _stream(state.exp_avg.q)),
-           "moe_adamw_moments")
+    _check(load_library().moe_adamw_moments(m, ms, v, vs, state.len, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
+                                            _stream(exp_avg)), "moe_adamw_moments")
     return exp_avg, exp_avg_sq
 
 

@@ -254,6 +254,39 @@ def test_on_another_stream_and_as_parameters():
     assert torch.allclose(p, torch.full_like(p, 0.9), atol=1e-6, rtol=0)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_that_is_read_back(bits):
+    """Moments, master and parameters may be other tensors from one step to the next, if they fit."""
+    a, b = tensors([300, 64], (BF16,), 15), tensors([300, 64], (BF16,), 15)
+    grads = tensors([300, 64], (BF16,), 16)
+    sa, sb = (moe.moe_adamw_state(p, bits=bits, master=True) for p in (a, b))
+    for t in (1, 2, 3):
+        moe.moe_adamw_step(sa, grads, step=t, seed=1, **HYPER)
+        moe.moe_adamw_step(sb, grads, step=t, seed=1, **HYPER)
+        for p in b:
+            p.data = p.data.clone()
+        sb.master = sb.master.clone()
+        for name in ("exp_avg", "exp_avg_sq"):
+            m = getattr(sb, name)
+            setattr(sb, name, m.clone() if bits == 32 else moe.Blocks8(m.q.clone(), m.scales.clone()))
+        assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(sa.master, sb.master)
+    m, short = sb.exp_avg, torch.zeros(96, device="cuda")
+    for other in (short, moe.Blocks8(short.byte(), torch.zeros(3, dtype=torch.uint8, device="cuda")), None,
+                  moe.moe_adamw_state(a, bits=40 - bits).exp_avg):
+        sb.exp_avg = other
+        for call in (lambda: moe.moe_adamw_step(sb, grads, step=4, **HYPER), lambda: moe.moe_adamw_moments(sb)):
+            with pytest.raises((ValueError, TypeError)):
+                call()
+    sb.exp_avg, sb.master = m, short
+    with pytest.raises(ValueError):
+        moe.moe_adamw_step(sb, grads, step=4, **HYPER)
+    sb.master = None
+    flat = torch.zeros(400, dtype=BF16, device="cuda")
+    b[0].data, b[1].data = flat[:300], flat[280:344]
+    with pytest.raises(ValueError):
+        moe.moe_adamw_step(sb, grads, step=4, **HYPER)
+
+
 def test_refusals():
     p, g = tensors([64, 40], (BF16,), 13), tensors([64, 40], (BF16,), 14)
     state = moe.moe_adamw_state(p)

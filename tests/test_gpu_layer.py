@@ -79,6 +79,16 @@ def test_gradients_of_the_whole_layer(stream):
         assert off < 24 * 2.0 ** -8, (name, off)
 
 
+def test_a_layer_without_rows():
+    w = weights(0, 128, 64, 8, BF16, 3)
+    f = forward(w, 2)
+    assert f.r_out.shape == f.n_out.shape == (0, 128)
+    g = moe.moe_layer_backward(w["r"], f, w["w_norm"], w["w_router"], w["w_ug"], w["w_down"], d_n_out=w["r"])
+    assert g["dr"].shape == (0, 128)
+    for name in ("dw_norm", "dw_router", "dw_ug", "dw_down", "dw_post", "dw_next"):
+        assert not g[name].any(), name  # sums over no rows
+
+
 def test_the_layer_is_its_calls():
     T, d, h, E, k = 40, 256, 128, 16, 4
     w = weights(T, d, h, E, BF16, 2)
