@@ -12,10 +12,10 @@
 // v_mfma_f32_16x16x32_bf16: lane l brings 8 values of row l % 16, those of lane quarter l / 16. A
 // lane loads 16 bytes, 32 weights of one row; exchanging dwords between the four quarters makes step s of
 // four cover values 32 s .. 32 s + 31 of a unit of 128, so that groups of 32, 64 and 128 all end with
-// a step. The weights are the second operand, so a lane ends with one weight row and four tokens of a product and
-// needs one scale and one zero a group, which the quarters load one group each and then exchange.
+// a step (wide tiles exchange them through LDS). The weights are the second operand, so a lane ends with one weight
+// row and four tokens of a product and needs one scale and one zero a group.
 
-#include <type_traits>
+#include <cstddef>
 
 #include "grouped.h"
 
@@ -190,12 +190,14 @@ struct WeightRows {
     }
   }
 
+  __device__ __forceinline__ uint32_t block_at(int b, int u) const {
+    return (GATED ? b & 1 : b) * row_bytes + (uint32_t)u * 64;
+  }
+
   __device__ __forceinline__ void load(const Int4Args& g, Unit& d, int u) const {
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const uint32_t at = (GATED ? b & 1 : b) * row_bytes + (uint32_t)u * 64;
-      d.w[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w[GATED ? b >> 1 : 0], w_off, at, 0));
-    }
+    for (int b = 0; b < kBlocks; ++b)
+      d.w[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w[GATED ? b >> 1 : 0], w_off, block_at(b, u), 0));
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       const int64_t skip = (int64_t)u * kGroups * g.w_rows;
@@ -213,53 +215,66 @@ struct WeightRows {
   }
 };
 
-// sum += s (q - z) x over one unit. tokens(m, s): the 8 values of this lane for step s, in the weights' order.
-template <bool GATED, int MB, int GS, class Tokens>
+// What a step of a unit adds to a group's sums: acc of x (16 + q), xs of x.
+template <int MB>
+__device__ __forceinline__ void multiply_step(const bf16x8 (&xv)[MB], const uint32_t (&w)[kBlocks], uint32_t sixteen,
+                                              const bf16x8& ones, f32x4_t (&acc)[kBlocks][MB], f32x4_t (&xs)[MB]) {
+#pragma unroll
+  for (int m = 0; m < MB; ++m) xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], ones, xs[m], 0, 0, 0);
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    const bf16x8 wv = unpack(w[b], sixteen);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], wv, acc[b][m], 0, 0, 0);
+  }
+}
+
+// At a group's end, sum += s (acc - (16 + z) xs).
+template <int MB>
+__device__ __forceinline__ void add_group(const Scales& now, const f32x4_t (&acc)[kBlocks][MB], const f32x4_t (&xs)[MB],
+                                          f32x4_t (&sum)[kBlocks][MB]) {
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    const float scale = b & 1 ? bf16_hi(now.s[b >> 1]) : bf16_lo(now.s[b >> 1]);
+    const float c = 16.0f + (float)((now.z >> (8 * b)) & 0xFFu);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum[b][m][r] = fmaf(scale, fmaf(-c, xs[m][r], acc[b][m][r]), sum[b][m][r]);
+      asm volatile("" : "+v"(sum[b][m]));  // added here: put off to the next unit, it would hold all of acc
+    }
+  }
+}
+
+template <int MB>
+__device__ __forceinline__ void clear_group(f32x4_t (&acc)[kBlocks][MB], f32x4_t (&xs)[MB]) {
+#pragma unroll
+  for (int m = 0; m < MB; ++m) {
+    xs[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) acc[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// sum += s (q - z) x over one unit in registers. tokens(s): the 8 values of this lane for step s, in the weights' order.
+template <bool GATED, int GS, class Tokens>
 __device__ __forceinline__ void multiply_unit(Unit& d, uint32_t no_zeros, const bf16x8& ones, Tokens tokens,
-                                              f32x4_t (&sum)[kBlocks][MB]) {
+                                              f32x4_t (&sum)[kBlocks][1]) {
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) transpose_quarters(d.w[b]);
   const Scales mine = {{d.s[0], d.s[1]}, (GATED ? d.z[0] | d.z[1] << 16 : d.z[0]) | no_zeros};
   Scales sc[2];
   uint32_t sixteen = 0x41804180u;
   asm volatile("" : "+v"(sixteen));
-  f32x4_t acc[kBlocks][MB], xs[MB];
+  f32x4_t acc[kBlocks][1], xs[1];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     if (s % 2 == 0 && (s == 0 || GS < 4)) spread_scales<GS>(mine, s / 2, sc);
-    bf16x8 xv[MB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) xv[m] = tokens(m, s);
-    if (s % GS == 0) {
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        xs[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) acc[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MB; ++m) xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], ones, xs[m], 0, 0, 0);
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const bf16x8 wv = unpack(d.w[b][s], sixteen);
-#pragma unroll
-      for (int m = 0; m < MB; ++m) acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m], wv, acc[b][m], 0, 0, 0);
-    }
-    if (s % GS == GS - 1) {
-      const Scales& now = sc[s & 1];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const float scale = b & 1 ? bf16_hi(now.s[b >> 1]) : bf16_lo(now.s[b >> 1]);
-        const float c = 16.0f + (float)((now.z >> (8 * b)) & 0xFFu);
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sum[b][m][r] = fmaf(scale, fmaf(-c, xs[m][r], acc[b][m][r]), sum[b][m][r]);
-          asm volatile("" : "+v"(sum[b][m]));  // added here: put off to the next unit, it would hold all of acc
-        }
-      }
-    }
+    const bf16x8 xv[1] = {tokens(s)};
+    const uint32_t w[kBlocks] = {d.w[0][s], d.w[1][s], d.w[2][s], d.w[3][s]};
+    if (s % GS == 0) clear_group(acc, xs);
+    multiply_step<1>(xv, w, sixteen, ones, acc, xs);
+    if (s % GS == GS - 1) add_group<1>(sc[s & 1], acc, xs, sum);
     __builtin_amdgcn_sched_barrier(0);  // (a step's operands at a time: unpacked early, they would fill the registers)
   }
 }
@@ -336,7 +351,7 @@ __global__ __launch_bounds__(kThreads, 4) void int4_kernel(Int4Args g) {
         const int k = u * kUnit + s * 32 + quarter * 8;  // (behind the row's end: its last values, multiplied as zeros)
         x[s] = *reinterpret_cast<const u32x4*>(xr + (k < K ? k : K - 8));
       }
-      multiply_unit<GATED, 1, GS>(unit, no_zeros, ones, [&](int, int s) {
+      multiply_unit<GATED, GS>(unit, no_zeros, ones, [&](int s) {
         return pair_up(u * kUnit + s * 32 + quarter * 8 < K ? x[s] : u32x4{0u, 0u, 0u, 0u});
       }, sum);
     }
@@ -353,17 +368,53 @@ __global__ __launch_bounds__(kThreads, 4) void int4_kernel(Int4Args g) {
   }
 }
 
+constexpr int wide_resident(int mb) { return mb == 2 ? 3 : 2; }  // workgroups a CU
+
+// A unit of a wide tile in LDS, brought there by direct loads. Token row t's 16-byte piece c stands at c ^ (t % 16): 16
+// rows' pieces of one c cover all banks. A weight row's quarters stand 256 bytes apart, so the 64 lanes of a step, which
+// read one dword each, cover all banks too. Scales and zeros are the wave's 64 rows' (gated: 32 gate rows, 32 up rows).
+template <int MB, int GS>
+struct WideUnit {
+  static constexpr int kGroups = 4 / GS;
+  u32x4 tokens[16 * MB][16];
+  uint32_t weights[kWaves][kBlocks][64][4];
+  uint16_t scales[kWaves][kGroups][64];
+  uint8_t zeros[kWaves][kGroups][64];
+};
+
+__device__ const u32x4 kZeros16 = {0u, 0u, 0u, 0u};  // what a token has behind its last value
+
+// 16 bytes from each lane's address, 4 through a buffer resource, into LDS as dma16_buf.
+__device__ __forceinline__ void dma16_at(const void* from, uint32_t lds_addr) {
+  lds_addr = __builtin_amdgcn_readfirstlane(lds_addr);
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(from), "s"(lds_addr)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4_buf(__amdgpu_buffer_rsrc_t rsrc, uint32_t off, uint32_t lds_addr) {
+  lds_addr = __builtin_amdgcn_readfirstlane(lds_addr);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(rsrc), "s"(lds_addr)
+               : "memory", "m0");
+}
+
 // More rows an expert: tiles of 16 MB rows by 256 weight rows (gated: 128 columns' gate and up rows), 64 for each of the
-// four waves over the whole contraction. The tokens' values go through LDS, one unit ahead, already in the weights' order.
-// Bound by unpacking (267 vector operations a unit and wave, 40 matrix instructions) and by how evenly the tiles fall on
-// the CUs. Measured: gate/up of 256 tokens, top-8 of 64 experts, skewed, 2048 -> 2 x 768 49 us (with the narrow
-// tiles 57; with the next unit's weights loaded ahead 55 us, two workgroups a CU and no spilled registers 58).
+// four waves over the whole contraction. One unit is multiplied while the next comes into LDS without passing registers.
+// Bound by unpacking (about 250 vector operations a unit and wave, 40 matrix instructions, and as many again a
+// group for its scales) and by how evenly the tiles fall on the CUs. Measured: gate/up of 256 tokens, top-8 of 64 experts,
+// skewed, 2048 -> 2 x 768 45.6 us (narrow tiles 57); units through registers, loaded where they are needed, 49, and 39
+// where this takes 35.7 with 32 rows for each expert. Tried: three or four units in LDS 36.7 us there, and 744 for
+// 618 with 1024 rows (fewer workgroups a CU); a step unpacked between the matrix instructions of the one before 36.4 and
+// 725 (its registers spill).
 template <bool GATED, int MB, int GS>
-__global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(Int4Args g) {
+__global__ __launch_bounds__(kThreads, wide_resident(MB)) void int4_wide_kernel(Int4Args g) {
   constexpr int BM = 16 * MB, kWaveCols = GATED ? 32 : 64, kCols = kWaves * kWaveCols;
-  __shared__ int offs[MOE_MAX_EXPERTS + 1], prefix[MOE_MAX_EXPERTS];
-  // Token row t's 16-byte piece c stands at c ^ (t % 16): 16 rows' pieces of one c cover all banks.
-  __shared__ u32x4 tokens[2][BM][16];
+  typedef WideUnit<MB, GS> Stage;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+  const Stage* ring = reinterpret_cast<const Stage*>(lds);
+  int *offs = reinterpret_cast<int*>(lds + 2 * sizeof(Stage)), *prefix = offs + g.E + 1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int quarter = lane >> 4, r16 = lane & 15;
@@ -375,7 +426,15 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(In
   const int units = (K + kUnit - 1) / kUnit;
   const int groups = (K + 32 * GS - 1) / (32 * GS);
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-  const int piece = tid & 15, slot = tid >> 4;  // of a token row, and which of 16 rows
+  uint32_t sixteen = 0x41804180u;
+  asm volatile("" : "+v"(sixteen));
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
+  // what this lane brings of a unit: 8 values of one token row of 16, scales of 8 weight rows, zeros of 4
+  const int slot = wave * 4 + quarter, value = ((lane & 15) ^ slot) * 8;
+  const uint32_t s_row = GATED ? ((lane & 7) >> 2) * (uint32_t)g.N + (lane & 3) * 8 : (lane & 7) * 8;
+  const uint32_t s_off = ((uint32_t)(lane >> 3) * (uint32_t)g.w_rows + s_row) * 2;
+  const uint32_t z_row = GATED ? ((lane & 15) >> 3) * (uint32_t)g.N + (lane & 7) * 4 : (lane & 15) * 4;
+  const uint32_t z_off = (uint32_t)(lane >> 4) * (uint32_t)g.w_rows + z_row;
 
   for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const uint32_t gm = (uint32_t)(tile / n_tiles);
@@ -399,37 +458,76 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(In
     WeightRows<GATED, GS> rows;
     rows.place(g, e, n0, groups, lane);
 
-    u32x4 next[MB];
-    auto read_tokens = [&](int u) {
-      const int k = u * kUnit + piece * 8;
+    auto stage = [&](int u, int at) {
+      const uint32_t to = lds0 + at * (uint32_t)sizeof(Stage);
 #pragma unroll
-      for (int m = 0; m < MB; ++m) next[m] = *reinterpret_cast<const u32x4*>(xr[m] + (k < K ? k : K - 8));
-    };
-    auto keep_tokens = [&](int u) {
-      const bool in = u * kUnit + piece * 8 < K;
+      for (int b = 0; b < kBlocks; ++b)
+        dma16_buf(rows.w[GATED ? b >> 1 : 0], rows.w_off, rows.block_at(b, u),
+                  to + (uint32_t)offsetof(Stage, weights) + (wave * kBlocks + b) * 1024);
+      const int64_t skip = (int64_t)u * Stage::kGroups * g.w_rows;
+      const auto sr = resource(g.scales + rows.s0[0] + skip, (rows.s_left[0] - skip) * 2);
+      const auto zr = resource(g.zeros + rows.s0[0] + skip, g.zeros != nullptr ? rows.s_left[0] - skip : 0);
+      if (lane < 8 * Stage::kGroups)
+        dma16_buf(sr, s_off, 0, to + (uint32_t)offsetof(Stage, scales) + wave * (Stage::kGroups * 128));
+      if (lane < 16 * Stage::kGroups)
+        dma4_buf(zr, z_off, to + (uint32_t)offsetof(Stage, zeros) + wave * (Stage::kGroups * 64));
+      const int k = u * kUnit + value;
 #pragma unroll
       for (int m = 0; m < MB; ++m)
-        tokens[u & 1][m * 16 + slot][piece ^ slot] = __builtin_bit_cast(u32x4, pair_up(in ? next[m] : u32x4{0u, 0u, 0u, 0u}));
+        dma16_at(k < K ? static_cast<const void*>(xr[m] + k) : &kZeros16, to + (m * 16 + wave * 4) * 256);
     };
+
     f32x4_t sum[kBlocks][MB];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
       for (int m = 0; m < MB; ++m) sum[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](Unit& d, int u) {
-      multiply_unit<GATED, MB, GS>(d, no_zeros, ones, [&](int m, int s) {
-        return __builtin_bit_cast(bf16x8, tokens[u & 1][m * 16 + r16][(s * 4 + quarter) ^ r16]);
-      }, sum);
+
+    auto multiply = [&](const Stage& st) {
+      u32x4 x[2][MB];
+      uint32_t w[2][kBlocks];
+      Scales sc[2];
+      auto read = [&](int s) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) x[s & 1][m] = st.tokens[m * 16 + r16][(s * 4 + quarter) ^ r16];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) w[s & 1][b] = st.weights[wave][b][s * 16 + r16][quarter];
+        if (s % GS == GS - 1) {
+          Scales& v = sc[s & 1];
+          const uint16_t* sp = st.scales[wave][s / GS];
+          const uint8_t* zp = st.zeros[wave][s / GS];
+          if constexpr (GATED) {
+            v.s[0] = reinterpret_cast<const uint32_t*>(sp)[r16], v.s[1] = reinterpret_cast<const uint32_t*>(sp)[16 + r16];
+            v.z = reinterpret_cast<const uint16_t*>(zp)[r16] | (uint32_t)reinterpret_cast<const uint16_t*>(zp)[16 + r16] << 16;
+          } else {
+            const u32x2_t two = reinterpret_cast<const u32x2_t*>(sp)[r16];
+            v.s[0] = two[0], v.s[1] = two[1];
+            v.z = reinterpret_cast<const uint32_t*>(zp)[r16];
+          }
+          v.z |= no_zeros;
+        }
+      };
+      f32x4_t acc[kBlocks][MB], xs[MB];
+      read(0);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s < 3) read(s + 1);
+        bf16x8 xv[MB];
+#pragma unroll
+        for (int m = 0; m < MB; ++m) xv[m] = pair_up(x[s & 1][m]);
+        if (s % GS == 0) clear_group(acc, xs);
+        multiply_step<MB>(xv, w[s & 1], sixteen, ones, acc, xs);
+        if (s % GS == GS - 1) add_group<MB>(sc[s & 1], acc, xs, sum);
+        __builtin_amdgcn_sched_barrier(0);  // (as in multiply_unit)
+      }
     };
 
-    read_tokens(0);
+    stage(0, 0);
     for (int u = 0; u < units; ++u) {
-      Unit unit;
-      rows.load(g, unit, u);
-      keep_tokens(u);
-      lds_barrier();  // unit u is there, and the area of u - 1 is free
-      if (u + 1 < units) read_tokens(u + 1);
-      multiply(unit, u);
+      wait_vmcnt_lds<0>();
+      bare_barrier();  // unit u is there, and the place of u - 1 is free
+      if (u + 1 < units) stage(u + 1, (u + 1) & 1);
+      multiply(ring[u & 1]);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m)
@@ -440,7 +538,7 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 3 : 2) void int4_wide_kernel(In
           store_columns<GATED>(g, row0 + t, n0 + r16 * (kWaveCols / 16),
                                f32x4_t{sum[0][m][r], sum[1][m][r], sum[2][m][r], sum[3][m][r]});
       }
-    lds_barrier();  // (the tokens' last reads, before the next tile's)
+    lds_barrier();  // (the ring's last reads, before the next tile's units)
   }
 }
 
@@ -452,32 +550,41 @@ double expected_tiles(const Int4Args& g, int rows, int cols) {
 }
 
 template <class Kernel>
-hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, int resident, hipStream_t stream) {
+hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, int resident, size_t lds, hipStream_t stream) {
+  if (lds > 64 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
   const int64_t most_experts = g.cap_rows < g.E ? g.cap_rows : g.E;
   const int64_t tiles = (g.cap_rows / rows + most_experts) * ((g.N + cols - 1) / cols);
   const int64_t fit = (int64_t)device_cu_count(current_device()) * resident;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), 0, stream, g);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kThreads), lds, stream, g);
   return hipGetLastError();
 }
 
-// The kind of tile whose estimated time in us is least. Narrow tiles (four resident a CU) wait 3 us for each unit of
-// their longest wave; a wide one waits for each unit of the contraction, 1.85 us with 32 rows and 2.65 with 64, or as
-// long as the tiles of a CU take to unpack, 1.0 and 1.7 us a tile. Over 110 calls (1 to 128 experts, 16 to 65536 rows,
-// 64 to 3128 values by 64 to 3120 columns) the choice takes 0.4% longer than the best one in the mean, 9% at worst; by
-// the mean of the rows per expert alone (up to 16, up to 48, above) it took 33% longer. 64 experts of 2048 -> 2 x 768
-// with 16, 32, 64 and 128 rows each: narrow 34, 54, 101, 191 us; 32 rows 38, 39, 61, 123; 64 rows -, -, 56, 90.
+// The kind of tile whose estimated time in us is least. Narrow tiles (four resident a CU) wait 2.8 us for each unit of
+// their longest wave; a wide one waits for each unit of the contraction, 1.2 us with 32 rows and 2.5 with 64, or as
+// long as the tiles of a CU take to unpack, 1.0 and 1.65 us a tile. Over 90 calls (1 to 128 experts, 16 to 4096 rows, 64 to
+// 3200 values by 64 to 3200 columns, even and skewed) the choice takes 0.5% longer than the best one in the mean, 14%
+// at worst; by the mean of the rows per expert alone (up to 16, up to 48, above) it took 33% longer. 64 experts of
+// 2048 -> 2 x 768 in groups of 128 with 16, 32, 64, 128 and 1024 rows each: 35, 36, 58, 90 and 618 us.
 template <bool GATED, int GS>
 hipError_t launch_rows(const Int4Args& g, hipStream_t stream) {
   constexpr int kOut = GATED ? 32 : 64;
   const double cus = (double)device_cu_count(current_device()), units = (double)((g.K + kUnit - 1) / kUnit);
   auto larger = [](double a, double b) { return a > b ? a : b; };
   const double longest = (double)(((g.K + kUnit - 1) / kUnit + kWaves - 1) / kWaves);
-  const double narrow = larger(1.0, expected_tiles(g, 16, kOut) / (4 * cus)) * (1.0 + 3.0 * longest);
-  const double wide32 = 3.0 + units * larger(1.85, 1.0 * expected_tiles(g, 32, 4 * kOut) / cus);
-  const double wide64 = 6.0 + units * larger(2.65, 1.7 * expected_tiles(g, 64, 4 * kOut) / cus);
-  if (narrow <= wide32 && narrow <= wide64) return launch_tiles(int4_kernel<GATED, GS>, g, 16, kOut, 4, stream);
-  if (wide32 <= wide64) return launch_tiles(int4_wide_kernel<GATED, 2, GS>, g, 32, 4 * kOut, 3, stream);
-  return launch_tiles(int4_wide_kernel<GATED, 4, GS>, g, 64, 4 * kOut, 2, stream);
+  const double narrow = larger(1.0, expected_tiles(g, 16, kOut) / (4 * cus)) * (1.0 + 2.8 * longest);
+  const double wide32 = 3.0 + units * larger(1.2, 1.0 * expected_tiles(g, 32, 4 * kOut) / cus);
+  const double wide64 = 2.7 + units * larger(2.5, 1.65 * expected_tiles(g, 64, 4 * kOut) / cus);
+  if (narrow <= wide32 && narrow <= wide64) return launch_tiles(int4_kernel<GATED, GS>, g, 16, kOut, 4, 0, stream);
+  const size_t tables = (2 * g.E + 1) * sizeof(int);
+  if (wide32 <= wide64)
+    return launch_tiles(int4_wide_kernel<GATED, 2, GS>, g, 32, 4 * kOut, wide_resident(2),
+                        2 * sizeof(WideUnit<2, GS>) + tables, stream);
+  return launch_tiles(int4_wide_kernel<GATED, 4, GS>, g, 64, 4 * kOut, wide_resident(4),
+                      2 * sizeof(WideUnit<4, GS>) + tables, stream);
 }
 
 template <bool GATED>

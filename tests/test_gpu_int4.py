@@ -155,7 +155,7 @@ def test_gate_up(T, k, E, d, h, group, zeros, gather):
     up(T, k, p / p.sum(), E, d, h, group, zeros, drop=True, gather=gather)
 
 
-@pytest.mark.parametrize("rows", [4000, 10000])  # tiles of 32 and of 64 rows
+@pytest.mark.parametrize("rows", [1000, 4000, 10000])  # tiles of 32 and, twice, of 64 rows
 @pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
 @pytest.mark.parametrize("K", [264, 512])
 def test_wide_tiles(rows, group, zeros, K):
