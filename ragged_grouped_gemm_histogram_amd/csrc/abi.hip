@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "common.h"
+#include "norm.h"
 #include "mxfp4.h"
 
 namespace moe {

@@ -121,16 +121,15 @@ hipError_t launch_gemm_up_swiglu_mxfp4(const uint8_t* x_q, const uint8_t* x_s, i
                                        int64_t cap_rows, int64_t d, int64_t h, int32_t E, uint16_t* h_buf, uint8_t* h_q,
                                        uint8_t* h_s, hipStream_t stream);  // to h_buf, or without one to h_q and h_s
 
-// Norms around a block. The backward leaves norm_partial_rows(T, d) rows of up to three partial column sums.
-int64_t norm_partial_rows(int64_t T, int64_t d);
+// Norms around a block.
 hipError_t launch_norm(const void* r, bool r_f32, const uint16_t* y, const void* w_post, const void* w_next,
                        const void* gate, int gate_kind, bool w_f32, bool post, bool next, float a, float b, float eps,
                        int64_t T, int64_t d, void* r_out, uint16_t* n_out, hipStream_t stream);  // without y: before
-hipError_t launch_norm_backward(const void* dr, const uint16_t* dn, const uint16_t* dn_add, const uint16_t* y, const void* r,
-                                bool r_f32, const void* w_post, const void* w_next, const void* gate, int gate_kind,
-                                bool w_f32, bool branch, bool post, bool next, float a, float b, float eps, int64_t T, int64_t d,
-                                void* dr_out, uint16_t* dy, float* d_gate, float* d_w_post, float* d_w_next,
-                                float* partial, hipStream_t stream);
+hipError_t launch_norm_backward(const void* dr, const uint16_t* dn, const uint16_t* dn_add, const uint16_t* y,
+                                const void* r, bool r_f32, const void* w_post, const void* w_next, const void* gate,
+                                int gate_kind, bool w_f32, bool branch, bool post, bool next, float a, float b, float eps,
+                                int64_t T, int64_t d, void* dr_out, uint16_t* dy, float* d_gate, float* d_w_post,
+                                float* d_w_next, float* partial, hipStream_t stream);
 
 // AdamW.
 hipError_t launch_adamw(const moe_adamw_tensor* list, void* const* params, const void* const* grads, int32_t count,

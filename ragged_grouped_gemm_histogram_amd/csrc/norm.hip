@@ -29,6 +29,7 @@
 // registers to read ahead, and some spill. Small calls wait for one chain of load, sum and store, 3 us, and the backward's second launch.
 
 #include "common.h"
+#include "norm.h"
 
 namespace moe {
 namespace {
