@@ -4,7 +4,11 @@
 //   p = (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // all in fp32 (gradients are read as they are, parameters from their fp32 copy where there is one). Bound
-// by HBM: 28 bytes a value with bf16 parameters, fp32 copies and moments, 10 with 8-bit moments alone.
+// by HBM: 28 bytes a value with bf16 parameters, fp32 copies and moments, 10 with 8-bit moments alone. Measured, bf16
+// parameters and gradients: 398 M values with fp32 copies and moments 2174 us (5.1 TB/s; a copy of 2 GiB runs at 4.9),
+// 302 M with 8-bit moments and random rounding 565 to 585 us (5.2 to 5.4 TB/s), the moments' values as bf16 370 (5.0).
+// Steps that brought it there: a pass's loads before the step of the one before, 2268 to 2215 and 743 to 616 us; whole
+// lines read and written past the caches, 2215 to 2175 and 616 to 575.
 //
 // Moments in 8 bits: 32 consecutive values share a power of two 2^(byte - 127). The first moment is
 // float8 e4m3, the block's largest magnitude in [128, 256) so that nothing saturates, to nearest even. The

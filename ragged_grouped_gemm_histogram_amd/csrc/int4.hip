@@ -549,11 +549,14 @@ double expected_tiles(const Int4Args& g, int rows, int cols) {
   return (by_rows > experts ? by_rows : experts) * (double)((g.N + cols - 1) / cols);
 }
 
+// LDS of a wide tile with the tables of as many experts as there can be (the same for every call: two may run at once).
+constexpr int kMostLds = 2 * (int)sizeof(WideUnit<4, 1>) + (2 * MOE_MAX_EXPERTS + 1) * (int)sizeof(int);
+
 template <class Kernel>
 hipError_t launch_tiles(Kernel kernel, const Int4Args& g, int rows, int cols, int resident, size_t lds, hipStream_t stream) {
   if (lds > 64 * 1024) {
     const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
     if (e != hipSuccess) return e;
   }
   const int64_t most_experts = g.cap_rows < g.E ? g.cap_rows : g.E;
