@@ -120,7 +120,8 @@ __device__ __forceinline__ void find_tile(const Finder& f, int E, uint32_t tile,
   const uint32_t base = __builtin_amdgcn_readlane(f.first, owner);
   const int at = owner * f.per + (lane < f.per ? lane : f.per - 1);
   const uint32_t mine = at < E ? (uint32_t)f.prefix[at] : ~0u;
-  const int in = __popcll(__ballot(lane < f.per && mine <= tile - base)) - 1;
+  // (an expert below E whatever the counts have wrapped to: a lane's first prefix is 0)
+  const int in = __popcll(__ballot(lane < f.per && at < E && mine <= tile - base)) - 1;
   e = owner * f.per + in;
   begin = base + __builtin_amdgcn_readlane(mine, in);
 }

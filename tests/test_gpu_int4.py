@@ -170,6 +170,39 @@ def test_many_experts():
         projection(rng.integers(0, 3, E).tolist(), 32, 8, 32, False)
 
 
+@pytest.mark.parametrize("rows", [40000, 70000])  # tiles of 32 and of 64 rows, tables of as many experts as there can be
+def test_wide_tiles_of_many_experts(rows):
+    rng = np.random.default_rng(rows)
+    p = np.arange(1, 1025) ** -0.5
+    projection(rng.multinomial(rows, p / p.sum()).tolist(), 64, 64, 32, True, spare=5)
+
+
+@pytest.mark.parametrize("rows", [40, 1000, 10000])  # each kind of tile
+def test_what_is_not_finite_stays_in_its_row_and_column(rows):
+    m, _ = weights(2, 2056, 264, 64, True)
+    x, off = normal((rows, 264), 20), offsets([rows // 2, rows - rows // 2])
+    clean = moe.moe_grouped_projection_int4(x, off, m)
+    x[3, 7], x[rows - 2, 263] = float("nan"), float("inf")
+    m.scales[1, 4, 2050] = float("nan")
+    got = moe.moe_grouped_projection_int4(x, off, m)
+    assert torch.isnan(got[[3, rows - 2]]).all() and torch.isnan(got[rows // 2:, 2050]).all()
+    keep = torch.ones_like(got, dtype=torch.bool)
+    keep[[3, rows - 2]] = False
+    keep[rows // 2:, 2050] = False
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("rows", [1000, 10000])
+def test_bad_offsets_stay_inside_wide_tiles(rows):
+    m, ref = weights(3, 2056, 264, 32, True)
+    x, y = normal((rows, 264), 21), torch.full((rows, 2056), 7.0, dtype=BF16, device="cuda")
+    off = torch.tensor([-9, rows - 100, rows // 2, 1 << 30], dtype=torch.int32, device="cuda")
+    moe.moe_grouped_projection_int4(x, off, m, y=y)
+    want = moe.moe_grouped_projection_int4(x, torch.tensor([0, rows // 2, rows // 2, rows], dtype=torch.int32, device="cuda"), m)
+    # rows from rows / 2 to rows - 100 belong to two experts
+    assert torch.equal(y[:rows // 2], want[:rows // 2]) and torch.equal(y[rows - 100:], want[rows - 100:])
+
+
 def test_bad_offsets_stay_inside():
     """Offsets past the capacity are cut, an expert whose end precedes its start is empty, and nothing else is written."""
     m, ref = weights(3, 16, 32, 32, True)
