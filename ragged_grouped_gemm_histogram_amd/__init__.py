@@ -1200,8 +1200,8 @@ class AdamW:
 
     def _take_params(self):
         """Parameters' addresses, checked again where one has moved."""
-        addresses = [p.data_ptr() for p in self.params]
-        if addresses != self._addresses or [p.numel() for p in self.params] != self._sizes:
+        addresses = list(map(_Tensor.data_ptr, self.params))
+        if addresses != self._addresses or list(map(_Tensor.numel, self.params)) != self._sizes:
             for i, (p, dtype, shape) in enumerate(zip(self.params, self._dtypes, self._shapes)):
                 _want(p, f"params[{i}]", dtype, tuple(shape), self._device)
             self._want_apart()
@@ -1222,11 +1222,11 @@ class AdamW:
                 t.grad_dtype = _LOGITS[dtype]
             self._grad_dtypes = dtypes
         index = self._device.index
-        if ([g.shape for g in grads] != self._shapes or [g.get_device() for g in grads] != [index] * len(grads)
-                or False in [g.is_contiguous() for g in grads]):
+        if ([g.shape for g in grads] != self._shapes or list(map(_Tensor.get_device, grads)) != [index] * len(grads)
+                or False in map(_Tensor.is_contiguous, grads)):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):  # (names the one that does not fit)
                 _want(g, f"grads[{i}]", g.dtype, tuple(shape), self._device)
-        self._grad_ptrs[:] = [g.data_ptr() for g in grads]
+        self._grad_ptrs[:] = list(map(_Tensor.data_ptr, grads))
 
 
 def moe_adamw_state(params, *, bits: int = 32, master: bool = False) -> AdamW:
