@@ -316,7 +316,7 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
   float* w_lds = reinterpret_cast<float*>(lds);  // the weights in the order of their sums as fp32, 0 past the last column
   constexpr int kRows = 64 / LANES;  // rows of a team's turn
   const int waves = g.team_waves, span = LANES == 64 ? 64 * waves : LANES, padded = span * 8 * V;
-  const int team = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / waves;  // the same for a whole wave
+  const int team = __builtin_amdgcn_readfirstlane(((int)threadIdx.x >> 6) / waves);  // (divided in vector registers: rows and addresses of rows shall be scalar)
   const int at = LANES == 64 ? (int)threadIdx.x - team * span : (int)threadIdx.x & (LANES - 1);
   const int sub = LANES == 64 ? 0 : ((int)threadIdx.x & 63) / LANES;  // this lane's row of the turn
   const float inv_d = 1.0f / (float)g.d;
@@ -380,7 +380,8 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
     }
   };
 
-  constexpr bool kKeep = WIDE;  // a row is widened again for its second use: held in fp32 over the sums, it would spill
+  // a row is widened again for its second use: held in fp32 over the sums, it would spill
+  constexpr bool kKeep = WIDE;
   int buf = 0;
   auto compute = [&](BackRow<S, V>& row, int64_t t) {
     // (the weights are read from LDS again for each use: kept over the rows, they would fill the registers)
@@ -421,11 +422,12 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
     }
     if (NEXT || POST || token) team_sum<LANES>(s, red, buf, waves, team * waves);
     const bool live = t + sub < g.T;
-    // (a row that is not there has zeros for its sums: no factor of it may be infinite)
-    const float k1 = NEXT && live ? rsqrtf(fmaf(s[0], inv_d, g.eps)) : 0.0f;
+    // (a row that is not there has zeros for its sums: beside others in a wave no factor of it may be infinite)
+    const bool there = LANES == 64 || live;
+    const float k1 = NEXT && there ? rsqrtf(fmaf(s[0], inv_d, g.eps)) : 0.0f;
     const float k2 = k1 * s[1] * inv_d * k1 * k1;
     const float qg = s[3] + k1 * s[4] - k2 * s[5];  // sum of q g
-    const float rsy = POST ? (live ? rsqrtf(fmaf(s[2], inv_d, g.eps)) : 0.0f) : 1.0f;
+    const float rsy = POST ? (there ? rsqrtf(fmaf(s[2], inv_d, g.eps)) : 0.0f) : 1.0f;
     float bt = g.b;
     if constexpr (BRANCH && !CHANNEL) bt = token ? g.b * row.gate : g.b;
     const float p1 = rsy * bt, p2 = rsy * qg * inv_d * rsy * rsy * bt;
@@ -473,10 +475,12 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
       }
       write8(dr_row, column(j), dx, S{});
       if constexpr (BRANCH) write8(dy_row, column(j), dy, uint16_t{});
+      if constexpr (LANES < 64 || V > 1) {
 #pragma unroll
-      for (int k = 0; k < kCols; ++k)
+        for (int k = 0; k < kCols; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(acc[k][j][i]));  // added here, not put off behind the next row
+          for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(acc[k][j][i]));  // added here, not put off behind the next row
+      }
       if constexpr (V > 1) {
         asm volatile("" : : : "memory");
         __builtin_amdgcn_sched_barrier(0);
@@ -485,7 +489,7 @@ __global__ __launch_bounds__(64 * (WIDE ? kMaxWaves : kBackWaves), 4) void norm_
   };
 
   // every workgroup's turn: rows t0 on, kRows of them a team; a team without a row goes along, for the barriers
-  const int teams = WIDE ? 1 : (int)blockDim.x / (64 * waves), mine = team * kRows;
+  const int teams = WIDE ? 1 : __builtin_amdgcn_readfirstlane((int)blockDim.x / (64 * waves)), mine = team * kRows;
   const int64_t turn = (int64_t)gridDim.x * teams * kRows;
   int64_t t0 = (int64_t)blockIdx.x * teams * kRows;
   if constexpr (V > 1 || LANES < 64) {
