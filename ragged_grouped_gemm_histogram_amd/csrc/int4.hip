@@ -18,6 +18,7 @@
 #include <cstddef>
 
 #include "grouped.h"
+#include "int4.h"
 
 namespace moe {
 namespace {
@@ -39,8 +40,6 @@ struct Int4Args {
   int64_t cap_rows;
   uint16_t* out;            // [cap_rows, N]
 };
-
-inline __host__ __device__ int64_t int4_row_bytes(int64_t K) { return 16 * ((K + 31) / 32); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __builtin_bit_cast(float, x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __builtin_bit_cast(float, x & 0xFFFF0000u); }
@@ -72,8 +71,8 @@ __device__ __forceinline__ void transpose_quarters(u32x4& w) {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kUnit = 128;
-constexpr int kBlocks = 4;  // blocks of 16 weight rows of a tile
+constexpr int kUnit = kInt4Unit;
+constexpr int kBlocks = kInt4Blocks;  // blocks of 16 weight rows of a tile
 
 __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t cap) { return v < 0 ? 0 : (v > cap ? cap : v); }
 
@@ -182,17 +181,18 @@ struct WeightRows {
     row_bytes = (uint32_t)int4_row_bytes(g.K);
     w_off = first * row_bytes + quarter * 16;
     s_off = (uint32_t)(quarter / GS) * (uint32_t)g.w_rows + first;
+    n0 = int4_first_column(n0, g.N);
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       const int64_t r0 = n0 + p * g.N;
-      w[p] = resource(g.q + ((int64_t)e * g.w_rows + r0) * row_bytes, (g.w_rows - r0) * row_bytes);
+      w[p] = resource(g.q + ((int64_t)e * g.w_rows + r0) * row_bytes, int4_bytes_left(g.w_rows, r0, row_bytes));
       s0[p] = uniform_i64((int64_t)e * groups * g.w_rows + r0);
       s_left[p] = uniform_i64((int64_t)groups * g.w_rows - r0);
     }
   }
 
   __device__ __forceinline__ uint32_t block_at(int b, int u) const {
-    return (GATED ? b & 1 : b) * row_bytes + (uint32_t)u * 64;
+    return int4_block_at(GATED, b, u, row_bytes);
   }
 
   __device__ __forceinline__ void load(const Int4Args& g, Unit& d, int u) const {
