@@ -1199,10 +1199,15 @@ class AdamW:
                 _want(v.scales, "exp_avg_sq.scales", torch.uint8, (n // 32,), dev).data_ptr(), master)
 
     def _take_params(self):
-        """Parameters' addresses, checked again where one has moved."""
-        addresses = list(map(_Tensor.data_ptr, self.params))
-        if addresses != self._addresses or list(map(_Tensor.numel, self.params)) != self._sizes:
-            for i, (p, dtype, shape) in enumerate(zip(self.params, self._dtypes, self._shapes)):
+        """Parameters' addresses. Where a value stands follows from address, size, type and contiguity; if any of them
+        has changed, all is checked again."""
+        params = self.params
+        addresses = list(map(_Tensor.data_ptr, params))
+        if (addresses != self._addresses or list(map(_Tensor.numel, params)) != self._sizes
+                or [p.dtype for p in params] != self._dtypes or False in map(_Tensor.is_contiguous, params)):
+            if len(params) != len(self._sizes):
+                raise ValueError(f"the state is of {len(self._sizes)} parameters, not {len(params)}")
+            for i, (p, dtype, shape) in enumerate(zip(params, self._dtypes, self._shapes)):
                 _want(p, f"params[{i}]", dtype, tuple(shape), self._device)
             self._want_apart()
             self._param_ptrs[:] = self._addresses = addresses
@@ -1210,9 +1215,9 @@ class AdamW:
     def _take_grads(self, grads):
         if len(grads) != len(self._sizes):
             raise ValueError(f"{len(self._sizes)} parameters but {len(grads)} gradients")
-        for i, g in enumerate(grads):
-            if not isinstance(g, _Tensor):
-                raise TypeError(f"grads[{i}] must be a torch.Tensor")
+        if not all(issubclass(t, _Tensor) for t in set(map(type, grads))):
+            i = next(i for i, g in enumerate(grads) if not isinstance(g, _Tensor))
+            raise TypeError(f"grads[{i}] must be a torch.Tensor")
         dtypes = [g.dtype for g in grads]
         if dtypes != self._grad_dtypes:
             for i, dtype in enumerate(dtypes):
@@ -1222,7 +1227,7 @@ class AdamW:
                 t.grad_dtype = _LOGITS[dtype]
             self._grad_dtypes = dtypes
         index = self._device.index
-        if ([g.shape for g in grads] != self._shapes or list(map(_Tensor.get_device, grads)) != [index] * len(grads)
+        if (list(map(_Tensor.size, grads)) != self._shapes or list(map(_Tensor.get_device, grads)) != [index] * len(grads)
                 or False in map(_Tensor.is_contiguous, grads)):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):  # (names the one that does not fit)
                 _want(g, f"grads[{i}]", g.dtype, tuple(shape), self._device)
