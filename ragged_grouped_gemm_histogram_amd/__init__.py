@@ -1145,7 +1145,7 @@ def _moment_places(params) -> tuple[list[int], int]:
 class AdamW:
     """What AdamW keeps for a list of parameters: one buffer a moment, fp32 [len] or Blocks8 of len values, with tensor
     i's values from ``places[i]`` on (the sizes before it, each rounded up to 32), and with ``master`` a fp32 copy of
-    the parameters at the same places. moe_adamw_state makes one."""
+    the parameters at the same places. None of them may share memory. moe_adamw_state makes one."""
     params: list
     exp_avg: torch.Tensor | Blocks8
     exp_avg_sq: torch.Tensor | Blocks8
@@ -1163,10 +1163,10 @@ class AdamW:
             if not isinstance(p, torch.Tensor) or p.dtype not in _LOGITS:
                 raise TypeError(f"params[{i}] must be a bfloat16 or float32 tensor")
             _want(p, f"params[{i}]", p.dtype, tuple(p.shape), dev)
-        self._want_apart()
         self.places, self.len = _moment_places(self.params)
         self._device = dev
-        self._take_moments()
+        self._moments = self._take_moments()
+        self._want_apart(self._moments)
         count = len(self.params)
         self._table, self._hyper = (_AdamTensor * count)(), _AdamHyper()
         self._param_ptrs, self._grad_ptrs = (ctypes.c_uint64 * count)(), (ctypes.c_uint64 * count)()
@@ -1177,10 +1177,14 @@ class AdamW:
         for t, n, at, dtype in zip(self._table, self._sizes, self.places, self._dtypes):
             t.n, t.offset, t.param_dtype = n, at, _LOGITS[dtype]
 
-    def _want_apart(self):
-        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in self.params if p.numel())
+    def _want_apart(self, moments):
+        n, wide = self.len, 4 if self.bits == 32 else 1
+        sizes = (wide * n, n // 32, wide * n, n // 32, 4 * n)
+        spans = [(p.data_ptr(), p.numel() * p.element_size()) for p in self.params]
+        spans += [(at, size) for at, size in zip(moments, sizes) if at is not None]
+        spans = sorted((at, at + size) for at, size in spans if size)
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("parameters share memory: each value is stepped once")
+            raise ValueError("parameters, moments or the master share memory: each value is stepped once")
 
     def _take_moments(self):
         """Addresses of the moments, their scales and the master, checked at every step: a state that is read back may
@@ -1199,18 +1203,21 @@ class AdamW:
                 _want(v.scales, "exp_avg_sq.scales", torch.uint8, (n // 32,), dev).data_ptr(), master)
 
     def _take_params(self):
-        """Parameters' addresses. Where a value stands follows from address, size, type and contiguity; if any of them
-        has changed, all is checked again."""
-        params = self.params
+        """The parameters' addresses into their table; returns the moments'. Where a value stands follows from address, size,
+        type and contiguity; if any of them has changed, all is checked again."""
+        params, moments = self.params, self._take_moments()
         addresses = list(map(_Tensor.data_ptr, params))
         if (addresses != self._addresses or list(map(_Tensor.numel, params)) != self._sizes
-                or [p.dtype for p in params] != self._dtypes or False in map(_Tensor.is_contiguous, params)):
+                or [p.dtype for p in params] != self._dtypes or False in map(_Tensor.is_contiguous, params)
+                or moments != self._moments):
             if len(params) != len(self._sizes):
                 raise ValueError(f"the state is of {len(self._sizes)} parameters, not {len(params)}")
             for i, (p, dtype, shape) in enumerate(zip(params, self._dtypes, self._shapes)):
                 _want(p, f"params[{i}]", dtype, tuple(shape), self._device)
-            self._want_apart()
+            self._want_apart(moments)
             self._param_ptrs[:] = self._addresses = addresses
+            self._moments = moments
+        return moments
 
     def _take_grads(self, grads):
         if len(grads) != len(self._sizes):
@@ -1269,7 +1276,7 @@ def moe_adamw_step(state: AdamW, grads, *, lr, betas=(0.9, 0.999), eps: float = 
     number or a fp32 [1] tensor on the device, ``step`` an int or an int32 [1] tensor, for steps captured in a graph;
     ``grad_scale`` fp32 [1] is multiplied to the gradients (a clipping factor). A ``seed`` rounds the second moment in 8
     bits, and bf16 parameters without a master, at random in proportion; without one they round to nearest."""
-    state._take_params()
+    m, ms, v, vs, master = state._take_params()
     state._take_grads(grads)
     dev, h = state._device, state._hyper
     lr_ptr = step_ptr = None
@@ -1283,7 +1290,6 @@ def moe_adamw_step(state: AdamW, grads, *, lr, betas=(0.9, 0.999), eps: float = 
         raise ValueError("seed must fit 32 bits")
     h.lr, (h.beta1, h.beta2), h.eps, h.weight_decay, h.step = lr, betas, eps, weight_decay, step
     h.seed, h.stochastic = (0, 0) if seed is None else (seed, 1)
-    m, ms, v, vs, master = state._take_moments()
     _check(load_library().moe_adamw_step(ctypes.addressof(state._table), ctypes.addressof(state._param_ptrs),
                                          ctypes.addressof(state._grad_ptrs), len(state._sizes), state.bits, state.len, m,
                                          ms, v, vs, master, ctypes.addressof(h), lr_ptr, step_ptr, grad_scale,

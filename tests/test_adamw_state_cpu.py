@@ -71,3 +71,47 @@ def test_gradients_that_are_no_tensors_are_named():
     for bad in (None, [1.0], 3):
         with pytest.raises(TypeError, match=r"grads\[1\]"):
             s._take_grads([torch.zeros(4, 4), bad])
+
+
+def blocks(memory, at):
+    """8-bit moments of 64 values in 66 bytes of `memory`."""
+    return moe.Blocks8(memory[at:at + 64], memory[at + 64:at + 66])
+
+
+def test_buffers_that_share_memory_are_refused():
+    p, m = [torch.zeros(64)], torch.zeros(256)
+    apart = (m[:64], m[64:128], m[128:192])
+    moe.AdamW(p, *apart)
+    for args in ((m[:64], m[:64]), (m[:64], m[32:96]), (m[:64], m[64:128], m[64:128]), (m[:64], m[64:128], m[127:191]),
+                 (p[0], m[:64]), (m[:64], p[0]), (m[:64], m[64:128], p[0])):
+        with pytest.raises(ValueError, match="share memory"):
+            moe.AdamW(p, *args)
+    b = torch.zeros(192, dtype=torch.uint8)
+    moe.AdamW(p, blocks(b, 0), blocks(b, 66))
+    for args in ((blocks(b, 0), blocks(b, 0)), (blocks(b, 0), blocks(b, 65)),
+                 (moe.Blocks8(b[:64], b[64:66]), moe.Blocks8(b[66:130], b[64:66])),
+                 (blocks(b, 0), blocks(b, 66), b.new_zeros(256).view(F32)[:64])):
+        if len(args) == 3:  # (apart: taken)
+            moe.AdamW(p, *args)
+            continue
+        with pytest.raises(ValueError, match="share memory"):
+            moe.AdamW(p, *args)
+
+
+def test_buffers_that_come_to_share_memory_are_refused():
+    s = state((64,), (8, 3), master=True)
+    s._take_params()
+    m, master = s.exp_avg, s.master
+    s.exp_avg = s.exp_avg_sq
+    with pytest.raises(ValueError, match="share memory"):
+        s._take_params()
+    with pytest.raises(ValueError, match="share memory"):  # and again
+        s._take_params()
+    s.exp_avg = m
+    s._take_params()
+    s.params[0].data = master[:64]
+    with pytest.raises(ValueError, match="share memory"):
+        s._take_params()
+    # all at once: what was a moment's memory is a parameter's now
+    s.params[0].data, s.exp_avg = s.exp_avg[:64], torch.zeros(96)
+    s._take_params()
