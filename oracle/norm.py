@@ -40,14 +40,23 @@ def through_norm(x, w, dn, eps):
     return dx, mag, dn * x * s
 
 
+def through_wide_norm(x, w, dn, eps):
+    """through_norm for rows whose d x d Jacobian would be too large: its product with h, written out."""
+    s = rs(x, eps)
+    h = dn * w
+    dx = s * (h - x * s ** 2 * (h * x).mean(axis=1, keepdims=True))
+    mag = s * (np.abs(h) + np.abs(x) * s ** 2 * np.abs(h * x).mean(axis=1, keepdims=True))
+    return dx, mag, dn * x * s
+
+
 def backward(d_r, d_n, r_out, y=None, *, post=False, w_post=1.0, gate=1.0, a=1.0, b=1.0, nxt=True, w_next=1.0, eps=1e-6,
-             gate_kind="none"):
+             gate_kind="none", through=through_norm):
     """dict of name -> (gradient, magnitudes): r, and y, gate, w_post, w_next where there are any."""
     out = {}
     g = np.zeros_like(r_out) if d_r is None else d_r
     mag = np.abs(g)
     if nxt:
-        dx, m, terms = through_norm(r_out, w_next, d_n, eps)
+        dx, m, terms = through(r_out, w_next, d_n, eps)
         g, mag = g + dx, mag + m
         out["w_next"] = terms.sum(0), np.abs(terms).sum(0)
     out["r"] = a * g, abs(a) * mag
@@ -60,7 +69,7 @@ def backward(d_r, d_n, r_out, y=None, *, post=False, w_post=1.0, gate=1.0, a=1.0
         out["gate"] = b * (g * u).sum(0), abs(b) * (mag * np.abs(u)).sum(0)
     du, m = b * gate * g, np.abs(b * gate) * mag
     if post:
-        dy, my, terms = through_norm(y, w_post, du, eps)
+        dy, my, terms = through(y, w_post, du, eps)
         s = rs(y, eps)
         out["w_post"] = terms.sum(0), (m * np.abs(y) * s).sum(0)
         w = np.abs(w_post)
