@@ -1222,9 +1222,11 @@ class AdamW:
     def _take_grads(self, grads):
         if len(grads) != len(self._sizes):
             raise ValueError(f"{len(self._sizes)} parameters but {len(grads)} gradients")
-        if not all(issubclass(t, _Tensor) for t in set(map(type, grads))):
+        try:
+            addresses = list(map(_Tensor.data_ptr, grads))
+        except TypeError:
             i = next(i for i, g in enumerate(grads) if not isinstance(g, _Tensor))
-            raise TypeError(f"grads[{i}] must be a torch.Tensor")
+            raise TypeError(f"grads[{i}] must be a torch.Tensor") from None
         dtypes = [g.dtype for g in grads]
         if dtypes != self._grad_dtypes:
             for i, dtype in enumerate(dtypes):
@@ -1238,7 +1240,7 @@ class AdamW:
                 or False in map(_Tensor.is_contiguous, grads)):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):  # (names the one that does not fit)
                 _want(g, f"grads[{i}]", g.dtype, tuple(shape), self._device)
-        self._grad_ptrs[:] = list(map(_Tensor.data_ptr, grads))
+        self._grad_ptrs[:] = addresses
 
 
 def moe_adamw_state(params, *, bits: int = 32, master: bool = False) -> AdamW:
