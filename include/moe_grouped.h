@@ -604,7 +604,7 @@ typedef struct moe_adamw_hyper {
  *   params, grads  each tensor's values, aligned to their element size (16 bytes
  *                  let whole vectors be read)
  *   len            values the moments' buffers hold, a multiple of 32
- *   master         fp32 [len] or NULL
+ *   master         fp32 [len] or NULL; parameters, moments, scales and master may not overlap
  *   lr_ptr         fp32 [1] on the device: the rate instead of hyper->lr; or NULL
  *   step_ptr       int32 [1] on the device: t instead of hyper->step; or NULL
  *   grad_scale     fp32 [1] on the device, multiplied to every gradient; or NULL

@@ -893,7 +893,8 @@ def moe_gemm_up_swiglu_int4(x: torch.Tensor, offsets: torch.Tensor, w_ug: Int4, 
 def moe_expert_forward_int4(x: torch.Tensor, expert_ids: torch.Tensor, routing_w: torch.Tensor, w_ug: Int4,
                             w_down: Int4):
     """The whole step on 4-bit experts, from bf16 token rows. ``w_ug`` holds [E, 2h] rows of d values, ``w_down``
-    [E, d] rows of h (moe_int4_quantize_weights of the bf16 weights). Returns (y, Permuted)."""
+    [E, d] rows of h (moe_int4_quantize_weights of the bf16 weights). Returns (y, Permuted). For decode and small batches:
+    from about 200 rows an expert on, moe_expert_forward on weights read back with moe_int4_dequantize_weights is faster."""
     k = expert_ids.shape[1]
     p = moe_permute(x, expert_ids, w_ug.q.shape[0], gather=False)
     h = moe_gemm_up_swiglu_int4(x, p.offsets, w_ug, perm=p.perm, k=k)

@@ -6,7 +6,8 @@
 // all in fp32 (gradients are read as they are, parameters from their fp32 copy where there is one). Bound
 // by HBM: 28 bytes a value with bf16 parameters, fp32 copies and moments, 10 with 8-bit moments alone. Measured, bf16
 // parameters and gradients: 398 M values with fp32 copies and moments 2174 us (5.1 TB/s; a copy of 2 GiB runs at 4.9),
-// 302 M with 8-bit moments and random rounding 565 to 585 us (5.2 to 5.4 TB/s), the moments' values as bf16 370 (5.0).
+// 302 M with 8-bit moments and random rounding 565 to 585 us (5.2 to 5.4 TB/s), the moments' values as bf16 370 (5.0). With
+// 32-bit moments and no copy 302 M bf16 parameters take 1291 us (5.1 TB/s, rounded at random 1467, 4.5), fp32 ones 1562 (5.4).
 // Steps that brought it there: a pass's loads before the step of the one before, 2268 to 2215 and 743 to 616 us; whole
 // lines read and written past the caches, 2215 to 2175 and 616 to 575.
 //

@@ -369,7 +369,9 @@ __global__ __launch_bounds__(kThreads, 4) void int4_kernel(Int4Args g) {
   }
 }
 
-constexpr int wide_resident(int mb) { return mb == 2 ? 3 : 2; }  // workgroups a CU
+// Workgroups a CU, as the grid counts them. LDS holds three with 32 rows in groups of 128 and, up to about 290 experts, of
+// 64; in groups of 32, or with more experts, two, and the third starts when one of them is done.
+constexpr int wide_resident(int mb) { return mb == 2 ? 3 : 2; }
 
 // A unit of a wide tile in LDS, brought there by direct loads. Token row t's 16-byte piece c stands at c ^ (t % 16): 16
 // rows' pieces of one c cover all banks. A weight row's quarters stand 256 bytes apart, so the 64 lanes of a step, which
@@ -408,7 +410,7 @@ __device__ __forceinline__ void dma4_buf(__amdgpu_buffer_rsrc_t rsrc, uint32_t o
 // skewed, 2048 -> 2 x 768 45.6 us (narrow tiles 57); units through registers, loaded where they are needed, 49, and 39
 // where this takes 35.7 with 32 rows for each expert. Tried: three or four units in LDS 36.7 us there, and 744 for
 // 618 with 1024 rows (fewer workgroups a CU); a step unpacked between the matrix instructions of the one before 36.4 and
-// 725 (its registers spill).
+// 725 (its registers spill). With 64 rows 1 to 13 registers of the 256 spill as it is.
 template <bool GATED, int MB, int GS>
 __global__ __launch_bounds__(kThreads, wide_resident(MB)) void int4_wide_kernel(Int4Args g) {
   constexpr int BM = 16 * MB, kWaveCols = GATED ? 32 : 64, kCols = kWaves * kWaveCols;

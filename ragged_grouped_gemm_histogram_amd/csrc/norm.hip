@@ -26,7 +26,9 @@
 //   4096 x 8192                   21.3 / 30.7         41.9 / 78.6         50.0 / 90.5, 99.7 / 136.7
 //   2048 x 16384                  21.3 / 31.7         51.4 / 87.2         55.1 / 98.8, 156 / 218
 // The last column's last row is 2.6 to 2.8 TB/s: above 8192 columns a lane's two vectors of all rows and sums leave no
-// registers to read ahead, and some spill. Small calls wait for one chain of load, sum and store, 3 us, and the backward's second launch.
+// registers to read ahead. Backwards with both norms spill there, with a gate per channel 46 registers (bf16) and 65 (fp32;
+// 53 and 90 with a second part of dn), without one 4 and 26; from 4097 columns on 18 and 34 (26 and 44), and none and 4; with
+// an fp32 stream and narrower rows one. Small calls wait for one chain of load, sum and store, 3 us, and the backward's second launch.
 
 #include "common.h"
 #include "norm.h"
@@ -301,7 +303,8 @@ struct BackRow {
 };
 
 constexpr int kBackWaves = 8;  // a workgroup: as many teams as fit, one WIDE team above
-constexpr int kBackLds = 128 * 1024;  // for the weights: three of 10920 columns, two of 16384
+// For the weights, their columns rounded up to 512 a wave (1024 with V = 2): three up to 10240 columns, two up to 16384.
+constexpr int kBackLds = 128 * 1024;
 
 // CHANNEL: the gate is one per channel. ADD: d_n comes in two parts. The column sums stand in the order dw_next,
 // dw_post, dgate, those that the form has. A row's loads go out before the row before it is computed (not with V = 2, nor
